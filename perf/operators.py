@@ -1,0 +1,458 @@
+"""The operators of the 4-bit KV cache, case by case: what each call gets, its plain form and its value in 64 bits.
+
+The cache (one head of a page is page_size / 16 tiles of 16 tokens, 2304 bytes a tile, head dim 128):
+
+  bytes    0..1023  K codes, token-major: token t, byte j holds dims 2j (low nibble) and 2j + 1 (high nibble)
+  bytes 1024..2047  V codes, [half][group r][pair p][i]: dim 16r + i of tokens 8 half + 2p (low) and 8 half + 2p + 1 (high)
+  bytes 2048..2303  scales, 32 words of 8 bytes: word w holds, of K, groups 2(w % 4) and 2(w % 4) + 1 of token w / 4 and then
+                    of token 8 + w / 4; of V, group w / 4 of tokens 2(w % 4), 2(w % 4) + 1 and then of 8 + 2(w % 4), 9 + 2(w % 4)
+
+A code is a 4-bit float (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6); a scale is an unsigned 8-bit
+float (five exponent bits, three mantissa bits, bias 15) over 16 dims of one token and head, and the value is their product.
+Quantising a block: scale = max |x| / 6 rounded to nearest even (at most 10240), code = x / scale rounded to nearest even,
+at most 6; a block with a NaN or an infinity gets the scale 255 (NaN).
+
+Operators: `write` quantises new tokens into the cache and reads them back, `read` reads a range of each sequence back,
+`decode` is attention of one query token a sequence, `prefill` of a ragged batch of the last tokens of each sequence.
+"""
+import math
+
+import torch
+
+own = False
+
+D = 128
+TILE = 2304
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def listed():
+    return [
+        # one decode step's new token of every sequence of a serving batch: latency
+        {"name": "write_step_b32", "op": "write", "B": 32, "T": 4000, "n": 1, "Hq": 32, "Hkv": 8, "page": 16, "type": "bf16", "ragged": True, "fused": True},
+        # a long prompt's keys and values, views of a fused projection
+        {"name": "write_prompt_32k", "op": "write", "B": 1, "T": 32768, "n": 32768, "Hq": 32, "Hkv": 8, "page": 16, "type": "bf16", "ragged": False, "fused": True},
+        # chunks of several prompts at odd places, one of them empty, 32-bit inputs
+        {"name": "write_ragged_f32", "op": "write", "B": 6, "T": 2999, "n": 1100, "Hq": 32, "Hkv": 4, "page": 64, "type": "f32", "ragged": True, "fused": False},
+        # the whole cache of a 128K sequence back in 16 bits, as the index training reads raw keys
+        {"name": "read_llama8b_128k", "op": "read", "B": 1, "T": 131072, "n": 131072, "Hq": 32, "Hkv": 8, "page": 16, "type": "bf16", "ragged": False},
+        # the recent part of a few sequences, from odd positions
+        {"name": "read_ragged_odd", "op": "read", "B": 5, "T": 1777, "n": 301, "Hq": 32, "Hkv": 4, "page": 32, "type": "f16", "ragged": True},
+        # the smallest decode call: latency
+        {"name": "decode_1k", "op": "decode", "B": 1, "T": 1000, "n": 1, "Hq": 32, "Hkv": 8, "page": 16, "type": "f32", "ragged": False, "window": 0, "causal": True},
+        # one layer of an 8B model at 128K, 32-bit query and result as the other decode calls take them
+        {"name": "decode_llama8b_128k", "op": "decode", "B": 1, "T": 131072, "n": 1, "Hq": 32, "Hkv": 8, "page": 16, "type": "f32", "ragged": False, "window": 0, "causal": True},
+        # the serving batch of 32 sequences of 32K
+        {"name": "decode_batch32_32k", "op": "decode", "B": 32, "T": 32768, "n": 1, "Hq": 32, "Hkv": 8, "page": 16, "type": "bf16", "ragged": False, "window": 0, "causal": True},
+        # eight query heads a KV head, lengths of 33K to 128K in one batch
+        {"name": "decode_qwen30b_ragged", "op": "decode", "B": 4, "T": 130999, "n": 1, "Hq": 32, "Hkv": 4, "page": 16, "type": "bf16", "ragged": True, "window": 0, "causal": True},
+        # five drafted tokens a sequence verified at once
+        {"name": "verify_b16_5", "op": "prefill", "B": 16, "T": 8191, "n": 5, "Hq": 32, "Hkv": 8, "page": 16, "type": "bf16", "ragged": True, "window": 0, "causal": True},
+        # a chunk of 2048 prompt tokens behind 30K cached ones
+        {"name": "prefill_chunk_32k", "op": "prefill", "B": 1, "T": 32768, "n": 2048, "Hq": 32, "Hkv": 8, "page": 16, "type": "bf16", "ragged": False, "window": 0, "causal": True},
+        # whole prompts of odd lengths under a sliding window
+        {"name": "prefill_ragged_window", "op": "prefill", "B": 6, "T": 3333, "n": 3333, "Hq": 32, "Hkv": 4, "page": 64, "type": "f16", "ragged": True, "window": 1024, "causal": True},
+    ]
+
+
+def draw(rng):
+    def size(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    op = rng.choice(["write", "read", "decode", "decode", "prefill", "prefill"])
+    Hkv = rng.choice([1, 2, 4, 8])
+    G = rng.choice([1, 2, 4, 8])
+    case = {"op": op, "Hkv": Hkv, "Hq": Hkv * G, "page": rng.choice([16, 32, 64, 128]), "type": rng.choice(["f32", "bf16", "f16"]),
+            "ragged": rng.random() < 0.7}
+    if op in ("write", "read"):
+        case["B"] = size(1, 48)
+        case["T"] = size(1, max(2, 200000 // (case["B"] * Hkv)))
+        case["n"] = 1 if rng.random() < 0.2 else size(1, case["T"])
+        if op == "write":
+            case["fused"] = rng.random() < 0.5
+        return case
+    case["window"] = 0 if rng.random() < 0.7 else size(1, 4096)
+    if op == "decode":
+        case.update(B=size(1, 64), n=1, causal=True)
+        case["T"] = size(1, min(200000, 4000000 // (case["B"] * Hkv)))
+        return case
+    case["causal"] = rng.random() < 0.8
+    if rng.random() < 0.5:  # a few tokens a sequence
+        case.update(B=size(1, 24), n=size(2, 16))
+        case["T"] = size(case["n"], min(60000, 1000000 // (case["B"] * Hkv)))
+    else:
+        case.update(B=size(1, 6), n=size(17, 2500))
+        case["T"] = size(case["n"], max(case["n"] + 1, 60000000 // (case["B"] * Hkv * G * case["n"])))
+    return case
+
+
+# ---- what a case means -------------------------------------------------------------------------------------------------
+
+
+def lengths(case):
+    """Tokens in the cache, and new, read or query tokens, of each sequence."""
+    T, n, B = case["T"], case["n"], case["B"]
+    if not case["ragged"]:
+        return [T] * B, [min(n, T)] * B
+    lens = [max(1, T - int(0.75 * T * ((b * 0.381966) % 1.0))) for b in range(B)]
+    news = [min(lens[b], max(1, n - int(0.6 * n * ((b * 0.618034) % 1.0)))) for b in range(B)]
+    if B >= 6 and n > 1:
+        news[4] = 0
+    return lens, news
+
+
+def starts(case):
+    lens, news = lengths(case)
+    if case["op"] == "read":  # a range that ends where it ends: a few tokens before the last
+        return [max(0, (t - n) - (3 * b) % 7) for b, (t, n) in enumerate(zip(lens, news))]
+    return [t - n for t, n in zip(lens, news)]
+
+
+def pairs(case):
+    """(query token, key) pairs that the mask leaves, over the batch."""
+    lens, news = lengths(case)
+    total, w = 0, case["window"]
+    for t, n in zip(lens, news):
+        if not case["causal"]:
+            total += n * t
+            continue
+        for_all = sum(range(t - n + 1, t + 1))
+        if w > 0:
+            for_all = sum(min(w, x) for x in range(t - n + 1, t + 1))
+        total += for_all
+    return total
+
+
+def keys_read(case):
+    lens, news = lengths(case)
+    if not case["causal"] or case["window"] == 0:
+        return sum(t for t, n in zip(lens, news) if n)
+    return sum(min(t, n - 1 + case["window"]) for t, n in zip(lens, news) if n)
+
+
+def work(case):
+    e = 4 if case["type"] == "f32" else 2
+    n = sum(lengths(case)[1])
+    held = 2 * (D // 2 + D // 16)  # bytes of one token and head, keys and values
+    if case["op"] == "write":  # 16- or 32-bit rows in, codes out and in again, rows out
+        return {"bytes": n * case["Hkv"] * (2 * D * e + held + held + 2 * D * e), "flops": n * case["Hkv"] * 2 * D * 4}
+    if case["op"] == "read":
+        return {"bytes": n * case["Hkv"] * (held + 2 * D * e), "flops": n * case["Hkv"] * 2 * D}
+    return {"bytes": keys_read(case) * case["Hkv"] * held + n * case["Hq"] * (2 * D * e + 4), "flops": pairs(case) * case["Hq"] * 4 * D}
+
+
+# ---- inputs ------------------------------------------------------------------------------------------------------------
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    g = torch.Generator(device=dev).manual_seed(seed)
+    lens, news = lengths(case)
+    B, Hkv, Hq, page = case["B"], case["Hkv"], case["Hq"], case["page"]
+    dt = TYPES[case["type"]]
+    need = [-(-t // page) for t in lens]
+    width = max(need) + 1
+    pages = sum(need) + 3
+    order = torch.randperm(pages, generator=g, device=dev).to(torch.int32).cpu()
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    at = 0
+    for b, k in enumerate(need):
+        table[b, :k] = order[at:at + k]
+        at += k
+    cu = [0]
+    for n in news:
+        cu.append(cu[-1] + n)
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    s = {"case": case, "page": page, "table": table.to(dev), "lens": i32(lens).to(dev), "lens_host": i32(lens), "cu": i32(cu).to(dev), "cu_host": i32(cu),
+         "start": i32(starts(case)).to(dev), "start_host": i32(starts(case)), "n": cu[-1], "n_max": max(news), "T_max": max(lens), "Hq": Hq, "type": dt}
+    # keys with a few large channels, as models have them; values without
+    channel = torch.ones(Hkv, D, device=dev)
+    channel.scatter_(1, torch.randint(0, D, (Hkv, 8), generator=g, device=dev), 6.0)
+    if case["op"] == "write":
+        n = cu[-1]
+        if case["fused"]:  # rows of a fused projection [q | k | v]
+            rows = torch.randn(n, Hq + 2 * Hkv, D, generator=g, device=dev).to(dt)
+            rows[:, Hq:Hq + Hkv] *= channel.to(dt)
+            s["k"], s["v"] = rows[:, Hq:Hq + Hkv], rows[:, Hq + Hkv:]
+        else:
+            s["k"] = (torch.randn(n, Hkv, D, generator=g, device=dev) * channel).to(dt)
+            s["v"] = torch.randn(n, Hkv, D, generator=g, device=dev).to(dt)
+        s["cache"] = torch.randint(0, 256, (pages, Hkv, page // 16, TILE), generator=g, device=dev, dtype=torch.uint8)
+    else:
+        s["cache"] = torch.empty(pages, Hkv, page // 16, TILE, device=dev, dtype=torch.uint8)
+        step = max(1, (1 << 27) // (Hkv * page * D))
+        for p0 in range(0, pages, step):
+            k = min(step, pages - p0)
+            x = torch.randn(2, k * Hkv * (page // 16), 16, D, generator=g, device=dev)
+            x[0].view(k, Hkv, -1, D).mul_(channel[None, :, None])
+            s["cache"][p0:p0 + k] = pack(*quantise(x[0]), *quantise(x[1])).view(k, Hkv, page // 16, TILE)
+        if case["op"] != "read":
+            s["q"] = torch.randn(cu[-1], Hq, D, generator=g, device=dev).to(dt)
+            s["scale"] = D ** -0.5
+            s["out"] = torch.empty(cu[-1], Hq, D, device=dev, dtype=dt)
+            s["lse"] = torch.empty(cu[-1], Hq, device=dev)
+    if case["op"] in ("write", "read"):
+        s["k_out"] = torch.empty(cu[-1], Hkv, D, device=dev, dtype=dt)
+        s["v_out"] = torch.empty(cu[-1], Hkv, D, device=dev, dtype=dt)
+    if own:
+        import sparse_long_context_pq_b200 as P
+        s["P"] = P
+        s["kv"] = P.KV4Cache(s["cache"], s["table"], s["lens"], s["lens_host"], Hq)
+        s["work"] = P.workspace(P.hsa_kv4_workspace_bytes(s["kv"]), dev)
+    return s
+
+
+# ---- the plain forms -----------------------------------------------------------------------------------------------------
+
+
+def quantise(x):
+    """Codes (4 bits) and scales (8 bits) of rows of 128."""
+    x = x.float().unflatten(-1, (8, 16))
+    top = x.abs().amax(-1)
+    y = (top / torch.full_like(top, 6.0)).clamp(max=10240.0)  # a true division: a number would be multiplied by its inverse
+    # nearest of three mantissa bits, ties to even; below 2^-14 multiples of 2^-17
+    step = torch.exp2(torch.floor(torch.log2(y.clamp(min=2.0 ** -14).double())) - 3).clamp(min=2.0 ** -17).float()
+    scale = torch.round(y / step) * step
+    r = torch.where(scale[..., None] > 0, x / scale[..., None].clamp(min=2.0 ** -17), 0.0)
+    a = r.abs()
+    code = ((a > 0.25).to(torch.uint8) + (a >= 0.75).to(torch.uint8) + (a > 1.25).to(torch.uint8) + (a >= 1.75).to(torch.uint8)
+            + (a > 2.5).to(torch.uint8) + (a >= 3.5).to(torch.uint8) + (a > 5.0).to(torch.uint8))
+    code = code + 8 * (r < 0).to(torch.uint8)
+    byte = (scale.half().view(torch.int16) >> 7).to(torch.uint8)
+    bad = ~torch.isfinite(top)
+    return torch.where(bad[..., None], 0, code).flatten(-2), torch.where(bad, 255, byte)
+
+
+def pack(kc, ks, vc, vs):
+    """Tiles [n, 2304] of codes [n, 16, 128] and scales [n, 16, 8]."""
+    n = kc.shape[0]
+    kb = (kc[..., 0::2] | (kc[..., 1::2] << 4)).flatten(1)
+    v = vc.view(n, 2, 4, 2, 8, 16)  # half, pair, member, group, dim
+    vb = (v[:, :, :, 0] | (v[:, :, :, 1] << 4)).transpose(2, 3).flatten(1)
+    k2 = ks.view(n, 2, 8, 4, 2).permute(0, 2, 3, 1, 4)  # token, word, half, group
+    v2 = vs.view(n, 2, 4, 2, 8).permute(0, 4, 2, 1, 3)  # group, pair, half, member
+    return torch.cat([kb, vb, torch.cat([k2, v2], 3).reshape(n, 256)], 1)
+
+
+def values(code, scale):
+    """32-bit values of codes [..., 128] and scales [..., 8]."""
+    m = (code & 7).float()
+    mag = torch.where(m < 4, m * 0.5, torch.where(m < 6, m - 2, 2 * m - 8))
+    sign = 1.0 - 2.0 * (code >> 3).float()
+    s = (scale.to(torch.int16) << 7).view(torch.float16).float()
+    return ((sign * mag).unflatten(-1, (8, 16)) * s[..., None]).flatten(-2)
+
+
+def unpack(tiles):
+    """Keys and values [n, 16, 128] of tiles [n, 2304], in 32 bits."""
+    n = tiles.shape[0]
+    kb = tiles[:, :1024].view(n, 16, 64)
+    kc = torch.stack([kb & 15, kb >> 4], -1).flatten(-2)
+    vb = tiles[:, 1024:2048].view(n, 2, 8, 4, 16).transpose(2, 3)
+    vc = torch.stack([vb & 15, vb >> 4], 3).reshape(n, 16, D)
+    sc = tiles[:, 2048:].view(n, 8, 4, 4, 2)
+    ks = sc[:, :, :, :2].permute(0, 3, 1, 2, 4).reshape(n, 16, 8)
+    vs = sc[:, :, :, 2:].permute(0, 3, 2, 4, 1).reshape(n, 16, 8)
+    return values(kc, ks), values(vc, vs)
+
+
+def places(s):
+    """Sequence and position of each new, read or query token."""
+    n = s["cu"][1:] - s["cu"][:-1]
+    b = torch.repeat_interleave(torch.arange(n.numel(), device=n.device), n, output_size=s["n"])
+    pos = torch.arange(s["n"], device=n.device) - s["cu"][b] + s["start"][b]
+    return b, pos
+
+
+def put(s):
+    b, pos = places(s)
+    cache, page = s["cache"], s["page"]
+    Hkv = cache.shape[1]
+    flat = cache.view(-1)
+    of = s["table"][b, pos // page].long()
+    head = torch.arange(Hkv, device=b.device)
+    tile = ((of[:, None] * Hkv + head) * (page // 16) + (pos % page // 16)[:, None]) * TILE  # byte offset of the tile, [token, head]
+    row = (pos % 16)[:, None]
+    kc, ks = quantise(s["k"])
+    vc, vs = quantise(s["v"])
+    byte = torch.arange(64, device=b.device)
+    flat[(tile + row * 64)[..., None] + byte] = kc[..., 0::2] | (kc[..., 1::2] << 4)
+    grp = torch.arange(8, device=b.device)
+    flat[(tile + 2048 + (row % 8) * 32 + (row // 8) * 2)[..., None] + grp // 2 * 8 + grp % 2] = ks
+    flat[(tile + 2048 + (row % 8 // 2) * 8 + 4 + (row // 8) * 2 + row % 2)[..., None] + grp * 32] = vs
+    d = torch.arange(D, device=b.device)
+    vat = (tile + 1024 + (row // 8) * 512 + (row % 8 // 2) * 16)[..., None] + d // 16 * 64 + d % 16
+    even, odd = (pos % 2 == 0).nonzero()[:, 0], (pos % 2 == 1).nonzero()[:, 0]
+    flat[vat[even]] = (flat[vat[even]] & 240) | vc[even]
+    flat[vat[odd]] = (flat[vat[odd]] & 15) | (vc[odd] << 4)
+
+
+def fetch(s):
+    """Keys and values of the whole sequences, [B, positions, Hkv, 128] in 32 bits."""
+    cache, page = s["cache"], s["page"]
+    got = cache[s["table"][:, :-(-s["T_max"] // page)].clamp(min=0).long()]  # [B, pages, Hkv, tiles, 2304]
+    B, np_, Hkv, nt, _ = got.shape
+    k, v = unpack(got.view(-1, TILE))
+    lay = lambda x: x.view(B, np_, Hkv, nt * 16, D).transpose(2, 3).reshape(B, np_ * nt * 16, Hkv, D)  # noqa: E731
+    return lay(k), lay(v)
+
+
+def fetch_rows(s):
+    b, pos = places(s)
+    cache, page = s["cache"], s["page"]
+    first = s["start"] // 16
+    tiles = int(max((st + n + 15) // 16 - st // 16 for st, n in zip(s["start_host"].tolist(), (s["cu_host"][1:] - s["cu_host"][:-1]).tolist())))
+    at = first[:, None] + torch.arange(tiles, device=b.device)
+    of = s["table"].gather(1, (at * 16 // page).clamp(max=s["table"].shape[1] - 1).long()).clamp(min=0).long()
+    got = cache[of[:, :, None], torch.arange(cache.shape[1], device=b.device), (at % (page // 16))[:, :, None]]
+    B, nt, Hkv, _ = got.shape
+    k, v = unpack(got.reshape(-1, TILE))
+    row = pos - first[b] * 16
+    lay = lambda x: x.view(B, nt, Hkv, 16, D)[b, row // 16, :, row % 16]  # noqa: E731
+    return lay(k), lay(v)
+
+
+def attend(s):
+    case = s["case"]
+    k, v = fetch(s)
+    B, T, Hkv, _ = k.shape
+    Hq = s["Hq"]
+    G, nq = Hq // Hkv, s["n_max"]
+    b, pos = places(s)
+    i = torch.arange(s["n"], device=b.device) - s["cu"][b]
+    q = torch.zeros(B, nq, Hq, D, device=b.device)
+    q[b, i] = s["q"].float()
+    at = torch.full((B, nq), -1, device=b.device, dtype=torch.long)
+    at[b, i] = pos
+    j = torch.arange(T, device=b.device)
+    seen = (j < s["lens"][:, None])[:, None].expand(B, nq, T)
+    if case["causal"]:
+        seen = seen & (j <= at[..., None])
+        if case["window"] > 0:
+            seen = seen & (j > at[..., None] - case["window"])
+    qh = q.view(B, nq, Hkv, G, D).permute(0, 2, 3, 1, 4).reshape(B, Hkv, G * nq, D)
+    x = torch.matmul(qh, k.permute(0, 2, 3, 1)).mul_(s["scale"]).view(B, Hkv, G, nq, T)
+    x.masked_fill_(~seen[:, None, None], -math.inf)
+    top = x.amax(-1, keepdim=True)
+    top = torch.where(torch.isfinite(top), top, torch.zeros_like(top))
+    p = x.sub_(top).exp_()
+    total = p.sum(-1, keepdim=True)
+    vals = v.permute(0, 2, 1, 3)
+    vals = vals.masked_fill(~(j < s["lens"][:, None])[:, None, :, None], 0.0)
+    o = torch.matmul(p.view(B, Hkv, G * nq, T), vals).view(B, Hkv, G, nq, D)
+    o = torch.where(total > 0, o / total, torch.zeros_like(o))
+    lse = (total.log() + top)[..., 0]
+    out = o.permute(0, 3, 1, 2, 4).reshape(B, nq, Hq, D)[b, i].to(s["type"])
+    return out, lse.permute(0, 3, 1, 2).reshape(B, nq, Hq)[b, i]
+
+
+def run(s):
+    op = s["case"]["op"]
+    if own:
+        P, kv = s["P"], s["kv"]
+        if op == "write":
+            P.hsa_kv4_write(kv, s["k"], s["v"], s["cu"], s["cu_host"], workspace_buf=s["work"])
+        if op in ("write", "read"):
+            return P.hsa_kv4_read(kv, s["start"], s["start_host"], s["cu"], s["cu_host"], k_out=s["k_out"], v_out=s["v_out"], workspace_buf=s["work"])
+        if op == "decode":
+            return P.dense_decode_kv4(kv, s["q"], s["out"], scale=s["scale"], window=s["case"]["window"], lse=s["lse"], workspace_buf=s["work"]), s["lse"]
+        return P.dense_prefill_kv4(kv, s["q"], s["cu"], s["cu_host"], s["out"], scale=s["scale"], causal=s["case"]["causal"], window=s["case"]["window"],
+                                   lse=s["lse"], workspace_buf=s["work"]), s["lse"]
+    if op == "write":
+        put(s)
+    if op in ("write", "read"):
+        k, v = fetch_rows(s)
+        return k.to(s["type"]), v.to(s["type"])
+    return attend(s)
+
+
+# ---- the definition in 64 bits -------------------------------------------------------------------------------------------
+
+GRID = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+SCALES = [math.ldexp(b % 8, -17) if b < 8 else math.ldexp(8 + b % 8, b // 8 - 18) for b in range(248)] + [math.inf] + 7 * [math.nan]
+
+
+def _rounded(x):
+    """The values that rows of 128 are held as, from the definition: the nearest scale of all 227, then the nearest of the
+    eight magnitudes, a tie going to the even code."""
+    dev = x.device
+    scales = torch.tensor(SCALES[:227], device=dev, dtype=torch.float64)
+
+    def nearest(table, y):
+        hi = torch.searchsorted(table, y).clamp(1, table.numel() - 1)
+        lo = hi - 1
+        below, above = y - table[lo], table[hi] - y
+        return torch.where((below < above) | ((below == above) & (lo % 2 == 0)), lo, hi)
+
+    x = x.double().reshape(-1, 16)
+    got = []
+    for part in x.split(1 << 21):
+        top = part.abs().max(-1, keepdim=True).values
+        s = scales[nearest(6 * scales, top.contiguous())]
+        grid = torch.tensor(GRID, device=dev, dtype=torch.float64)
+        y = torch.where(s > 0, part.abs() / s, torch.zeros_like(part)).clamp(max=6.0)
+        got.append(torch.sign(part) * grid[nearest(grid, y.contiguous())] * s)
+    return torch.cat(got)
+
+
+def _held(s, b, kv, first, last):
+    """Positions [first, last) of sequence b in 64 bits, [positions, Hkv, 128]; kv: 0 keys, 1 values."""
+    cache, page, dev = s["cache"], s["page"], s["cache"].device
+    t = torch.arange(first, last, device=dev)
+    base = cache[s["table"][b][t // page].long(), :, t % page // 16].long()  # [positions, Hkv, 2304]
+    d, r = torch.arange(D, device=dev), (t % 16)[:, None]
+    if kv == 0:
+        at, high = r * 64 + d // 2, (d % 2).expand(len(t), D)
+        sat = 2048 + ((r % 8) * 4 + d // 32) * 8 + r // 8 * 2 + d // 16 % 2
+    else:
+        at, high = 1024 + r // 8 * 512 + d // 16 * 64 + r % 8 // 2 * 16 + d % 16, (r % 2).expand(len(t), D)
+        sat = 2048 + (d // 16 * 4 + r % 8 // 2) * 8 + 4 + r // 8 * 2 + r % 2
+    take = lambda i: base.gather(2, i[:, None].expand(-1, base.shape[1], -1))  # noqa: E731
+    code = take(at) >> (4 * high)[:, None] & 15
+    scales = torch.tensor(SCALES, device=dev, dtype=torch.float64)
+    grid = torch.tensor(GRID + [-g for g in GRID], device=dev, dtype=torch.float64)
+    return grid[code] * scales[take(sat)]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    lens, news = lengths(case)
+    at = starts(case)
+    if case["op"] == "write":
+        lay = lambda x: _rounded(x).view(x.shape)  # noqa: E731
+        return lay(s["k"]), lay(s["v"])
+    if case["op"] == "read":
+        parts = [[_held(s, b, kv, at[b] + lo, at[b] + min(lo + 8192, n)) for b, n in enumerate(news) for lo in range(0, n, 8192)] for kv in (0, 1)]
+        return torch.cat(parts[0]), torch.cat(parts[1])
+    Hkv, G, w = case["Hkv"], case["Hq"] // case["Hkv"], case["window"]
+    outs, lses = [], []
+    for b, n in enumerate(news):
+        if n == 0:
+            continue
+        rows = s["q"][s["cu_host"][b]:s["cu_host"][b + 1]].double().view(n, Hkv, G, D)
+        me = torch.arange(at[b], at[b] + n, device=rows.device)
+        part = 512
+        best = torch.full((n, Hkv, G), -math.inf, device=rows.device, dtype=torch.float64)
+        num, den = torch.zeros(n, Hkv, G, D, device=rows.device, dtype=torch.float64), torch.zeros(n, Hkv, G, device=rows.device, dtype=torch.float64)
+        for lo in range(0, lens[b], 16384):  # keys in pieces, joined by their largest logit
+            hi = min(lens[b], lo + 16384)
+            k, v = _held(s, b, 0, lo, hi), _held(s, b, 1, lo, hi)
+            key = torch.arange(lo, hi, device=rows.device)
+            for r0 in range(0, n, part):
+                r = slice(r0, min(n, r0 + part))
+                x = torch.einsum("qhgd,khd->qhgk", rows[r], k) * s["scale"]
+                if case["causal"]:
+                    hide = key[None] > me[r, None]
+                    if w > 0:
+                        hide |= key[None] + w <= me[r, None]
+                    x = torch.where(hide[:, None, None], -math.inf, x)
+                new = torch.maximum(best[r], x.max(-1).values)
+                ref = torch.where(new == -math.inf, 0.0, new)
+                old = torch.exp(best[r] - ref)
+                p = torch.exp(x - ref[..., None])
+                den[r] = den[r] * old + p.sum(-1)
+                num[r] = num[r] * old[..., None] + torch.einsum("qhgk,khd->qhgd", p, v)
+                best[r] = new
+        outs.append(torch.where(den[..., None] > 0, num / den[..., None].clamp(min=1e-300), torch.zeros_like(num)).reshape(n, Hkv * G, D))
+        lses.append((torch.log(den) + best).reshape(n, Hkv * G))
+    return torch.cat(outs), torch.cat(lses)
