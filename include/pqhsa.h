@@ -322,6 +322,112 @@ hsa_status hsa_train_index(const hsa_kv_cache* kv, hsa_index* index, int32_t n_t
                            int32_t* assign_out, void* workspace, size_t workspace_bytes,
                            cudaStream_t stream);
 
+/* ---- 4-bit KV cache ------------------------------------------------------- */
+
+/*
+ * A paged KV cache held in 4 bits: 144 bytes a token and KV head for keys and values
+ * together, where the bf16 cache takes 512. The PQ-HSA article has no counterpart; these
+ * calls stand beside dense_decode for caches that would not fit in 16 bits, and
+ * hsa_kv4_read gives the raw keys that hsa_train_index and hsa_append_encode work on.
+ *
+ * Number format. A code is a 4-bit float: sign, two exponent bits, one mantissa bit
+ * (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6). Blocks of 16 consecutive dims of one token and
+ * head share a scale, an unsigned 8-bit float of five exponent bits and three mantissa bits
+ * (bias 15: the byte shifted left by 7 is the same number in fp16). A value is code times
+ * scale, at most six significant bits in [2^-18, 61440]: exact in fp16, bf16 and fp32.
+ * Quantising a block x: scale = max|x| / 6 rounded to the nearest scale (at most 10240),
+ * code = x / scale rounded to the nearest code (at most 6 in magnitude); ties to the even
+ * mantissa. Blocks that hold a NaN or an infinity get the scale byte 255 and read back as
+ * NaN; larger finite values than 61440 saturate there.
+ *
+ * Memory. One head of a page is page_size / 16 tiles of 16 tokens, HSA_KV4_TILE_BYTES each:
+ *   [0, 1024)     key codes: 64 bytes a token, byte j = dims 2j (low nibble), 2j + 1 (high);
+ *   [1024, 2048)  value codes [2][8][4][16]: byte (half, r, p, i) = dim 16r + i of tokens
+ *                 8 half + 2p (low nibble) and 8 half + 2p + 1 (high);
+ *   [2048, 2304)  scales, 32 words of 8 bytes: word 4r + p = keys: blocks 2p, 2p + 1 of token
+ *                 r, then of token 8 + r; values: block r of tokens 2p, 2p + 1, then of
+ *                 tokens 8 + 2p, 9 + 2p.
+ * A lane of a warp finds all that it multiplies (mma fragments of keys and of values) in two
+ * 16-byte pieces of keys, two of values and one word of scales, all at 16 (8) x lane.
+ *
+ * Tokens, block table and lengths are those of hsa_kv_cache: token t of sequence b lives in
+ * page block_table[b * max_pages + t / page_size]. The kernels go by the device arrays; the
+ * *_host copies serve validation and planning, so a captured call may be replayed with other
+ * lengths as long as they fit the block table and, where a call takes rows, the row counts do
+ * not grow. Every call takes the same workspace (hsa_kv4_workspace_bytes; error word first,
+ * see hsa_read_error); calls that overlap on the GPU need one each.
+ */
+#define HSA_KV4_TILE_TOKENS 16
+#define HSA_KV4_TILE_BYTES 2304
+
+typedef enum { HSA_F32 = 0, HSA_BF16 = 1, HSA_F16 = 2 } hsa_dtype;
+
+typedef struct {
+  void* cache;                     /* u8 [num_pages][Hkv][page_size / 16][HSA_KV4_TILE_BYTES], 256-B aligned */
+  const int32_t* block_table;      /* [B][max_pages] page ids, each in [0, num_pages) */
+  const int32_t* seq_lens;         /* [B] tokens in each sequence */
+  const int32_t* seq_lens_host;    /* [B] host copy of seq_lens */
+  int32_t B, Hq, Hkv, D, page_size, max_pages, num_pages;   /* D = 128; page_size 16, 32, 64 or 128;
+                                      Hq a multiple of Hkv, at most 128 query heads a KV head */
+} hsa_kv4_cache;
+
+/* Rows of 128 values by token and KV head (elements between tokens and between heads; rows
+   are contiguous). Pointer and strides: multiples of 16 bytes. */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} hsa_kv4_rows;
+
+/* Workspace bytes of any kv4 call on this cache (0 on invalid arguments). */
+size_t hsa_kv4_workspace_bytes(const hsa_kv4_cache* kv);
+
+/*
+ * Quantises new tokens into the cache. Sequence b gets rows [cu_new[b], cu_new[b + 1]) of
+ * k and v (of dtype, read only) as its last tokens: positions [seq_lens[b] - n_b, seq_lens[b]),
+ * so seq_lens counts them already. Other tokens of the pages keep their bytes. cu_new: device
+ * int32 [B + 1], starting at 0 and not falling, with its host copy. A page written here must
+ * belong to one sequence of the batch. A token whose page is out of range is skipped and flagged.
+ */
+hsa_status hsa_kv4_write(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hsa_kv4_rows* v, int32_t dtype,
+                         const int32_t* cu_new, const int32_t* cu_new_host, void* workspace,
+                         size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Reads positions [start[b], start[b] + n_b) of every sequence back into rows
+ * [cu[b], cu[b + 1]) of k and v (of dtype; written, other rows stay as they are), n_b =
+ * cu[b + 1] - cu[b]. Every value is exact in all three types. start: device int32 [B] with
+ * its host copy. Rows whose page is out of range become zero and are flagged.
+ */
+hsa_status hsa_kv4_read(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hsa_kv4_rows* v, int32_t dtype,
+                        const int32_t* start, const int32_t* start_host, const int32_t* cu, const int32_t* cu_host,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Attention of one query token a sequence over its cached tokens (dense_decode of a 4-bit
+ * cache): out_g = softmax(scale * q_g K^T) V over the last `window` tokens of the sequence, or
+ * over all with window = 0. q, out: [B][Hq][D] of dtype, contiguous, 16-B aligned. lse: NULL or
+ * fp32 [B][Hq], log of the sum of e^(logit). A sequence without tokens gets zeros and -inf.
+ */
+hsa_status dense_decode_kv4(const hsa_kv4_cache* kv, const void* q, void* out, float* lse, int32_t dtype, float scale,
+                            int32_t window, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Attention of a ragged batch of query tokens: rows [cu_q[b], cu_q[b + 1]) of q are the last
+ * n_b tokens of sequence b (their keys and values already in the cache), row i at position
+ * p = seq_lens[b] - n_b + i. With causal = 1 it attends positions <= p, with window > 0 of those
+ * the last `window`; with causal = 0 (window must be 0) all of the sequence. A row whose mask
+ * leaves nothing (p < 0) gets zeros and -inf. q, out: [rows][Hq][D] of dtype, rows of q
+ * q_stride elements apart (a multiple of 16 bytes), out contiguous; both 16-B aligned. lse:
+ * NULL or fp32 [rows][Hq]. cu_q: device int32 [B + 1] as cu_new, with its host copy.
+ */
+hsa_status dense_prefill_kv4(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void* out, float* lse,
+                             int32_t dtype, const int32_t* cu_q, const int32_t* cu_q_host, float scale,
+                             int32_t causal, int32_t window, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/* sizeof of the kv4 structs, for bindings to check. */
+void hsa_kv4_abi_sizes(int64_t* cache, int64_t* rows);
+
 /* ---- diagnostics --------------------------------------------------------- */
 
 /* Human-readable name of a status. */

@@ -24,10 +24,13 @@ __all__ = [
     "dense_decode_workspace_bytes", "hsa_index_workspace_bytes", "hsa_read_error", "hsa_strerror",
     "selected_counts", "DecodeStep", "HSA_DEVERR_PAGE", "HSA_DEVERR_CLUSTER", "HSA_DEVERR_TIMEOUT",
     "HSA_DEVERR_SELECT",
+    "KV4Cache", "KV4_TILE_BYTES", "hsa_kv4_workspace_bytes", "hsa_kv4_write", "hsa_kv4_read", "dense_decode_kv4",
+    "dense_prefill_kv4",
 ]
 
 HSA_DEVERR_PAGE, HSA_DEVERR_CLUSTER, HSA_DEVERR_TIMEOUT, HSA_DEVERR_SELECT = 1, 2, 4, 8
 M_SUB, DSUB, NCODE, HEAD_DIM = 16, 8, 256, 128
+KV4_TILE_TOKENS, KV4_TILE_BYTES = 16, 2304
 
 
 class _KV(ctypes.Structure):
@@ -48,6 +51,18 @@ class _Index(ctypes.Structure):
                 ("C", ctypes.c_int32), ("M", ctypes.c_int32), ("dsub", ctypes.c_int32),
                 ("ncode", ctypes.c_int32), ("cap", ctypes.c_int32), ("n_sink", ctypes.c_int32),
                 ("list_slots", ctypes.c_int32)]
+
+
+class _KV4(ctypes.Structure):
+    _fields_ = [("cache", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                ("seq_lens_host", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+                ("D", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("num_pages", ctypes.c_int32)]
+
+
+class _KV4Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 def index_list_slots(cap: int, C: int) -> int:
@@ -73,7 +88,8 @@ EXPORTS = ("hsa_decode", "hsa_decode_host", "hsa_decode_step_create", "hsa_decod
            "hsa_decode_step_destroy", "dense_decode", "hsa_build_from_codes", "hsa_append_encode",
            "hsa_index_list_slots", "hsa_decode_workspace_bytes", "hsa_decode_host_workspace_bytes",
            "dense_decode_workspace_bytes", "hsa_index_workspace_bytes",
-           "hsa_read_error", "hsa_strerror", "hsa_abi_sizes")
+           "hsa_read_error", "hsa_strerror", "hsa_abi_sizes", "hsa_kv4_workspace_bytes", "hsa_kv4_write",
+           "hsa_kv4_read", "dense_decode_kv4", "dense_prefill_kv4", "hsa_kv4_abi_sizes")
 
 _lib = None
 
@@ -114,6 +130,17 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.hsa_read_error.argtypes = [vp, P(i32), vp]
     lib.hsa_strerror.argtypes = [ctypes.c_int]
     lib.hsa_abi_sizes.argtypes = [P(ctypes.c_int64)] * 4
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.hsa_kv4_workspace_bytes.argtypes = [P(_KV4)]
+    lib.hsa_kv4_workspace_bytes.restype = sz
+    lib.hsa_kv4_write.argtypes = [P(_KV4), P(_KV4Rows), P(_KV4Rows), i32, vp, vp, vp, sz, vp]
+    lib.hsa_kv4_read.argtypes = [P(_KV4), P(_KV4Rows), P(_KV4Rows), i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.dense_decode_kv4.argtypes = [P(_KV4), vp, vp, vp, i32, f32, i32, vp, sz, vp]
+    lib.dense_prefill_kv4.argtypes = [P(_KV4), vp, i64, vp, vp, i32, vp, vp, f32, i32, i32, vp, sz, vp]
+    lib.hsa_kv4_abi_sizes.argtypes = [P(ctypes.c_int64)] * 2
+    lib.hsa_kv4_abi_sizes.restype = None
+    for f in ("hsa_kv4_write", "hsa_kv4_read", "dense_decode_kv4", "dense_prefill_kv4"):
+        getattr(lib, f).restype = ctypes.c_int
     for f in ("hsa_decode", "hsa_decode_host", "hsa_decode_step_create", "hsa_decode_step_run", "dense_decode",
               "hsa_build_from_codes", "hsa_append_encode", "hsa_read_error", "hsa_train_index"):
         getattr(lib, f).restype = ctypes.c_int
@@ -127,6 +154,9 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     mine = [ctypes.sizeof(t) for t in (_KV, _Index, _Params, _Debug)]
     if [s.value for s in sizes] != mine:
         raise RuntimeError(f"ABI struct size mismatch: library {[s.value for s in sizes]} vs binding {mine}")
+    lib.hsa_kv4_abi_sizes(ctypes.byref(sizes[0]), ctypes.byref(sizes[1]))
+    if [s.value for s in sizes[:2]] != [ctypes.sizeof(_KV4), ctypes.sizeof(_KV4Rows)]:
+        raise RuntimeError(f"ABI struct size mismatch of the kv4 structs: library {[s.value for s in sizes[:2]]}")
     if path == _build.LIB_PATH or "PQHSA_LIB" in os.environ:
         _lib = lib
     return lib
@@ -541,4 +571,222 @@ def dense_decode_static(kv: PagedKV, q: torch.Tensor, out: Optional[torch.Tensor
     _on_gpu(q, out)
     _check("dense_decode_static", fn(ctypes.byref(kvs), q.data_ptr(), out.data_ptr(), ctypes.c_float(scale),
                                      _stream(stream)))
+    return out
+
+
+# ---- 4-bit KV cache ------------------------------------------------------------------------
+
+_KV4_TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+@dataclass(frozen=True, eq=False)
+class KV4Cache:
+    """Paged KV cache held in 4 bits (number format and tile layout: include/pqhsa.h), with the block
+    table and lengths: 144 bytes a token and KV head. The views are checked and marshalled once,
+    here, as DecodeStep does it; the tensors' contents (lengths too) may change between calls.
+    KV4Cache.empty() allocates the pages."""
+
+    cache: torch.Tensor            # uint8 [num_pages, Hkv, page_size / 16, KV4_TILE_BYTES] (device)
+    block_table: torch.Tensor      # int32 [B, max_pages] (device)
+    seq_lens: torch.Tensor         # int32 [B] (device)
+    seq_lens_host: torch.Tensor    # int32 [B] (cpu)
+    Hq: int
+
+    def __post_init__(self):
+        c, bt = self.cache, self.block_table
+        _need(c.dtype == torch.uint8 and c.dim() == 4 and c.is_contiguous() and c.shape[3] == KV4_TILE_BYTES,
+              f"cache: expected a contiguous uint8 tensor [pages, Hkv, page_size / 16, {KV4_TILE_BYTES}]")
+        _need(bt.dtype == torch.int32 and bt.dim() == 2 and bt.is_contiguous(),
+              "block_table: expected a contiguous int32 tensor [B, max_pages]")
+        B = bt.shape[0]
+        for t, name in ((self.seq_lens, "seq_lens"), (self.seq_lens_host, "seq_lens_host")):
+            _need(t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == (B,),
+                  f"{name}: expected a contiguous int32 tensor [{B}]")
+        _need(self.seq_lens_host.device.type == "cpu", "seq_lens_host: expected a host tensor")
+        _on_gpu(c, bt, self.seq_lens)
+        _need(bt.device == c.device and self.seq_lens.device == c.device, "the cache's tensors are on different devices")
+        s = _KV4(_ptr(c), _ptr(bt), _ptr(self.seq_lens), _ptr(self.seq_lens_host), B, self.Hq, c.shape[1], HEAD_DIM,
+                 c.shape[2] * KV4_TILE_TOKENS, bt.shape[1], c.shape[0])
+        object.__setattr__(self, "_struct", s)
+        object.__setattr__(self, "_ref", ctypes.byref(s))
+        object.__setattr__(self, "_index", c.device.index)
+
+    @staticmethod
+    def empty(num_pages: int, Hkv: int, page_size: int, device) -> torch.Tensor:
+        """Pages for the `cache` field; their contents need no initialisation."""
+        _need(page_size % KV4_TILE_TOKENS == 0, f"page_size: a multiple of {KV4_TILE_TOKENS}")
+        return torch.empty(num_pages, Hkv, page_size // KV4_TILE_TOKENS, KV4_TILE_BYTES, dtype=torch.uint8,
+                           device=device)
+
+    @property
+    def B(self) -> int:
+        return self.block_table.shape[0]
+
+    @property
+    def Hkv(self) -> int:
+        return self.cache.shape[1]
+
+    @property
+    def page_size(self) -> int:
+        return self.cache.shape[2] * KV4_TILE_TOKENS
+
+    def struct(self) -> _KV4:
+        return self._struct
+
+
+def hsa_kv4_workspace_bytes(kv: KV4Cache) -> int:
+    """Workspace of any kv4 call on this cache."""
+    n = load_library().hsa_kv4_workspace_bytes(kv._ref)
+    if n == 0:
+        raise HSAError("hsa_kv4_workspace_bytes", 1)
+    return int(n)
+
+
+def _kv4_on(kv: KV4Cache, *ts) -> None:
+    for t in ts:
+        if t is not None and t.device != kv.cache.device:
+            raise ValueError(f"expected a tensor on {kv.cache.device}, got one on {t.device}")
+
+
+def _kv4_new(kv: KV4Cache, stream, make):
+    """make() with its allocation (and whatever fills it) on the device and stream of the call."""
+    if stream is None:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=kv.cache.device)
+    with torch.cuda.stream(stream):
+        return make()
+
+
+def _kv4_workspace(kv: KV4Cache, workspace_buf, stream) -> torch.Tensor:
+    if workspace_buf is None:
+        n = hsa_kv4_workspace_bytes(kv)
+        return _kv4_new(kv, stream, lambda: workspace(n, kv.cache.device))
+    _kv4_on(kv, workspace_buf)
+    return workspace_buf
+
+
+def _kv4_call(kv: KV4Cache, name: str, args, workspace_buf, stream) -> None:
+    """One library call on the cache's device (the current one or not) and the given or current stream."""
+    if torch.cuda.current_device() != kv._index:
+        with torch.cuda.device(kv._index):
+            return _kv4_call(kv, name, args, workspace_buf, stream)
+    ws = _kv4_workspace(kv, workspace_buf, stream)
+    st = getattr(load_library(), name)(kv._ref, *args, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    if st != 0:
+        raise HSAError(name, st)
+
+
+def _kv4_rows(kv: KV4Cache, t: torch.Tensor, name: str, n: int) -> _KV4Rows:
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != kv.Hkv or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+        raise ValueError(f"{name}: expected [{n}, {kv.Hkv}, {HEAD_DIM}] with contiguous rows")
+    return _KV4Rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _kv4_cu(kv: KV4Cache, cu: torch.Tensor, cu_host: torch.Tensor, name: str) -> int:
+    """Checks the row offsets of the sequences; returns the rows of the call."""
+    want = (kv.B + 1,)
+    if (cu.dtype != torch.int32 or cu_host.dtype != torch.int32 or tuple(cu.shape) != want
+            or tuple(cu_host.shape) != want or not cu.is_contiguous() or not cu_host.is_contiguous()
+            or cu_host.device.type != "cpu"):
+        raise ValueError(f"{name}: expected contiguous int32 tensors [{kv.B + 1}] on the device and on the host")
+    _kv4_on(kv, cu)
+    return int(cu_host[-1])
+
+
+def _kv4_type(*ts: torch.Tensor) -> int:
+    code = _KV4_TYPES.get(ts[0].dtype)
+    if code is None or any(t.dtype != ts[0].dtype for t in ts):
+        raise ValueError("expected tensors of one type: float32, bfloat16 or float16")
+    return code
+
+
+def hsa_kv4_write(kv: KV4Cache, k: torch.Tensor, v: torch.Tensor, cu_new: torch.Tensor, cu_new_host: torch.Tensor, *,
+                  workspace_buf: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise new tokens into the cache (see hsa_kv4_write in include/pqhsa.h): sequence b's last tokens are
+    rows [cu_new[b], cu_new[b + 1]) of k and v [rows, Hkv, 128], of any token and head strides (views of a
+    fused projection need no copy). Set seq_lens and seq_lens_host to the lengths with them first."""
+    n = _kv4_cu(kv, cu_new, cu_new_host, "cu_new")
+    _kv4_on(kv, k, v)
+    code = _kv4_type(k, v)
+    if n == 0:
+        return
+    kr, vr = _kv4_rows(kv, k, "k", n), _kv4_rows(kv, v, "v", n)
+    _kv4_call(kv, "hsa_kv4_write", (ctypes.byref(kr), ctypes.byref(vr), code, cu_new.data_ptr(),
+                                    cu_new_host.data_ptr()), workspace_buf, stream)
+
+
+def hsa_kv4_read(kv: KV4Cache, start: torch.Tensor, start_host: torch.Tensor, cu: torch.Tensor,
+                 cu_host: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                 workspace_buf: Optional[torch.Tensor] = None, stream=None):
+    """Read positions [start[b], start[b] + n_b) of every sequence back (see hsa_kv4_read in include/pqhsa.h) as
+    rows [cu[b], cu[b + 1]) of two tensors [rows, Hkv, 128], new ones of `dtype` or the given ones."""
+    n = _kv4_cu(kv, cu, cu_host, "cu")
+    if (start.dtype != torch.int32 or start_host.dtype != torch.int32 or tuple(start.shape) != (kv.B,)
+            or tuple(start_host.shape) != (kv.B,) or not start.is_contiguous() or not start_host.is_contiguous()
+            or start_host.device.type != "cpu"):
+        raise ValueError(f"start: expected contiguous int32 tensors [{kv.B}] on the device and on the host")
+    new = lambda: torch.empty(n, kv.Hkv, HEAD_DIM, dtype=dtype, device=kv.cache.device)  # noqa: E731
+    if k_out is None:
+        k_out = _kv4_new(kv, stream, new)
+    if v_out is None:
+        v_out = _kv4_new(kv, stream, new)
+    _kv4_on(kv, start, k_out, v_out)
+    code = _kv4_type(k_out, v_out)
+    if n == 0:
+        return k_out, v_out
+    kr, vr = _kv4_rows(kv, k_out, "k_out", n), _kv4_rows(kv, v_out, "v_out", n)
+    _kv4_call(kv, "hsa_kv4_read", (ctypes.byref(kr), ctypes.byref(vr), code, start.data_ptr(), start_host.data_ptr(),
+                                   cu.data_ptr(), cu_host.data_ptr()), workspace_buf, stream)
+    return k_out, v_out
+
+
+def _kv4_out(kv: KV4Cache, q: torch.Tensor, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], stream):
+    shape = q.shape
+    if out is None:
+        out = _kv4_new(kv, stream, lambda: torch.empty(shape, dtype=q.dtype, device=q.device))
+    elif out.shape != shape or not out.is_contiguous():
+        raise ValueError(f"out: expected a contiguous tensor {list(shape)}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != shape[:2] or not lse.is_contiguous()):
+        raise ValueError(f"lse: expected a contiguous float32 tensor {list(shape[:2])}")
+    _kv4_on(kv, q, out, lse)
+    return out
+
+
+def dense_decode_kv4(kv: KV4Cache, q: torch.Tensor, out: Optional[torch.Tensor] = None, *, scale: float,
+                     window: int = 0, lse: Optional[torch.Tensor] = None,
+                     workspace_buf: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of one query token a sequence over a 4-bit cache (see dense_decode_kv4 in include/pqhsa.h).
+    q, out: [B, Hq, 128] in float32, bfloat16 or float16; lse: float32 [B, Hq], filled if given."""
+    if tuple(q.shape) != (kv.B, kv.Hq, HEAD_DIM) or not q.is_contiguous():
+        raise ValueError(f"q: expected a contiguous tensor [{kv.B}, {kv.Hq}, {HEAD_DIM}]")
+    out = _kv4_out(kv, q, out, lse, stream)
+    _kv4_call(kv, "dense_decode_kv4", (q.data_ptr(), out.data_ptr(), _ptr(lse), _kv4_type(q, out), scale, window),
+              workspace_buf, stream)
+    return out
+
+
+def dense_prefill_kv4(kv: KV4Cache, q: torch.Tensor, cu_q: torch.Tensor, cu_q_host: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, *, scale: float, causal: bool = True, window: int = 0,
+                      lse: Optional[torch.Tensor] = None, workspace_buf: Optional[torch.Tensor] = None,
+                      stream=None) -> torch.Tensor:
+    """Attention of the last tokens of every sequence over a 4-bit cache that holds them already (see
+    dense_prefill_kv4 in include/pqhsa.h): chunks of prompts, drafted tokens to verify. q: [rows, Hq, 128] of any
+    token stride, rows [cu_q[b], cu_q[b + 1]) of sequence b; out: the same shape, contiguous."""
+    n = _kv4_cu(kv, cu_q, cu_q_host, "cu_q")
+    if tuple(q.shape) != (n, kv.Hq, HEAD_DIM) or (n and (q.stride(2) != 1 or q.stride(1) != HEAD_DIM)):
+        raise ValueError(f"q: expected [{n}, {kv.Hq}, {HEAD_DIM}] with contiguous heads")
+    out = _kv4_out(kv, q, out, lse, stream)
+    code = _kv4_type(q, out)
+    if n == 0:
+        return out
+    _kv4_call(kv, "dense_prefill_kv4", (q.data_ptr(), q.stride(0), out.data_ptr(), _ptr(lse), code, cu_q.data_ptr(),
+                                        cu_q_host.data_ptr(), scale, 1 if causal else 0, window),
+              workspace_buf, stream)
     return out

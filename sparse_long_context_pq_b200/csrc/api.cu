@@ -82,6 +82,13 @@ bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
 namespace pqhsa {
 
+int device_sms() {
+  const DeviceInfo* d = device_info();
+  return d ? d->sms : 0;
+}
+
+bool pdl_enabled() { return use_pdl(); }
+
 // Tensor map over a paged cache viewed as rows of D bf16: [num_pages*Hkv*page_size][128],
 // box = 64 columns x box_rows rows, 128-byte swizzle.
 bool make_kv_tmap(CUtensorMap* map, const void* base, const hsa_kv_cache* kv, int box_rows) {

@@ -1,0 +1,114 @@
+// Device helpers and launch interfaces of the 4-bit KV cache (number format and tile layout:
+// include/pqhsa.h).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace pqhsa {
+
+constexpr int kTileTok = HSA_KV4_TILE_TOKENS;      // tokens per tile
+constexpr int kTileBytes = HSA_KV4_TILE_BYTES;
+constexpr int kOffV = 1024;                        // value codes within a tile
+constexpr int kOffScale = 2048;                    // scale words within a tile
+constexpr int kKv4MaxSms = 160;                    // blocks that the workspace has slots for, by SMs
+
+// What every kv4 kernel knows of the cache.
+struct Kv4View {
+  uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  int32_t* err;
+  int B, Hq, Hkv, max_pages, num_pages;
+  int page_tiles_log2;       // log2(page_size / 16)
+};
+
+// Tokens of sequence b, never more than its block table covers.
+__device__ __forceinline__ int kv4_len(const Kv4View& c, int b) {
+  const long long cap = static_cast<long long>(c.max_pages) << (c.page_tiles_log2 + 4);
+  return static_cast<int>(max(0ll, min(static_cast<long long>(c.seq_lens[b]), cap)));
+}
+
+// Page of 16-token tile t of sequence b, -1 (flagged) if the block table has none.
+__device__ __forceinline__ int kv4_page(const Kv4View& c, int b, int t) {
+  const int page = c.block_table[static_cast<size_t>(b) * c.max_pages + (t >> c.page_tiles_log2)];
+  if (page < 0 || page >= c.num_pages) {
+    record_error(c.err, HSA_DEVERR_PAGE);
+    return -1;
+  }
+  return page;
+}
+
+// Byte offset of head h's tile t (a sequence's tile number) in its page.
+__device__ __forceinline__ size_t kv4_tile_offset(const Kv4View& c, int page, int h, int t) {
+  const size_t in_page = t & ((1 << c.page_tiles_log2) - 1);
+  return (((static_cast<size_t>(page) * c.Hkv + h) << c.page_tiles_log2) + in_page) * kTileBytes;
+}
+
+// The four bytes of w, each a pair of codes (low nibble first), as fp16 pairs.
+__device__ __forceinline__ void e2m1_to_f16x2(uint32_t w, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+      : "r"(w));
+}
+// Product of two fp16 pairs (exact for a code and a scale: at most six significant bits).
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Scale byte `i` of w in both halves of an fp16 pair: byte << 7 is the scale in fp16.
+__device__ __forceinline__ uint32_t scale_both(uint32_t w, int i) { return ((w >> (8 * i)) & 0xffu) * 0x00800080u; }
+// Scale bytes `i` and `i + 1` of w as an fp16 pair.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t w, int i) {
+  const uint32_t v = w >> (8 * i);
+  return ((v & 0xffu) << 7) | ((v & 0xff00u) << 15);
+}
+
+// ---- launch interfaces -------------------------------------------------------
+struct Kv4RowsParams {
+  Kv4View c;
+  uint8_t* k;                 // rows of T, first element
+  uint8_t* v;
+  long long k_tok, k_head, v_tok, v_head;   // strides in bytes
+  const int32_t* cu;          // [B + 1]
+  const int32_t* start;       // read: first position; write: null (the last tokens)
+  int n_rows;                 // rows behind k and v (cu_host[B])
+};
+// max_tiles: the most 16-token tiles that one sequence's rows touch
+cudaError_t launch_kv4_write(int dtype, const Kv4RowsParams& p, int max_tiles, cudaStream_t stream, bool pdl);
+cudaError_t launch_kv4_read(int dtype, const Kv4RowsParams& p, int max_tiles, cudaStream_t stream, bool pdl);
+
+struct Kv4AttendParams {
+  Kv4View c;
+  const uint8_t* q;           // rows of [Hq][128] of the call's type
+  long long q_tok;            // bytes between query tokens
+  uint8_t* out;               // [rows][Hq][128]
+  float* lse;                 // [rows][Hq] or null
+  const int32_t* cu;          // [B + 1], or null: one query token a sequence
+  float* parts;               // partial results of the blocks (see kv4_attend.cu)
+  int n_rows;                 // query tokens behind q
+  int causal, window, G;
+  float scale;
+};
+// Rows (query tokens x heads of a group) of one unit of work; max_rows: the most that a sequence has for one KV head.
+int kv4_attend_rows(int dtype, int max_rows);
+size_t kv4_attend_part_bytes();
+// tiles: of all units together.
+cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long tiles, int max_rows,
+                              cudaStream_t stream, bool pdl);
+
+// api.cu
+int device_sms();      // multiprocessors of the current device, 0 on an error
+bool pdl_enabled();
+
+}  // namespace pqhsa

@@ -1,0 +1,208 @@
+// Host side of the 4-bit KV cache calls of include/pqhsa.h: argument validation, planning and
+// launches. No allocation and no state.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/pqhsa.h"
+#include "kv4.cuh"
+
+using namespace pqhsa;
+
+namespace {
+
+constexpr int kMaxGroup = 128;      // query heads a KV head
+constexpr int kMaxBatch = 65535;    // grid rows
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+size_t elem_bytes(int32_t dtype) { return dtype == HSA_F32 ? 4 : 2; }
+bool known_type(int32_t dtype) { return dtype == HSA_F32 || dtype == HSA_BF16 || dtype == HSA_F16; }
+
+hsa_status check_kv4(const hsa_kv4_cache* kv) {
+  if (!kv || !kv->cache || !kv->block_table || !kv->seq_lens || !kv->seq_lens_host) return HSA_ERR_INVALID_ARG;
+  if (kv->B < 1 || kv->Hkv < 1 || kv->Hq < 1 || kv->max_pages < 1 || kv->num_pages < 1) return HSA_ERR_INVALID_ARG;
+  if (kv->Hq % kv->Hkv) return HSA_ERR_INVALID_ARG;
+  if (kv->Hq / kv->Hkv > kMaxGroup || kv->B > kMaxBatch) return HSA_ERR_UNSUPPORTED;
+  if (kv->D != kD) return HSA_ERR_UNSUPPORTED;
+  if (kv->page_size != 16 && kv->page_size != 32 && kv->page_size != 64 && kv->page_size != 128)
+    return HSA_ERR_UNSUPPORTED;
+  if (!aligned(kv->cache, 256) || !aligned(kv->block_table, 4) || !aligned(kv->seq_lens, 4)) return HSA_ERR_ALIGNMENT;
+  const long long tmax = static_cast<long long>(kv->max_pages) * kv->page_size;
+  if (tmax >= (1LL << 31)) return HSA_ERR_UNSUPPORTED;   // positions are 32-bit
+  for (int b = 0; b < kv->B; ++b)
+    if (kv->seq_lens_host[b] < 0 || kv->seq_lens_host[b] > tmax) return HSA_ERR_CAPACITY;
+  return HSA_OK;
+}
+
+size_t workspace_bytes() { return align_up(sizeof(WsHeader), 256) + align_up(kv4_attend_part_bytes(), 256); }
+
+hsa_status check_workspace(const void* ws, size_t bytes) {
+  return !ws || !aligned(ws, 256) || bytes < workspace_bytes() ? HSA_ERR_WORKSPACE : HSA_OK;
+}
+
+hsa_status check_rows(const hsa_kv4_rows* r, int32_t dtype) {
+  if (!r || !r->data) return HSA_ERR_INVALID_ARG;
+  const long long e = elem_bytes(dtype);
+  if (!aligned(r->data, 16) || r->token_stride * e % 16 || r->head_stride * e % 16) return HSA_ERR_ALIGNMENT;
+  return HSA_OK;
+}
+
+// cu[0] = 0, not falling; *most: the largest step.
+hsa_status check_cu(const int32_t* cu, const int32_t* cu_host, int B, int* most) {
+  if (!cu || !cu_host) return HSA_ERR_INVALID_ARG;
+  if (!aligned(cu, 4)) return HSA_ERR_ALIGNMENT;
+  if (cu_host[0] != 0) return HSA_ERR_INVALID_ARG;
+  *most = 0;
+  for (int b = 0; b < B; ++b) {
+    if (cu_host[b + 1] < cu_host[b]) return HSA_ERR_INVALID_ARG;
+    *most = std::max(*most, cu_host[b + 1] - cu_host[b]);
+  }
+  return HSA_OK;
+}
+
+Kv4View view(const hsa_kv4_cache* kv, void* ws) {
+  Kv4View c = {};
+  c.cache = static_cast<uint8_t*>(kv->cache);
+  c.block_table = kv->block_table;
+  c.seq_lens = kv->seq_lens;
+  c.err = static_cast<int32_t*>(ws);
+  c.B = kv->B;
+  c.Hq = kv->Hq;
+  c.Hkv = kv->Hkv;
+  c.max_pages = kv->max_pages;
+  c.num_pages = kv->num_pages;
+  for (int s = kv->page_size / kTileTok; s > 1; s >>= 1) ++c.page_tiles_log2;
+  return c;
+}
+
+Kv4RowsParams rows_params(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hsa_kv4_rows* v, int32_t dtype,
+                          const int32_t* cu, int n_rows, void* ws) {
+  const long long e = elem_bytes(dtype);
+  Kv4RowsParams p = {};
+  p.c = view(kv, ws);
+  p.k = static_cast<uint8_t*>(k->data);
+  p.v = static_cast<uint8_t*>(v->data);
+  p.k_tok = k->token_stride * e;
+  p.k_head = k->head_stride * e;
+  p.v_tok = v->token_stride * e;
+  p.v_head = v->head_stride * e;
+  p.cu = cu;
+  p.n_rows = n_rows;
+  return p;
+}
+
+// Checks shared by the two attention calls, and their launch. cu_host: null with one query token a sequence.
+hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void* out, float* lse, int32_t dtype,
+                  const int32_t* cu, const int32_t* cu_host, float scale, int32_t causal, int32_t window, void* ws,
+                  size_t ws_bytes, cudaStream_t stream) {
+  hsa_status st = check_kv4(kv);
+  if (st != HSA_OK) return st;
+  if (!q || !out || !known_type(dtype) || !std::isfinite(scale) || window < 0 || (causal != 0 && causal != 1))
+    return HSA_ERR_INVALID_ARG;
+  if (window > 0 && !causal) return HSA_ERR_INVALID_ARG;
+  int most = 1, n_rows = kv->B;
+  if (cu_host || cu) {
+    st = check_cu(cu, cu_host, kv->B, &most);
+    if (st != HSA_OK) return st;
+    n_rows = cu_host[kv->B];
+    if (static_cast<long long>(most) * (kv->Hq / kv->Hkv) >= (1LL << 30)) return HSA_ERR_UNSUPPORTED;
+  }
+  const long long e = elem_bytes(dtype);
+  if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) || q_stride * e % 16) return HSA_ERR_ALIGNMENT;
+  st = check_workspace(ws, ws_bytes);
+  if (st != HSA_OK) return st;
+  if (n_rows == 0) return HSA_OK;
+  const int sms = device_sms();
+  if (!sms) return HSA_ERR_CUDA;
+  Kv4AttendParams p = {};
+  p.c = view(kv, ws);
+  p.q = static_cast<const uint8_t*>(q);
+  p.q_tok = q_stride * e;
+  p.out = static_cast<uint8_t*>(out);
+  p.lse = lse;
+  p.cu = cu;
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(sizeof(WsHeader), 256));
+  p.n_rows = n_rows;
+  p.causal = causal;
+  p.window = window;
+  p.G = kv->Hq / kv->Hkv;
+  p.scale = scale;
+  const int rows = kv4_attend_rows(dtype, most * p.G);
+  long long tiles = 0;   // of all units: the kernels take equal shares of them
+  for (int b = 0; b < kv->B; ++b) {
+    const long long T = kv->seq_lens_host[b], n = cu_host ? cu_host[b + 1] - cu_host[b] : 1;
+    if (n == 0) continue;
+    const long long lo = window > 0 ? std::max(0ll, T - n - window + 1) / kTileTok : 0;
+    tiles += ((T + kTileTok - 1) / kTileTok - lo) * ((n * p.G + rows - 1) / rows) * kv->Hkv;
+  }
+  return launch_kv4_attend(dtype, rows, p, sms, tiles, most * p.G, stream, pdl_enabled()) == cudaSuccess ? HSA_OK
+                                                                                                       : HSA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+void hsa_kv4_abi_sizes(int64_t* cache, int64_t* rows) {
+  if (cache) *cache = sizeof(hsa_kv4_cache);
+  if (rows) *rows = sizeof(hsa_kv4_rows);
+}
+
+size_t hsa_kv4_workspace_bytes(const hsa_kv4_cache* kv) { return check_kv4(kv) == HSA_OK ? workspace_bytes() : 0; }
+
+hsa_status hsa_kv4_write(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hsa_kv4_rows* v, int32_t dtype,
+                         const int32_t* cu_new, const int32_t* cu_new_host, void* ws, size_t ws_bytes,
+                         cudaStream_t stream) {
+  hsa_status st = check_kv4(kv);
+  if (st != HSA_OK) return st;
+  if (!known_type(dtype)) return HSA_ERR_INVALID_ARG;
+  if ((st = check_rows(k, dtype)) != HSA_OK || (st = check_rows(v, dtype)) != HSA_OK) return st;
+  int most = 0;
+  if ((st = check_cu(cu_new, cu_new_host, kv->B, &most)) != HSA_OK) return st;
+  for (int b = 0; b < kv->B; ++b)
+    if (cu_new_host[b + 1] - cu_new_host[b] > kv->seq_lens_host[b]) return HSA_ERR_CAPACITY;
+  if ((st = check_workspace(ws, ws_bytes)) != HSA_OK) return st;
+  if (most == 0) return HSA_OK;
+  const Kv4RowsParams p = rows_params(kv, k, v, dtype, cu_new, cu_new_host[kv->B], ws);
+  return launch_kv4_write(dtype, p, most / kTileTok + 2, stream, pdl_enabled()) == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
+}
+
+hsa_status hsa_kv4_read(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hsa_kv4_rows* v, int32_t dtype,
+                        const int32_t* start, const int32_t* start_host, const int32_t* cu, const int32_t* cu_host,
+                        void* ws, size_t ws_bytes, cudaStream_t stream) {
+  hsa_status st = check_kv4(kv);
+  if (st != HSA_OK) return st;
+  if (!known_type(dtype) || !start || !start_host) return HSA_ERR_INVALID_ARG;
+  if ((st = check_rows(k, dtype)) != HSA_OK || (st = check_rows(v, dtype)) != HSA_OK) return st;
+  int most = 0;
+  if ((st = check_cu(cu, cu_host, kv->B, &most)) != HSA_OK) return st;
+  if (!aligned(start, 4)) return HSA_ERR_ALIGNMENT;
+  for (int b = 0; b < kv->B; ++b) {
+    if (start_host[b] < 0) return HSA_ERR_INVALID_ARG;
+    if (static_cast<long long>(start_host[b]) + cu_host[b + 1] - cu_host[b] > kv->seq_lens_host[b])
+      return HSA_ERR_CAPACITY;
+  }
+  if ((st = check_workspace(ws, ws_bytes)) != HSA_OK) return st;
+  if (most == 0) return HSA_OK;
+  Kv4RowsParams p = rows_params(kv, k, v, dtype, cu, cu_host[kv->B], ws);
+  p.start = start;
+  return launch_kv4_read(dtype, p, most / kTileTok + 2, stream, pdl_enabled()) == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
+}
+
+hsa_status dense_decode_kv4(const hsa_kv4_cache* kv, const void* q, void* out, float* lse, int32_t dtype, float scale,
+                            int32_t window, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  return attend(kv, q, kv ? static_cast<int64_t>(kv->Hq) * kD : 0, out, lse, dtype, nullptr, nullptr, scale, 1, window,
+                ws, ws_bytes, stream);
+}
+
+hsa_status dense_prefill_kv4(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void* out, float* lse,
+                             int32_t dtype, const int32_t* cu_q, const int32_t* cu_q_host, float scale, int32_t causal,
+                             int32_t window, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!cu_q || !cu_q_host) return HSA_ERR_INVALID_ARG;
+  return attend(kv, q, q_stride, out, lse, dtype, cu_q, cu_q_host, scale, causal, window, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,319 @@
+// Rows into and out of the 4-bit KV cache: quantise as written, and read back.
+//
+// One warp works on one tile (16 tokens of one sequence and KV head). A lane holds whole
+// scale blocks: of the keys, dims [32 (lane % 4), +32) of tokens lane / 4 and 8 + lane / 4
+// (two blocks each); of the values, dims [16 (lane / 4), +16) of the token pairs 2 (lane % 4)
+// and 8 + 2 (lane % 4) (one block a token). So no value crosses lanes, and each lane's codes
+// and scales are four 16-byte pieces and one 8-byte word of the tile at 16 (8) x lane.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kv4.cuh"
+
+namespace pqhsa {
+namespace {
+
+constexpr int kRowsThreads = 256;
+
+template <typename T>
+struct Elem;
+template <>
+struct Elem<float> {
+  static __device__ __forceinline__ void load16(const uint8_t* p, float* x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(p)[i];
+      x[4 * i] = v.x;
+      x[4 * i + 1] = v.y;
+      x[4 * i + 2] = v.z;
+      x[4 * i + 3] = v.w;
+    }
+  }
+  // 16 values from fp16 pairs
+  static __device__ __forceinline__ void store16(uint8_t* p, const uint32_t* h) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
+      reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
+    }
+  }
+};
+template <>
+struct Elem<__nv_bfloat16> {
+  static __device__ __forceinline__ void load16(const uint8_t* p, float* x) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[8 * i + 2 * j] = bf16lo(w[j]);
+        x[8 * i + 2 * j + 1] = bf16hi(w[j]);
+      }
+    }
+  }
+  static __device__ __forceinline__ void store16(uint8_t* p, const uint32_t* h) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);   // exact
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+};
+template <>
+struct Elem<__half> {
+  static __device__ __forceinline__ void load16(const uint8_t* p, float* x) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+        x[8 * i + 2 * j] = a.x;
+        x[8 * i + 2 * j + 1] = a.y;
+      }
+    }
+  }
+  static __device__ __forceinline__ void store16(uint8_t* p, const uint32_t* h) {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+};
+
+// One block: scale byte and 16 values over scale, not yet rounded to codes.
+// a / 6 and x / scale are correctly rounded divisions: a quotient at a rounding border of the
+// few-bit result is then exact, so ties are ties, and no quotient beside a border reaches it.
+__device__ __forceinline__ uint32_t quantise16(float* x) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  if (top >= 0x7f800000u) {   // a NaN or an infinity
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    return 255u;
+  }
+  const float y = fminf(__fdiv_rn(__uint_as_float(top), 6.f), 10240.f);
+  uint32_t byte;
+  float scale;
+  if (y >= 6.103515625e-05f) {   // 2^-14, the smallest normal scale: three mantissa bits, nearest even
+    const uint32_t u = __float_as_uint(y);
+    const uint32_t r = (u + 0x7ffffu + ((u >> 20) & 1u)) >> 20;
+    byte = r - ((127u - 15u) << 3);
+    scale = __uint_as_float(r << 20);
+  } else {                       // multiples of 2^-17
+    const float n = rintf(y * 131072.f);
+    byte = static_cast<uint32_t>(n);
+    scale = n * 7.62939453125e-06f;
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = byte ? __fdiv_rn(x[i], scale) : 0.f;
+  return byte;
+}
+
+// Two values as one byte of codes (lo in the low nibble), nearest even, at most 6.
+__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
+  uint32_t d;
+  asm("{\n\t.reg .b8 b;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
+      "cvt.u32.u8 %0, b;\n\t}"
+      : "=r"(d)
+      : "f"(lo), "f"(hi));
+  return d;
+}
+
+__device__ __forceinline__ void zero16(float* x) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.f;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(Kv4RowsParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const Kv4View& c = p.c;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.y;
+  const int r0 = p.cu[b];
+  const int p1 = kv4_len(c, b);
+  const int n = min(p.cu[b + 1] - r0, p.n_rows - r0);
+  const int p0 = max(0, p1 - n);
+  const int first = r0 + n - p1;   // row of position 0 (may be negative)
+  if (n <= 0 || r0 < 0 || p1 <= 0) return;
+  const int t0 = p0 / kTileTok, t1 = (p1 + kTileTok - 1) / kTileTok;
+  const long long items = static_cast<long long>(t1 - t0) * c.Hkv;
+  const long long stride = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
+  for (long long it = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += stride) {
+    const int t = t0 + static_cast<int>(it / c.Hkv), h = static_cast<int>(it % c.Hkv);
+    const int page = kv4_page(c, b, t);
+    if (page < 0) continue;
+    uint8_t* tile = c.cache + kv4_tile_offset(c, page, h, t);
+    const int pos = t * kTileTok;
+    uint2* sw = reinterpret_cast<uint2*>(tile + kOffScale) + lane;
+    const bool whole = pos >= p0 && pos + kTileTok <= p1;
+    uint2 scales = whole ? make_uint2(0u, 0u) : *sw;   // tokens that stay keep their bytes
+    const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int pk = pos + half * 8 + r;
+      if (pk >= p0 && pk < p1) {
+        const uint8_t* row = p.k + (static_cast<long long>(first) + pk) * p.k_tok + h * p.k_head + q * 32 * sizeof(T);
+        float x[16], y[16];
+        Elem<T>::load16(row, x);
+        Elem<T>::load16(row + 16 * sizeof(T), y);
+        const uint32_t s = quantise16(x) | (quantise16(y) << 8);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          w[i >> 2] |= codes2(x[2 * i], x[2 * i + 1]) << (8 * (i & 3));
+          w[2 + (i >> 2)] |= codes2(y[2 * i], y[2 * i + 1]) << (8 * (i & 3));
+        }
+        reinterpret_cast<uint4*>(tile + half * 512)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+        scales.x = (scales.x & ~(0xffffu << (16 * half))) | (s << (16 * half));
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int pv = pos + half * 8 + 2 * q;
+      const bool in0 = pv >= p0 && pv < p1, in1 = pv + 1 >= p0 && pv + 1 < p1;
+      if (in0 || in1) {
+        const uint8_t* row = p.v + (static_cast<long long>(first) + pv) * p.v_tok + h * p.v_head + r * 16 * sizeof(T);
+        float x[16], y[16];
+        uint4* at = reinterpret_cast<uint4*>(tile + kOffV + half * 512) + lane;
+        if (in0) Elem<T>::load16(row, x); else zero16(x);
+        if (in1) Elem<T>::load16(row + p.v_tok, y); else zero16(y);
+        const uint32_t s0 = quantise16(x), s1 = quantise16(y);
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i >> 2] |= codes2(x[i], y[i]) << (8 * (i & 3));
+        uint32_t keep = (in0 ? 0u : 0x0f0f0f0fu) | (in1 ? 0u : 0xf0f0f0f0u);
+        if (keep) {
+          const uint4 old = *at;
+          w[0] = (w[0] & ~keep) | (old.x & keep);
+          w[1] = (w[1] & ~keep) | (old.y & keep);
+          w[2] = (w[2] & ~keep) | (old.z & keep);
+          w[3] = (w[3] & ~keep) | (old.w & keep);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+        const uint32_t m = (in0 ? 0xffu : 0u) | (in1 ? 0xff00u : 0u);
+        scales.y = (scales.y & ~(m << (16 * half))) | (((s0 | (s1 << 8)) & m) << (16 * half));
+      }
+    }
+    *sw = scales;
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowsParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const Kv4View& c = p.c;
+  const int lane = threadIdx.x & 31;
+  const int b = blockIdx.y;
+  const int r0 = p.cu[b];
+  const int p0 = p.start[b];
+  const int n = min(p.cu[b + 1] - r0, p.n_rows - r0);
+  if (n <= 0 || r0 < 0 || p0 < 0) return;
+  const long long cap = static_cast<long long>(c.max_pages) << (c.page_tiles_log2 + 4);
+  const int p1 = static_cast<int>(min(static_cast<long long>(p0) + n, cap));
+  const int t0 = p0 / kTileTok, t1 = (p1 + kTileTok - 1) / kTileTok;
+  const long long items = static_cast<long long>(t1 - t0) * c.Hkv;
+  const long long stride = static_cast<long long>(gridDim.x) * (kRowsThreads / 32);
+  for (long long it = static_cast<long long>(blockIdx.x) * (kRowsThreads / 32) + (threadIdx.x >> 5); it < items;
+       it += stride) {
+    const int t = t0 + static_cast<int>(it / c.Hkv), h = static_cast<int>(it % c.Hkv);
+    const int page = kv4_page(c, b, t);
+    uint4 code[4] = {};
+    uint2 sc = make_uint2(0u, 0u);
+    if (page >= 0) {
+      const uint8_t* tile = c.cache + kv4_tile_offset(c, page, h, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) code[i] = __ldg(reinterpret_cast<const uint4*>(tile + i * 512) + lane);
+      sc = __ldg(reinterpret_cast<const uint2*>(tile + kOffScale) + lane);
+    }
+    const int pos = t * kTileTok;
+    const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int pk = pos + half * 8 + r;
+      if (pk >= p0 && pk < p1) {
+        uint8_t* row = p.k + (static_cast<long long>(r0) + (pk - p0)) * p.k_tok + h * p.k_head + q * 32 * sizeof(T);
+        const uint32_t w[4] = {code[half].x, code[half].y, code[half].z, code[half].w};
+        uint32_t f[16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e2m1_to_f16x2(w[i], f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        const uint32_t sa = scale_both(sc.x, 2 * half), sb = scale_both(sc.x, 2 * half + 1);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = hmul2(f[i], i < 8 ? sa : sb);
+        Elem<T>::store16(row, f);
+        Elem<T>::store16(row + 16 * sizeof(T), f + 8);
+      }
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int pv = pos + half * 8 + 2 * q;
+      const bool in0 = pv >= p0 && pv < p1, in1 = pv + 1 >= p0 && pv + 1 < p1;
+      if (in0 || in1) {
+        uint8_t* row = p.v + (static_cast<long long>(r0) + (pv - p0)) * p.v_tok + h * p.v_head + r * 16 * sizeof(T);
+        const uint32_t w[4] = {code[2 + half].x, code[2 + half].y, code[2 + half].z, code[2 + half].w};
+        uint32_t f[16], a[8], d[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e2m1_to_f16x2(w[i], f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+        const uint32_t s = scale_pair(sc.y, 2 * half);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = hmul2(f[i], s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {   // (token, token + 1) pairs to (dim, dim + 1) pairs
+          a[i] = __byte_perm(f[2 * i], f[2 * i + 1], 0x5410);
+          d[i] = __byte_perm(f[2 * i], f[2 * i + 1], 0x7632);
+        }
+        if (in0) Elem<T>::store16(row, a);
+        if (in1) Elem<T>::store16(row + p.v_tok, d);
+      }
+    }
+  }
+}
+
+template <typename T, bool kWrite>
+cudaError_t launch_rows(const Kv4RowsParams& p, int max_tiles, cudaStream_t stream, bool pdl) {
+  const long long warps = static_cast<long long>(max_tiles) * p.c.Hkv;
+  const long long blocks = (warps + kRowsThreads / 32 - 1) / (kRowsThreads / 32);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 1 ? 1 : blocks > 65536 ? 65536 : blocks), p.c.B);
+  cfg.blockDim = dim3(kRowsThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (kWrite) return cudaLaunchKernelEx(&cfg, kv4_write_kernel<T>, p);
+  return cudaLaunchKernelEx(&cfg, kv4_read_kernel<T>, p);
+}
+
+template <bool kWrite>
+cudaError_t launch_rows_of(int dtype, const Kv4RowsParams& p, int max_tiles, cudaStream_t stream, bool pdl) {
+  switch (dtype) {
+    case HSA_F32: return launch_rows<float, kWrite>(p, max_tiles, stream, pdl);
+    case HSA_BF16: return launch_rows<__nv_bfloat16, kWrite>(p, max_tiles, stream, pdl);
+    case HSA_F16: return launch_rows<__half, kWrite>(p, max_tiles, stream, pdl);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_write(int dtype, const Kv4RowsParams& p, int max_tiles, cudaStream_t stream, bool pdl) {
+  return launch_rows_of<true>(dtype, p, max_tiles, stream, pdl);
+}
+cudaError_t launch_kv4_read(int dtype, const Kv4RowsParams& p, int max_tiles, cudaStream_t stream, bool pdl) {
+  return launch_rows_of<false>(dtype, p, max_tiles, stream, pdl);
+}
+
+}  // namespace pqhsa

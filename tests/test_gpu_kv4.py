@@ -1,0 +1,598 @@
+"""The 4-bit KV cache on the GPU against the float64 oracle: bytes written, values read back, attention of one and of
+several query tokens, at the sizes and masks where they can go wrong."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_long_context_pq_b200 as P
+from oracle import kv4_oracle as O4
+
+pytestmark = pytest.mark.gpu
+
+D = 128
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32)
+
+
+class Case:
+    """Pages in a shuffled order, with random codes and scales in the range of real keys and values."""
+
+    def __init__(self, lens, Hkv, G, page, seed=0, spare=2, scales=(104, 120), filler=None):
+        rng = np.random.default_rng(seed)
+        self.rng, self.lens, self.Hkv, self.G, self.page = rng, list(lens), Hkv, G, page
+        need = [-(-t // page) for t in lens]
+        pages = sum(need) + spare
+        order = rng.permutation(pages)
+        self.table = np.full((len(lens), max(need) + 1), -1, dtype=np.int32)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[at:at + n]
+            at += n
+        self.bytes = rng.integers(0, 256, (pages, Hkv, page // 16, O4.TILE_BYTES), dtype=np.uint8)
+        self.bytes[..., 2048:] = rng.integers(*scales, self.bytes[..., 2048:].shape, dtype=np.uint8)
+        if filler is not None:   # bytes of tokens past the end, and of pages that nobody uses
+            keep = np.zeros(self.bytes.shape, dtype=bool)
+            d = np.arange(D)
+            for b, t in enumerate(lens):
+                for pos in range(t):
+                    for h in range(Hkv):
+                        tile = O4.tile_of(keep, self.table[b], h, pos, page)
+                        for value in (False, True):
+                            a, _, s = O4._address(pos % 16, d, value)
+                            tile[a] = True
+                            tile[s] = True
+            self.bytes = np.where(keep, self.bytes, filler).astype(np.uint8)
+
+    def device(self):
+        dev = torch.device("cuda:0")
+        self.kv = P.KV4Cache(torch.from_numpy(self.bytes.copy()).to(dev), torch.from_numpy(self.table).to(dev),
+                             i32(self.lens).to(dev), i32(self.lens), self.Hkv * self.G)
+        self.ws = P.workspace(P.hsa_kv4_workspace_bytes(self.kv), dev)
+        return self.kv
+
+    def held(self, b, h, lo=0, hi=None):
+        return O4.get(self.bytes, self.table[b], h, range(lo, self.lens[b] if hi is None else hi), self.page)
+
+    def error(self):
+        return P.hsa_read_error(self.ws)
+
+
+def rows(rng, shape, kind):
+    return torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(TYPES[kind])
+
+
+def cu_of(news):
+    return i32(np.cumsum([0] + list(news)))
+
+
+def check(got, lse, q, case, news, scale, kind, causal=True, window=0, units=None):
+    """Compare with the oracle. How far a row may be off, relative to the largest |value| in its reach:
+    - a logit: q in 22 bits (11 in one fp16 number of a 16-bit q, which holds it to 2^-25 of its largest element:
+      2^-22 covers both) and at most 16 fp32 sums of 2^-23, of scale * sum |q||k|; the power of two adds 2^-21;
+      weights and their sum each take that error;
+    - a weight in 16-bit calls is rounded to fp16, 2^-11; the rounding of the result is eps / 2;
+    - sums over tokens: one fp32 addition of 2^-23 for each 16-token step, in warps of at most T / 16 steps."""
+    got, lse = got.double().cpu().numpy(), lse.double().cpu().numpy()
+    qn = q.double().cpu().numpy()
+    cu = np.cumsum([0] + list(news))
+    G = case.G
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind]
+    for b, n in enumerate(news):
+        T = case.lens[b]
+        for h in range(case.Hkv):
+            if n == 0 or (units is not None and (b, h) not in units):
+                continue
+            k, v = case.held(b, h)
+            pos = T - n + np.arange(n)
+            j = np.arange(T)
+            seen = np.ones((n, T), dtype=bool)
+            if causal:
+                seen = j[None] <= pos[:, None]
+                if window:
+                    seen &= j[None] > pos[:, None] - window
+            finite_k, finite_v = np.nan_to_num(np.abs(k)), np.nan_to_num(np.abs(v))
+            for g in range(G):
+                r = qn[cu[b]:cu[b + 1], h * G + g]
+                ref, ref_lse = O4.attend(r, k, v, scale, seen)
+                mine, mine_lse = got[cu[b]:cu[b + 1], h * G + g], lse[cu[b]:cu[b + 1], h * G + g]
+                logit = abs(scale) * (np.abs(r) @ finite_k.T).max(1, initial=0.0) if T else np.zeros(n)
+                rel = 2 * (logit * (2.0 ** -22 + 16 * 2.0 ** -23) + 2.0 ** -21 + (T / 16 + 16) * 2.0 ** -23)
+                if kind != "f32":
+                    rel = rel + 2.0 ** -11
+                tol = rel * finite_v.max(initial=0.0) + np.abs(np.nan_to_num(ref)).max(1) * half
+                nan = np.isnan(ref)
+                assert np.array_equal(np.isnan(mine), nan), (b, h, g)
+                off = np.abs(np.where(nan, 0, mine - np.where(nan, 0, ref))).max(1)
+                assert (off <= tol).all(), (b, h, g, float((off / np.maximum(tol, 1e-300)).max()))
+                empty = np.isneginf(ref_lse)
+                assert np.array_equal(np.isneginf(mine_lse), empty), (b, h, g)
+                known = ~empty & ~np.isnan(ref_lse)
+                assert np.array_equal(np.isnan(mine_lse[~empty]), np.isnan(ref_lse[~empty])), (b, h, g)
+                lse_tol = rel + 2.0 ** -22 * np.abs(np.nan_to_num(ref_lse, neginf=0.0))
+                assert (np.abs(mine_lse - ref_lse)[known] <= lse_tol[known]).all(), (b, h, g)
+
+
+# ---- write -----------------------------------------------------------------------------------------------------
+
+
+def written(case, k, v, news):
+    """The oracle's bytes after the write."""
+    want = case.bytes.copy()
+    at = 0
+    for b, n in enumerate(news):
+        for i in range(n):
+            for h in range(case.Hkv):
+                O4.put(want, case.table[b], h, case.lens[b] - n + i, case.page, k[at, h].double().numpy(),
+                       v[at, h].double().numpy())
+            at += 1
+    return want
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("lens,news,Hkv,page", [
+    ([1], [1], 1, 16), ([16, 17, 15], [16, 1, 2], 2, 16), ([33, 40, 7, 64], [20, 0, 7, 1], 3, 32), ([130, 100], [129, 37], 2, 64),
+    ([200], [131], 1, 128),
+])
+def test_write_gives_the_oracles_bytes(cuda_device, kind, lens, news, Hkv, page):
+    case = Case(lens, Hkv, 1, page, seed=len(lens))
+    kv = case.device()
+    k, v = rows(case.rng, (sum(news), Hkv, D), kind), rows(case.rng, (sum(news), Hkv, D), kind) * 3
+    cu = cu_of(news)
+    P.hsa_kv4_write(kv, k.to(cuda_device), v.to(cuda_device), cu.to(cuda_device), cu, workspace_buf=case.ws)
+    assert np.array_equal(kv.cache.cpu().numpy(), written(case, k, v, news))
+    assert case.error() == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_write_at_the_edges_of_the_format(cuda_device, kind):
+    """Zeros, the smallest and largest scales, saturation, blocks with NaN and infinities, exact ties."""
+    n = 24
+    case = Case([n], 1, 1, 16, seed=3)
+    kv = case.device()
+    x = torch.from_numpy(case.rng.standard_normal((n, 1, D)).astype(np.float32))
+    x *= torch.exp2(torch.linspace(-40, 30, n))[:, None, None]
+    x[0] = 0
+    x[1, 0, 16:32] = -0.0
+    x[2, 0, 3] = float("nan")
+    x[2, 0, 40] = float("inf")
+    x[2, 0, 70] = -float("inf")
+    x[3, 0, :16] = torch.arange(16) * 0.25               # ties of the codes (scale 0.625)
+    x[4, 0] = 0
+    x[4, 0, 0::16] = 6.0 * torch.tensor([(8 + i + 0.5) / 8 for i in range(8)])   # ties of the scales
+    x[5, 0] = 6.0 * 2.0 ** -18                           # below half of the smallest scale step: a tie, to zero
+    x[6, 0] = 6.1 * 2.0 ** -18
+    x[7, 0] = 61440.0
+    x[8, 0] = 65000.0
+    if kind == "f32":
+        x[9, 0] = 3.0e38
+        x[10, 0] = 1e-44
+    x = x.to(TYPES[kind])
+    y = x.flip(0)
+    cu = cu_of([n])
+    P.hsa_kv4_write(kv, x.to(cuda_device), y.to(cuda_device), cu.to(cuda_device), cu, workspace_buf=case.ws)
+    assert np.array_equal(kv.cache.cpu().numpy(), written(case, x, y, [n]))
+
+
+def test_write_of_single_steps_equals_one_write(cuda_device):
+    """21 tokens one by one, and at once; keys and values as views of a fused projection."""
+    n, Hkv = 21, 2
+    one, many = Case([5 + n, 3 + n], Hkv, 2, 16, seed=9), Case([5 + n, 3 + n], Hkv, 2, 16, seed=9)
+    kv1, kv2 = one.device(), many.device()
+    fused = rows(one.rng, (2 * n, 8, D), "bf16").to(cuda_device)
+    k, v = fused[:, 4:6], fused[:, 6:8]
+    cu = cu_of([n, n])
+    P.hsa_kv4_write(kv1, k, v, cu.to(cuda_device), cu)
+    step = cu_of([1, 1])
+    for i in range(n):
+        lens = i32([5 + i + 1, 3 + i + 1])
+        kv2.seq_lens.copy_(lens)
+        kv2.seq_lens_host.copy_(lens)
+        sel = torch.tensor([i, n + i], device=cuda_device)
+        P.hsa_kv4_write(kv2, k[sel], v[sel], step.to(cuda_device), step)
+    assert torch.equal(kv1.cache, kv2.cache)
+
+
+# ---- read ------------------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("lens,start,news,page", [
+    ([1], [0], [1], 16), ([40, 33, 90], [3, 33, 0], [30, 0, 90], 16), ([300], [131], [100], 128), ([77, 64], [15, 16], [2, 48], 32),
+])
+def test_read_is_exact(cuda_device, kind, lens, start, news, page):
+    Hkv = 2
+    case = Case(lens, Hkv, 1, page, seed=sum(lens), scales=(0, 227))
+    kv = case.device()
+    cu, st = cu_of(news), i32(start)
+    n = sum(news)
+    room = torch.full((2, n + 1, Hkv + 1, D + 8), 7.0, dtype=TYPES[kind], device=cuda_device)
+    ko, vo = room[0, :n, :Hkv, :D], room[1, :n, :Hkv, :D]
+    P.hsa_kv4_read(kv, st.to(cuda_device), st, cu.to(cuda_device), cu, k_out=ko, v_out=vo, workspace_buf=case.ws)
+    at = 0
+    for b, m in enumerate(news):
+        for h in range(Hkv):
+            k, v = case.held(b, h, start[b], start[b] + m)
+            assert np.array_equal(ko[at:at + m, h].double().cpu().numpy(), k)
+            assert np.array_equal(vo[at:at + m, h].double().cpu().numpy(), v)
+        at += m
+    assert (room[:, n:] == 7).all() and (room[:, :, Hkv:] == 7).all() and (room[..., D:] == 7).all()
+    k2, v2 = P.hsa_kv4_read(kv, st.to(cuda_device), st, cu.to(cuda_device), cu, dtype=TYPES[kind])
+    assert torch.equal(k2, ko) and torch.equal(v2, vo)
+    assert case.error() == 0
+
+
+# ---- decode ----------------------------------------------------------------------------------------------------
+
+
+def decode(case, q, scale, window=0, stream=None):
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda:0")
+    out = P.dense_decode_kv4(case.kv, q.to("cuda:0"), scale=scale, window=window, lse=lse, workspace_buf=case.ws,
+                             stream=stream)
+    return out, lse
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("lens,Hkv,G,page,window", [
+    ([1], 1, 1, 16, 0),
+    ([0, 5, 0], 2, 4, 16, 0),
+    ([15, 16, 17, 31, 33], 2, 2, 16, 0),
+    ([1000], 2, 4, 16, 0),
+    ([700, 3, 129], 1, 8, 64, 0),
+    ([257, 640], 2, 5, 32, 0),
+    ([300, 31], 1, 16, 128, 0),
+    ([513], 1, 20, 16, 0),
+    ([190], 1, 40, 32, 0),
+    ([1000, 64, 2], 2, 4, 16, 33),
+    ([129, 500], 1, 3, 32, 1),
+])
+def test_decode(cuda_device, kind, lens, Hkv, G, page, window):
+    case = Case(lens, Hkv, G, page, seed=7 * len(lens) + G, filler=255)
+    case.device()
+    q = rows(case.rng, (len(lens), Hkv * G, D), kind)
+    scale = D ** -0.5
+    out, lse = decode(case, q, scale, window)
+    check(out, lse, q, case, [1] * len(lens), scale, kind, window=window)
+    assert case.error() == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_decode_long_units_over_many_blocks(cuda_device, kind):
+    """Long enough that every unit is shared by several blocks, beside short ones; sampled units."""
+    lens = [30011, 40, 16000, 0, 1]
+    case = Case(lens, 4, 4, 16, seed=21)
+    case.device()
+    q = rows(case.rng, (len(lens), 16, D), kind)
+    out, lse = decode(case, q, 0.1)
+    check(out, lse, q, case, [1] * 5, 0.1, kind, units={(0, 1), (1, 3), (2, 0), (4, 2)})
+    assert torch.equal(out[3], torch.zeros_like(out[3])) and torch.isneginf(lse[3]).all()
+    again, _ = decode(case, q, 0.1)
+    assert torch.equal(out, again)   # no atomics: the same bits every time
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16"])
+def test_decode_large_logits_and_growing_maximum(cuda_device, kind):
+    """Logits of several hundred whose maximum grows from tile to tile; zero, tiny and huge queries."""
+    case = Case([600], 1, 4, 16, seed=5)
+    kv = case.device()
+    k = torch.zeros(600, 1, D)
+    k[:, 0, 0] = torch.linspace(0.1, 30.0, 600)
+    k[:, 0, 17] = 1.0
+    cu = cu_of([600])
+    P.hsa_kv4_write(kv, k.to(cuda_device), torch.randn(600, 1, D).to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    q = rows(case.rng, (1, 4, D), kind)
+    q[0, 0, 0] = 20.0
+    q[0, 1] = 0
+    q[0, 2] *= 1e-4 if kind == "f16" else 1e-30
+    q[0, 3] = 0
+    q[0, 3, 0] = 60000.0 if kind == "f16" else 1e20
+    out, lse = decode(case, q, 0.5 if kind == "f16" else 1.0)
+    check(out[:, :3], lse[:, :3], q[:, :3], _with_groups(case, 3), [1], 0.5 if kind == "f16" else 1.0, kind)
+    best = case.held(0, 0)[1][-8:]   # the largest keys tie or lead: all the weight is on the last ones
+    assert np.isfinite(out.double().cpu().numpy()).all()
+    assert (np.abs(out[0, 3].double().cpu().numpy()) <= np.abs(best).max(0) * 1.01 + 1e-6).all()
+
+
+def _with_groups(case, G):
+    other = Case.__new__(Case)
+    other.__dict__.update(case.__dict__)
+    other.G = G
+    return other
+
+
+def test_a_negative_and_a_zero_scale(cuda_device):
+    case = Case([100], 1, 2, 16, seed=4)
+    case.device()
+    q = rows(case.rng, (1, 2, D), "f32")
+    for scale in (-0.2, 0.0):
+        out, lse = decode(case, q, scale)
+        check(out, lse, q, case, [1], scale, "f32")
+
+
+def test_masked_nan_does_not_spread(cuda_device):
+    """A token whose key or value blocks are NaN: only rows that see it are NaN (a value block in its own dims)."""
+    lens, n = [50], 9
+    case = Case(lens, 1, 2, 16, seed=8)
+    kv = case.device()
+    k, v = torch.randn(n, 1, D), torch.randn(n, 1, D)
+    v[4, 0, 37] = float("nan")        # dims 32..47 of position 45
+    k[7, 0, 5] = float("inf")         # position 48
+    v[8, 0, 100] = float("inf")       # position 49
+    cu = cu_of([n])
+    P.hsa_kv4_write(kv, k.to(cuda_device), v.to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    for kind in ("f32", "bf16"):
+        q = rows(case.rng, (n, 2, D), kind)
+        for window in (0, 3):
+            out, lse = prefill(case, q, [n], 0.1, window=window)
+            bad = torch.isnan(out).cpu()
+            assert not bad[:4].any() and bad[4, :, 32:48].all() and not bad[4, :, :32].any()
+            assert bad[7].all() and bad[8].all()
+            if window == 3:
+                assert not bad[6, :, :32].any() and bad[6, :, 32:48].all()
+            check(out, lse, q, case, [n], 0.1, kind, window=window)
+
+
+# ---- prefill ---------------------------------------------------------------------------------------------------
+
+
+def prefill(case, q, news, scale, causal=True, window=0, pad=0):
+    cu = cu_of(news)
+    lse = torch.full((q.shape[0], q.shape[1]), float("nan"), device="cuda:0")
+    qd = q.to("cuda:0")
+    if pad:   # a view with a longer token stride
+        wide = torch.full((q.shape[0], q.shape[1] + pad, D), float("nan"), dtype=q.dtype, device="cuda:0")
+        wide[:, :q.shape[1]] = qd
+        qd = wide[:, :q.shape[1]]
+    out = P.dense_prefill_kv4(case.kv, qd, cu.to("cuda:0"), cu, scale=scale, causal=causal, window=window, lse=lse,
+                              workspace_buf=case.ws)
+    return out, lse
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("lens,news,Hkv,G,page,causal,window", [
+    ([1], [1], 1, 1, 16, True, 0),
+    ([20, 5], [5, 5], 2, 4, 16, True, 0),
+    ([100, 64, 33], [5, 0, 33], 1, 8, 32, True, 0),
+    ([3, 40], [9, 2], 1, 4, 16, True, 0),                 # more query tokens than tokens: rows without a mask
+    ([0, 17], [3, 3], 2, 2, 16, True, 0),
+    ([130], [130], 2, 1, 64, True, 0),
+    ([257, 300], [257, 129], 1, 4, 128, True, 0),
+    ([257, 300], [70, 129], 1, 4, 16, True, 40),
+    ([150, 90], [60, 90], 2, 2, 16, False, 0),
+    ([400], [100], 1, 7, 32, True, 0),
+    ([90, 200], [33, 3], 1, 24, 16, True, 17),
+    ([600], [1], 1, 64, 64, True, 0),
+    ([513, 12, 300], [513, 12, 260], 1, 2, 16, True, 0),
+    ([700], [300], 2, 4, 32, True, 1),
+])
+def test_prefill(cuda_device, kind, lens, news, Hkv, G, page, causal, window):
+    case = Case(lens, Hkv, G, page, seed=sum(lens) + G, filler=255)
+    case.device()
+    q = rows(case.rng, (sum(news), Hkv * G, D), kind)
+    out, lse = prefill(case, q, news, 0.09, causal, window, pad=3 if G == 4 else 0)
+    check(out, lse, q, case, news, 0.09, kind, causal, window)
+    assert case.error() == 0
+
+
+# ---- what the calls promise ------------------------------------------------------------------------------------
+
+
+def test_bad_pages_are_flagged_and_skipped(cuda_device):
+    lens = [70, 50]
+    case = Case(lens, 2, 4, 16, seed=2)
+    kv = case.device()
+    kv.block_table[0, 2] = 1000
+    kv.block_table[1, 1] = -7
+    q = rows(case.rng, (2, 8, D), "f32")
+    out, lse = decode(case, q, 0.1)
+    assert case.error() == P.HSA_DEVERR_PAGE and case.error() == 0
+    k0 = [p for p in range(70) if not 32 <= p < 48]     # the tokens that are left
+    for h in range(2):
+        k, v = case.held(0, h)
+        ref, _ = O4.attend(q[0, h * 4:h * 4 + 4].double().numpy(), k[k0], v[k0], 0.1, np.ones((4, len(k0)), dtype=bool))
+        assert np.abs(out[0, h * 4:h * 4 + 4].double().cpu().numpy() - ref).max() <= 1e-5 * np.abs(v).max()
+    before = kv.cache.clone()
+    cu = cu_of([70, 0])
+    k = torch.randn(70, 2, D, device=cuda_device)
+    P.hsa_kv4_write(kv, k, k, cu.to(cuda_device), cu, workspace_buf=case.ws)
+    assert case.error() == P.HSA_DEVERR_PAGE
+    touched = (kv.cache != before).flatten(1).any(1).nonzero()[:, 0].tolist()
+    assert set(touched) <= set(case.table[0, [0, 1, 3, 4]].tolist())
+    st = i32([0, 0])
+    ko, vo = P.hsa_kv4_read(kv, st.to(cuda_device), st, cu.to(cuda_device), cu, dtype=torch.float32, workspace_buf=case.ws)
+    assert case.error() == P.HSA_DEVERR_PAGE
+    assert (ko[32:48] == 0).all() and (vo[32:48] == 0).all() and (ko[:32] != 0).any()
+
+
+def test_capture_and_replay_with_other_lengths(cuda_device):
+    """One captured step (write a token, attend) replayed while the sequences grow, against eager calls."""
+    lens = [40, 700]
+    case = Case([t + 40 for t in lens], 2, 4, 16, seed=12)
+    kv = case.device()
+    k, v = torch.randn(2, 2, D, device=cuda_device), torch.randn(2, 2, D, device=cuda_device)
+    q = torch.randn(2, 8, D, device=cuda_device)
+    out = torch.empty_like(q)
+    cu = cu_of([1, 1])
+    cud = cu.to(cuda_device)
+    ws2 = P.workspace(P.hsa_kv4_workspace_bytes(kv), cuda_device)
+
+    def step(w):
+        P.hsa_kv4_write(kv, k, v, cud, cu, workspace_buf=w)
+        P.dense_decode_kv4(kv, q, out, scale=0.1, workspace_buf=w)
+
+    kv.seq_lens.copy_(i32(lens))
+    kv.seq_lens_host.copy_(i32(lens))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(case.ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(case.ws)
+    for i in range(1, 40, 3):
+        now = i32([t + i for t in lens])
+        kv.seq_lens.copy_(now)
+        for x in (k, v, q):
+            x.normal_()
+        graph.replay()
+        got = out.clone()
+        kv.seq_lens_host.copy_(now)
+        step(ws2)
+        # other block shares (planned from the host lengths): the same sums in another order
+        assert (got - out).abs().max() <= 1e-5 * 8
+    assert case.error() == 0
+
+
+def test_other_streams_with_their_own_workspaces(cuda_device):
+    case = Case([3000, 200], 2, 4, 16, seed=30)
+    kv = case.device()
+    q = rows(case.rng, (2, 8, D), "bf16").to(cuda_device)
+    want = P.dense_decode_kv4(kv, q, scale=0.1)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = [P.dense_decode_kv4(kv, q, scale=0.1, stream=s) for s in streams for _ in range(3)]
+    outs.append(P.dense_decode_kv4(kv, q, scale=0.1, stream=streams[0].cuda_stream))
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o, want)
+
+
+def test_offsets_past_32_bits(cuda_device):
+    """A cache of more than 4 GiB whose sequence lives in its last pages."""
+    Hkv, page, T = 8, 128, 300
+    pages = (5 << 30) // (Hkv * page // 16 * O4.TILE_BYTES)
+    cache = P.KV4Cache.empty(pages, Hkv, page, cuda_device)
+    table = i32([[pages - 1, 0, pages - 2]])
+    kv = P.KV4Cache(cache, table.to(cuda_device), i32([T]).to(cuda_device), i32([T]), Hkv)
+    k, v = torch.randn(T, Hkv, D), torch.randn(T, Hkv, D)
+    cu, st = cu_of([T]), i32([0])
+    P.hsa_kv4_write(kv, k.to(cuda_device), v.to(cuda_device), cu.to(cuda_device), cu)
+    ko, vo = P.hsa_kv4_read(kv, st.to(cuda_device), st, cu.to(cuda_device), cu, dtype=torch.float32)
+    for got, x in ((ko, k), (vo, v)):
+        want = O4.values(*O4.quantise(x.double().numpy()))
+        assert np.array_equal(got.double().cpu().numpy(), want)
+    q = torch.randn(1, Hkv, D)
+    out = P.dense_decode_kv4(kv, q.to(cuda_device), scale=0.1)
+    ref, _ = O4.attend(q[0, 5:6].double().numpy(), ko[:, 5].double().cpu().numpy(), vo[:, 5].double().cpu().numpy(), 0.1,
+                       np.ones((1, T), dtype=bool))
+    assert np.abs(out[0, 5].double().cpu().numpy() - ref[0]).max() <= 1e-5 * 8
+
+
+def test_refusals_with_device_tensors(cuda_device):
+    case = Case([40], 2, 2, 16)
+    kv = case.device()
+    q = torch.zeros(1, 4, D, device=cuda_device)
+    cu = cu_of([2])
+    cud = cu.to(cuda_device)
+    for bad in (q[:, :3], q.double(), q[..., :64], torch.zeros(1, 4, 2 * D, device=cuda_device)[..., ::2]):
+        with pytest.raises(ValueError):
+            P.dense_decode_kv4(kv, bad, scale=0.1)
+    with pytest.raises(ValueError):
+        P.dense_decode_kv4(kv, q, torch.empty(1, 4, D, dtype=torch.bfloat16, device=cuda_device), scale=0.1)
+    with pytest.raises(ValueError):
+        P.dense_decode_kv4(kv, q, scale=0.1, lse=torch.empty(4, device=cuda_device))
+    with pytest.raises(ValueError):
+        P.dense_decode_kv4(kv, q.cpu(), scale=0.1)
+    with pytest.raises(P.HSAError):
+        P.dense_decode_kv4(kv, q, scale=0.1, window=-1)
+    with pytest.raises(P.HSAError):
+        P.dense_decode_kv4(kv, q, scale=0.1, workspace_buf=torch.zeros(256, dtype=torch.uint8, device=cuda_device))
+    k = torch.zeros(2, 2, D, device=cuda_device)
+    with pytest.raises(ValueError):
+        P.hsa_kv4_write(kv, k, k.half(), cud, cu)
+    with pytest.raises(ValueError):
+        P.hsa_kv4_write(kv, k[:1], k, cud, cu)
+    with pytest.raises(ValueError):
+        P.hsa_kv4_write(kv, k, k, cud, cu.long())
+    with pytest.raises(ValueError):
+        P.hsa_kv4_write(kv, k.transpose(1, 2).contiguous().transpose(1, 2), k, cud, cu)
+    many = cu_of([41])
+    k41 = torch.zeros(41, 2, D, device=cuda_device)
+    with pytest.raises(P.HSAError):
+        P.hsa_kv4_write(kv, k41, k41, many.to(cuda_device), many)
+    with pytest.raises(ValueError):
+        P.dense_prefill_kv4(kv, torch.zeros(2, 4, 2 * D, device=cuda_device)[..., :D].transpose(0, 1), cud, cu, scale=0.1)
+
+
+# ---- together --------------------------------------------------------------------------------------------------
+
+
+def test_a_sequence_from_prompt_to_decoded_tokens(cuda_device):
+    """Prompts written and attended in chunks, tokens appended and decoded one by one, the cache read back into bf16
+    pages: dense_decode over those gives what dense_decode_kv4 gives, and an index is trained on the keys."""
+    B, Hkv, G, page, total = 2, 2, 4, 16, 600
+    Hq, scale = Hkv * G, D ** -0.5
+    lens = [0, 0]
+    target = [total, 480]
+    case = Case(target, Hkv, G, page, seed=77)
+    kv = case.device()
+    gen = torch.Generator(device=cuda_device).manual_seed(3)
+    k = [torch.randn(t, Hkv, D, generator=gen, device=cuda_device).bfloat16() for t in target]
+    v = [torch.randn(t, Hkv, D, generator=gen, device=cuda_device).bfloat16() for t in target]
+    held = [[torch.from_numpy(O4.values(*O4.quantise(x.double().cpu().numpy()))) for x in side] for side in (k, v)]
+
+    def advance(news):
+        cu = cu_of(news)
+        for b in range(B):
+            lens[b] += news[b]
+        kv.seq_lens.copy_(i32(lens))
+        kv.seq_lens_host.copy_(i32(lens))
+        pick = lambda x: torch.cat([x[b][lens[b] - news[b]:lens[b]] for b in range(B)])  # noqa: E731
+        P.hsa_kv4_write(kv, pick(k), pick(v), cu.to(cuda_device), cu, workspace_buf=case.ws)
+        q = torch.randn(sum(news), Hq, D, generator=gen, device=cuda_device)
+        if max(news) == 1 and min(news) == 1:
+            out = P.dense_decode_kv4(kv, q, scale=scale, workspace_buf=case.ws)
+        else:
+            out = P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, scale=scale, workspace_buf=case.ws)
+        got, at = out.double().cpu().numpy(), 0
+        for b in range(B):
+            T, n = lens[b], news[b]
+            pos = T - n + np.arange(n)
+            seen = np.arange(T)[None] <= pos[:, None]
+            for hq in range(0, Hq, 3):
+                h = hq // G
+                ref, _ = O4.attend(q[at:at + n, hq].double().cpu().numpy(), held[0][b][:T, h].numpy(),
+                                   held[1][b][:T, h].numpy(), scale, seen)
+                if n:
+                    assert np.abs(got[at:at + n, hq] - ref).max() <= 2e-5 * 5
+            at += n
+        return out, q
+
+    advance([300, 0])
+    advance([250, 470])
+    advance([5, 5])
+    for _ in range(5):
+        out, q = advance([1, 1])
+    while lens[0] < total:
+        out, q = advance([min(20, total - lens[0]), 0])
+    q = torch.randn(B, Hq, D, generator=gen, device=cuda_device)
+    out = P.dense_decode_kv4(kv, q, scale=scale, workspace_buf=case.ws)
+    # back into bf16 pages of the same block table
+    cu, st = cu_of(target), i32([0, 0])
+    kb, vb = P.hsa_kv4_read(kv, st.to(cuda_device), st, cu.to(cuda_device), cu, workspace_buf=case.ws)
+    pages = kv.cache.shape[0]
+    kc = torch.zeros(pages, Hkv, page, D, dtype=torch.bfloat16, device=cuda_device)
+    vc = torch.zeros_like(kc)
+    for b in range(B):
+        pos = torch.arange(target[b], device=cuda_device)
+        page_of = kv.block_table[b][pos // page].long()
+        kc[page_of, :, pos % page] = kb[cu[b]:cu[b + 1]]
+        vc[page_of, :, pos % page] = vb[cu[b]:cu[b + 1]]
+    bf = P.PagedKV(kc, vc, kv.block_table.clamp(min=0), kv.seq_lens, kv.seq_lens_host, Hq)
+    dense = P.dense_decode(bf, q, scale=scale)
+    # dense_decode splits q and P into two bf16 parts (2^-16 each) of logits up to about 10
+    assert (dense - out).abs().max() <= 5 * 4 * 2.0 ** -15 * 10
+    ix = P.PQIndex.allocate(B, Hkv, 4, 600, 4, cuda_device)
+    slots = torch.randint(0, 400, (B, Hkv, 4 + 16 * 256), dtype=torch.int32, device=cuda_device)
+    P.hsa_train_index(bf, ix, 400, slots, coarse_iters=1, pq_iters=1)
+    P.hsa_append_encode(bf, ix, 400)
+    sparse = P.hsa_decode(bf, ix, q, scale=scale, budget=1.0)    # every token selected: dense attention
+    assert (sparse - out).abs().max() <= 5 * 4 * 2.0 ** -15 * 10
+    assert case.error() == 0
