@@ -43,10 +43,13 @@ __device__ __forceinline__ int kv4_page(const Kv4View& c, int b, int t) {
   return page;
 }
 
-// Byte offset of head h's tile t (a sequence's tile number) in its page.
+// Number in the cache (below 2^31, as the host checks) of head h's tile t (a sequence's tile number) in its page.
+__device__ __forceinline__ uint32_t kv4_tile_index(const Kv4View& c, int page, int h, int t) {
+  const uint32_t in_page = t & ((1 << c.page_tiles_log2) - 1);
+  return ((static_cast<uint32_t>(page) * c.Hkv + h) << c.page_tiles_log2) + in_page;
+}
 __device__ __forceinline__ size_t kv4_tile_offset(const Kv4View& c, int page, int h, int t) {
-  const size_t in_page = t & ((1 << c.page_tiles_log2) - 1);
-  return (((static_cast<size_t>(page) * c.Hkv + h) << c.page_tiles_log2) + in_page) * kTileBytes;
+  return static_cast<size_t>(kv4_tile_index(c, page, h, t)) * kTileBytes;
 }
 
 // The four bytes of w, each a pair of codes (low nibble first), as fp16 pairs.
@@ -98,14 +101,16 @@ struct Kv4AttendParams {
   float* parts;               // partial results of the blocks (see kv4_attend.cu)
   int n_rows;                 // query tokens behind q
   int causal, window, G;
+  uint32_t inv_G;             // ceil(2^32 / G)
   float scale;
 };
 // Rows (query tokens x heads of a group) of one unit of work; max_rows: the most that a sequence has for one KV head.
 int kv4_attend_rows(int dtype, int max_rows);
 size_t kv4_attend_part_bytes();
-// tiles: of all units together.
-cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long tiles, int max_rows,
-                              cudaStream_t stream, bool pdl);
+// Steps (of kv4_attend_step_tokens tokens) and units of the whole call.
+int kv4_attend_step_tokens();
+cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long steps, long long units,
+                              int max_rows, cudaStream_t stream, bool pdl);
 
 // api.cu
 int device_sms();      // multiprocessors of the current device, 0 on an error

@@ -32,6 +32,8 @@ hsa_status check_kv4(const hsa_kv4_cache* kv) {
   if (!aligned(kv->cache, 256) || !aligned(kv->block_table, 4) || !aligned(kv->seq_lens, 4)) return HSA_ERR_ALIGNMENT;
   const long long tmax = static_cast<long long>(kv->max_pages) * kv->page_size;
   if (tmax >= (1LL << 31)) return HSA_ERR_UNSUPPORTED;   // positions are 32-bit
+  if (static_cast<long long>(kv->num_pages) * kv->Hkv * (kv->page_size / kTileTok) >= (1LL << 31))
+    return HSA_ERR_UNSUPPORTED;                          // tile numbers are 32-bit
   for (int b = 0; b < kv->B; ++b)
     if (kv->seq_lens_host[b] < 0 || kv->seq_lens_host[b] > tmax) return HSA_ERR_CAPACITY;
   return HSA_OK;
@@ -108,7 +110,7 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
     st = check_cu(cu, cu_host, kv->B, &most);
     if (st != HSA_OK) return st;
     n_rows = cu_host[kv->B];
-    if (static_cast<long long>(most) * (kv->Hq / kv->Hkv) >= (1LL << 30)) return HSA_ERR_UNSUPPORTED;
+    if (static_cast<long long>(most) * (kv->Hq / kv->Hkv) >= (1LL << 25)) return HSA_ERR_UNSUPPORTED;   // token_of
   }
   const long long e = elem_bytes(dtype);
   if (!aligned(q, 16) || !aligned(out, 16) || (lse && !aligned(lse, 4)) || q_stride * e % 16) return HSA_ERR_ALIGNMENT;
@@ -129,17 +131,21 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   p.causal = causal;
   p.window = window;
   p.G = kv->Hq / kv->Hkv;
+  p.inv_G = static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G);   // not used for G = 1
   p.scale = scale;
   const int rows = kv4_attend_rows(dtype, most * p.G);
-  long long tiles = 0;   // of all units: the kernels take equal shares of them
+  long long steps = 0, units = 0;   // the kernel's warps take equal shares of all units' steps
+  const int step = kv4_attend_step_tokens();
   for (int b = 0; b < kv->B; ++b) {
     const long long T = kv->seq_lens_host[b], n = cu_host ? cu_host[b + 1] - cu_host[b] : 1;
     if (n == 0) continue;
-    const long long lo = window > 0 ? std::max(0ll, T - n - window + 1) / kTileTok : 0;
-    tiles += ((T + kTileTok - 1) / kTileTok - lo) * ((n * p.G + rows - 1) / rows) * kv->Hkv;
+    const long long lo = window > 0 ? std::max(0ll, T - n - window + 1) / step : 0;
+    const long long u = (n * p.G + rows - 1) / rows * kv->Hkv;
+    steps += ((T + step - 1) / step - lo) * u;
+    units += u;
   }
-  return launch_kv4_attend(dtype, rows, p, sms, tiles, most * p.G, stream, pdl_enabled()) == cudaSuccess ? HSA_OK
-                                                                                                       : HSA_ERR_CUDA;
+  const cudaError_t err = launch_kv4_attend(dtype, rows, p, sms, steps, units, most * p.G, stream, pdl_enabled());
+  return err == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
 }
 
 }  // namespace

@@ -1,14 +1,17 @@
 // Attention over the 4-bit KV cache for few query rows a KV head (decode, verification of
-// drafted tokens): every warp streams 16-token tiles through registers and joins its rows'
-// online softmax states at the end.
+// drafted tokens): every warp streams tiles through registers and keeps its rows' online
+// softmax state to the end of its share.
 //
-// Work. A unit is (sequence, KV head, tile of query rows); its tokens are 16-token tiles. All
-// units' tiles lie on one line, in the order of (sequence, head, row tile), and every block
-// takes an equal share of that line, so long and short sequences load the blocks alike. A
-// block works through its share unit by unit (a segment each), its warps taking the
-// segment's tiles in turn. A unit that lies within one block's share is finished there; of
-// one that does not, each block leaves a partial (m, l, acc) in the workspace, two slots a
-// block, and the merge kernel joins them. Shares follow from the device lengths alone.
+// Work. A unit is (sequence, KV head, tile of query rows); its tokens are steps of two
+// 16-token tiles. All units' steps lie on one line, in the order of (sequence, head, row
+// tile). Every block takes an equal share of that line and every warp of it an equal share
+// of that, so long and short sequences load all warps alike and no barrier stands between
+// two units. A warp works through its share unit by unit (a segment each). Units that lie
+// within one warp's share are finished there. Of the others a warp has at most two, its
+// first and its last: the first goes to a slot in the workspace, the last to shared memory,
+// and after the block's only barrier its warps join them. Units that cross blocks leave one
+// partial (m, l, acc) a block, and the merge kernel joins those. Shares follow from the
+// device lengths alone.
 //
 // Mathematics of a tile, on mma.sync m16n8k16 (fp16 in, fp32 sums): S^T = K q^T with the 16
 // tokens as rows and 8 query rows as columns, P = 2^(S f - ref), O^T += V^T P with dims as
@@ -18,8 +21,9 @@
 // and P likewise, so that 32-bit calls keep 32-bit accuracy. With at most four 32-bit rows hi
 // and lo share one fragment (columns 0-3 and 4-7).
 //
-// ref is the row's largest logit so far, up to a growth of 2^kGrow that does not yet move it:
-// P <= 2^(kHead + kGrow) < 65504 and below 2^(kHead - 24) of the largest it is lost.
+// ref is the row's largest logit so far less kHead; it moves when a logit exceeds it by
+// kHead + kGrow, so P <= 2^(kHead + kGrow) < 65504, and a weight below 2^(-24 - kHead) of the
+// largest is lost.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -30,11 +34,12 @@
 namespace pqhsa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 4;          // tiles in flight a warp
+constexpr int kStep = 2;            // tiles a step
+constexpr int kStepTok = kStep * kTileTok;
+constexpr int kStepBytes = kStep * kTileBytes;
 constexpr float kHead = 11.f, kGrow = 4.f;
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
+constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kPitch = kD + 4;      // floats a row of a warp's partial in shared memory
 
 enum Mode { kHi, kHiLo, kPack };
@@ -43,11 +48,16 @@ template <int NR, Mode M>
 struct Shape {
   static constexpr int RT = M == kPack ? 4 : 8 * NR;             // query rows of a unit
   static constexpr int QF = NR * (M == kHiLo ? 2 : 1);           // q fragments
-  static constexpr bool q_smem = NR > 1;
-  static constexpr size_t ring = static_cast<size_t>(kWarps) * kStages * kTileBytes;
-  static constexpr size_t part = static_cast<size_t>(kWarps) * RT * (kPitch + 2) * sizeof(float);
+  static constexpr bool q_smem = NR > 1;                         // in shared memory, a set a warp
+  static constexpr int warps = NR == 1 ? 16 : 8;                 // one block an SM: 128 or 255 registers a thread
+  static constexpr int stages = NR == 1 ? 3 : 4;
+  static constexpr size_t ring = static_cast<size_t>(stages) * kStepBytes;      // a warp's
+  static constexpr size_t part = static_cast<size_t>(RT) * (kPitch + 2) * sizeof(float);
+  static_assert(part <= ring, "a warp's last partial lies over its ring");
   static constexpr size_t qbytes = q_smem ? static_cast<size_t>(QF) * 8 * 32 * 8 : 0;
-  static constexpr size_t total = ring + part + qbytes;
+  static constexpr size_t total = warps * (ring + qbytes);
+  static_assert(total + 2048 <= 227 * 1024, "shared memory of a block");
+  static_assert(2 * warps <= 32, "a lane for each segment that is joined");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -70,12 +80,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 }
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 
-// ---- shares of the line of tiles ---------------------------------------------
+// ---- shares of the line of steps ---------------------------------------------
 
 struct Seq {
   int T, n, r0;          // tokens, query tokens, first query token's row
-  int lo, nt, nrt;       // first tile, tiles, row tiles
-  long long count;       // tiles on the line
+  int lo, nt, nrt;       // first step, steps, row tiles
+  long long count;       // steps on the line
 };
 
 __device__ __forceinline__ Seq sequence(const Kv4AttendParams& p, int b, int RT) {
@@ -86,44 +96,86 @@ __device__ __forceinline__ Seq sequence(const Kv4AttendParams& p, int b, int RT)
   s.n = max(0, min(s.n, p.n_rows - s.r0));
   if (s.r0 < 0) s.n = 0;
   const long long first = static_cast<long long>(s.T) - s.n - p.window + 1;   // leftmost position of a window
-  s.lo = p.window > 0 && first > 0 ? static_cast<int>(first / kTileTok) : 0;
-  const int hi = (s.T + kTileTok - 1) / kTileTok;
+  s.lo = p.window > 0 && first > 0 ? static_cast<int>(first / kStepTok) : 0;
+  const int hi = (s.T + kStepTok - 1) / kStepTok;
   s.nt = s.n > 0 ? hi - s.lo : 0;
   s.nrt = (s.n * p.G + RT - 1) / RT;
   s.count = static_cast<long long>(s.nt) * s.nrt * p.c.Hkv;
   return s;
 }
 
-// Tiles of all sequences, by a whole warp; before: tiles of the sequences before `b`.
-__device__ __forceinline__ long long line_length(const Kv4AttendParams& p, int RT, int b, long long* before) {
-  const int lane = threadIdx.x & 31;
-  long long all = 0, head = 0;
-  for (int i = lane; i < p.c.B; i += 32) {
-    const long long n = sequence(p, i, RT).count;
-    all += n;
-    if (i < b) head += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, o);
-    head += __shfl_xor_sync(0xffffffffu, head, o);
-  }
-  *before = head;
-  return all;
+// Query token and head of the group of a query row; p.inv_G = ceil(2^32 / G), exact for rows below 2^25.
+__device__ __forceinline__ int token_of(const Kv4AttendParams& p, int row) {
+  return p.G == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.inv_G));
+}
+__device__ __forceinline__ size_t head_row(const Kv4AttendParams& p, int r0, int h, int qrow) {
+  const int i = token_of(p, qrow);
+  return (static_cast<size_t>(r0) + i) * p.c.Hq + static_cast<size_t>(h) * p.G + (qrow - i * p.G);
 }
 
-// Sequence that holds tile g of the line and the tiles before it, by a whole warp.
+// Quotient of numbers that hardly ever need 64 bits.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
+// The line of all steps and its equal shares: the first `rest` blocks take one step more.
+struct Line {
+  long long W, each, rest;
+  int N;
+  __device__ __forceinline__ Line(long long w, int blocks) : W(w) {
+    N = static_cast<int>(min(static_cast<long long>(blocks), w));
+    each = N > 0 ? quotient(w, N) : 0;
+    rest = w - each * N;
+  }
+  __device__ __forceinline__ long long begin(int c) const { return each * c + min(static_cast<long long>(c), rest); }
+  __device__ __forceinline__ int block_of(long long g) const {
+    const long long big = rest * (each + 1);
+    return static_cast<int>(g < big ? quotient(g, each + 1) : rest + quotient(g - big, each));
+  }
+};
+
+// Inclusive sum over the lanes of a warp.
+__device__ __forceinline__ long long lane_sums(long long n) {
+  const int lane = threadIdx.x & 31;
+  if (__all_sync(0xffffffffu, n < (1 << 26))) {
+    int x = static_cast<int>(n);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) n += y;
+  }
+  return n;
+}
+
+// Steps of all sequences, and of those before sequence b, by a whole warp.
+__device__ __forceinline__ long long line_length(const Kv4AttendParams& p, int RT, int b, long long* before) {
+  const int lane = threadIdx.x & 31;
+  long long base = 0;
+  *before = 0;
+  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+    const long long n = b0 + lane < p.c.B ? sequence(p, b0 + lane, RT).count : 0;
+    const long long x = lane_sums(n);
+    if (b >= b0 && b < b0 + 32) *before = base + __shfl_sync(0xffffffffu, x - n, b - b0);
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+  return base;
+}
+
+// Sequence that holds step g of the line and the steps before it, by a whole warp.
 __device__ __forceinline__ int locate(const Kv4AttendParams& p, int RT, long long g, long long* before) {
   const int lane = threadIdx.x & 31;
   long long base = 0;
   for (int b0 = 0; b0 < p.c.B; b0 += 32) {
     const long long n = b0 + lane < p.c.B ? sequence(p, b0 + lane, RT).count : 0;
-    long long x = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
+    const long long x = lane_sums(n);
     const unsigned past = __ballot_sync(0xffffffffu, base + x > g);
     if (past) {
       const int l = __ffs(past) - 1;
@@ -136,10 +188,8 @@ __device__ __forceinline__ int locate(const Kv4AttendParams& p, int RT, long lon
   return p.c.B;
 }
 
-__device__ __forceinline__ long long share_begin(long long W, int N, int c) { return W * c / N; }
-__device__ __forceinline__ int share_of(long long W, int N, long long g) {
-  return static_cast<int>(((g + 1) * N - 1) / W);
-}
+// 2^e for e in [-126, 127].
+__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 
 template <typename T>
 __device__ __forceinline__ void store_out(uint8_t* out, size_t at, float4 v);
@@ -212,245 +262,317 @@ __device__ __forceinline__ void load_q32<__half>(const uint8_t* row, float* x) {
   }
 }
 
+// A segment that is joined with others of its unit.
+struct Segment {
+  int unit, b;           // unit: row tile and head, -1: none
+  int h, r0, row0, rows; // head, first query token's row, first and number of query rows
+  int open;              // bits: begins at its unit's first step, ends at its last, begins the block
+};
+
 template <typename T, int NR, Mode M>
-__global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1) kv4_attend_kernel(Kv4AttendParams p) {
+__global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel(Kv4AttendParams p) {
   using S = Shape<NR, M>;
   constexpr int RT = S::RT;
+  constexpr int kWarps = S::warps;
+  constexpr int kSlot = RT * (kD + 2);             // floats of a slot in the workspace
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ Segment segs[2 * kWarps];             // a warp's first and last
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + static_cast<size_t>(warp) * kStages * kTileBytes;
-  float* part = reinterpret_cast<float*>(smem + S::ring);
-  float* part_m = part + kWarps * RT * kPitch;        // [warp][RT]
-  float* part_l = part_m + kWarps * RT;
-  uint2* qs = reinterpret_cast<uint2*>(smem + S::ring + S::part);   // [fragment][8][lane]
+  uint8_t* ring = smem + warp * S::ring;
+  uint2* qs = reinterpret_cast<uint2*>(smem + kWarps * S::ring + warp * S::qbytes);   // [fragment][8][lane]
+  if (lane < 2) segs[2 * warp + lane].unit = -1;
+  __syncwarp();
 
   pdl_wait();
   pdl_launch_dependents();
 
-  long long before = 0;
-  const long long W = line_length(p, RT, 0, &before);
-  const int N = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
-  if (static_cast<int>(blockIdx.x) >= N) return;
-  long long g = share_begin(W, N, blockIdx.x);
-  const long long g_end = share_begin(W, N, blockIdx.x + 1);
-  int b = locate(p, RT, g, &before);
-  Seq s = sequence(p, b, RT);
-  bool first_segment = true;
+  // ---- this block's and this warp's share of the line ----
+  Seq s = {};
+  long long before = 0, W, sums = 0;
+  const bool few = p.c.B <= 32;                    // one sequence a lane, read once
+  if (few) {
+    if (lane < p.c.B) s = sequence(p, lane, RT);
+    sums = lane_sums(s.count);
+    W = __shfl_sync(0xffffffffu, sums, 31);
+  } else {
+    W = line_length(p, RT, 0, &before);
+  }
+  const Line line(W, gridDim.x);
+  if (static_cast<int>(blockIdx.x) >= line.N) return;
+  const long long block_g = line.begin(blockIdx.x);
+  const int block_len = static_cast<int>(line.begin(blockIdx.x + 1) - block_g);
+  long long g = block_g + static_cast<long long>(block_len) * warp / kWarps;
+  const long long g_end = block_g + static_cast<long long>(block_len) * (warp + 1) / kWarps;
+  float* first_slot = p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * kWarps + warp) * kSlot;
 
-  while (g < g_end) {
-    while (g - before >= s.count) {   // next sequence with work
-      before += s.count;
-      s = sequence(p, ++b, RT);
+  if (g < g_end) {
+    int b;
+    if (few) {
+      b = __ffs(__ballot_sync(0xffffffffu, sums > g)) - 1;
+      before = __shfl_sync(0xffffffffu, sums - s.count, b);
+      s.T = __shfl_sync(0xffffffffu, s.T, b);
+      s.n = __shfl_sync(0xffffffffu, s.n, b);
+      s.r0 = __shfl_sync(0xffffffffu, s.r0, b);
+      s.lo = __shfl_sync(0xffffffffu, s.lo, b);
+      s.nt = __shfl_sync(0xffffffffu, s.nt, b);
+      s.nrt = __shfl_sync(0xffffffffu, s.nrt, b);
+      s.count = __shfl_sync(0xffffffffu, s.count, b);
+    } else {
+      b = locate(p, RT, g, &before);
+      s = sequence(p, b, RT);
     }
-    const long long in_seq = g - before;
-    const int unit = static_cast<int>(in_seq / s.nt);          // h * nrt + row tile
-    const int a = static_cast<int>(in_seq % s.nt);             // first tile of the segment
-    const int len = static_cast<int>(min(static_cast<long long>(s.nt - a), g_end - g));
-    const int h = unit / s.nrt, rt = unit % s.nrt;
-    const int rows = min(RT, s.n * p.G - rt * RT);             // valid query rows
-
-    // ---- query fragments and the bounds of each of this lane's columns ----
-    uint32_t qf[S::q_smem ? 1 : S::QF][16];
-    float f[2 * NR];
-    int hi[2 * NR], lo[2 * NR];
-    if (S::q_smem) __syncthreads();   // the last segment's fragments have been read
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-      const int col = M == kPack ? (r & 3) : nt * 8 + r;
-      float x[32];
-      float top = 0.f;
-      if (col < rows) {
-        const int row = rt * RT + col;
-        load_q32<T>(p.q + (static_cast<long long>(s.r0) + row / p.G) * p.q_tok +
-                        (static_cast<size_t>(h) * p.G + row % p.G) * kD * sizeof(T) + t * 32 * sizeof(T),
-                    x);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = 0.f;
+    while (g < g_end && b < p.c.B) {
+      if (g - before >= s.count) {   // next sequence with work
+        before += s.count;
+        if (++b < p.c.B) s = sequence(p, b, RT);
+        continue;
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = top > 0.f && top < INFINITY ? ilogbf(top) + 1 : 0;
+      const long long in_seq = g - before;
+      const int unit = static_cast<int>(quotient(in_seq, s.nt));                    // h * nrt + row tile
+      const int a = static_cast<int>(in_seq - static_cast<long long>(unit) * s.nt); // first step of the segment
+      const int len = static_cast<int>(min(static_cast<long long>(s.nt - a), g_end - g));
+      const int h = s.nrt == 1 ? unit : unit / s.nrt, rt = unit - h * s.nrt;
+      const int row0 = rt * RT;
+      const int rows = min(RT, s.n * p.G - row0);                // valid query rows
+
+      // ---- copies: stages - 1 steps ahead, tile numbers 16 steps ahead ----
+      const int tile0 = (s.lo + a) * kStep;
+      const int last_tile = (s.T - 1) / kTileTok;
+      int where = -1;               // lane: tile of the cache that holds tile0 + 32 * batch + lane
+      unsigned missing = 0;         // two bits a stage: its tiles that have no page, or lie past the end
+      auto issue = [&](int i) {
+        if (i < len) {
+          if ((i & 15) == 0) {
+            const int tl = tile0 + i * kStep + lane;
+            where = -1;
+            if (tl < tile0 + len * kStep && tl <= last_tile) {
+              const int page = kv4_page(p.c, b, tl);
+              if (page >= 0) where = static_cast<int>(kv4_tile_index(p.c, page, h, tl));
+            }
+          }
+          const int st = i % S::stages;
+          missing &= ~(3u << (2 * st));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float x0 = scalbnf(x[2 * i], -e), x1 = scalbnf(x[2 * i + 1], -e);
-        const uint32_t hi2 = pack_f16x2(x0, x1);
-        uint32_t lo2 = 0u;
-        if (M != kHi) {
-          const float2 back = unpack_f16x2(hi2);
-          lo2 = pack_f16x2(x0 - back.x, x1 - back.y);
+          for (int u = 0; u < kStep; ++u) {
+            const int w = __shfl_sync(0xffffffffu, where, (i * kStep + u) & 31);
+            if (w >= 0) {
+              const uint8_t* src = p.c.cache + static_cast<size_t>(static_cast<uint32_t>(w)) * kTileBytes + lane * 16;
+              uint8_t* dst = ring + st * kStepBytes + u * kTileBytes + lane * 16;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) cp_async_16(dst + j * 512, src + j * 512);
+              if (lane < 16) cp_async_16(dst + kOffScale, src + kOffScale);
+            } else {
+              missing |= 1u << (2 * st + u);
+            }
+          }
         }
-        const uint32_t v = M == kPack && r >= 4 ? lo2 : hi2;
-        if (S::q_smem) {
-          if (warp == 0) {
+        cp_async_commit();
+      };
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < S::stages - 1; ++i) issue(i);
+
+      // ---- query fragments and the bounds of each of this lane's columns ----
+      uint32_t qf[S::q_smem ? 1 : S::QF][16];
+      float f[2 * NR];
+      int hi[2 * NR], lo[2 * NR];
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt) {
+        const int col = M == kPack ? (r & 3) : nt * 8 + r;
+        float x[32];
+        float top = 0.f;
+        if (col < rows) {
+          const int i = token_of(p, row0 + col);
+          load_q32<T>(p.q + (static_cast<long long>(s.r0) + i) * p.q_tok +
+                          (static_cast<size_t>(h) * p.G + (row0 + col - i * p.G)) * kD * sizeof(T) + t * 32 * sizeof(T),
+                      x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0.f;
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e > top >= 2^(e - 1) for normal numbers; out of range or not finite: as it is
+        int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
+        e = e > 126 ? 0 : max(e, -126);
+        const float down = pow2i(-e);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float x0 = x[2 * i] * down, x1 = x[2 * i + 1] * down;
+          const uint32_t hi2 = pack_f16x2(x0, x1);
+          uint32_t lo2 = 0u;
+          if (M != kHi) {
+            const float2 back = unpack_f16x2(hi2);
+            lo2 = pack_f16x2(x0 - back.x, x1 - back.y);
+          }
+          const uint32_t v = M == kPack && r >= 4 ? lo2 : hi2;
+          if (S::q_smem) {
             reinterpret_cast<uint32_t*>(qs + ((M == kHiLo ? 2 * nt : nt) * 8 + i / 2) * 32 + lane)[i & 1] = v;
             if (M == kHiLo) reinterpret_cast<uint32_t*>(qs + ((2 * nt + 1) * 8 + i / 2) * 32 + lane)[i & 1] = lo2;
+          } else {
+            qf[0][i] = v;
+            if (M == kHiLo) qf[S::QF - 1][i] = lo2;
           }
-        } else {
-          qf[0][i] = v;
-          if (M == kHiLo) qf[S::QF - 1][i] = lo2;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int mine = M == kPack ? ((2 * t + j) & 3) : 2 * t + j;
+          const int ec = __shfl_sync(0xffffffffu, e, 4 * mine);
+          const int c = nt * 8 + mine;
+          // never so small that a masked logit, -inf times f, is NaN; logits under 2^-80 are as good as 0
+          const float fc = p.scale * kLog2e * pow2i(ec);
+          f[2 * nt + j] = fabsf(fc) < 1e-36f ? copysignf(1e-36f, fc) : fc;
+          const int pos = s.T - s.n + token_of(p, row0 + c);
+          hi[2 * nt + j] = c >= rows ? -1 : p.causal ? pos : s.T - 1;
+          lo[2 * nt + j] = p.window > 0 ? pos - p.window + 1 : 0;
         }
       }
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int mine = M == kPack ? ((2 * t + j) & 3) : 2 * t + j;
-        const int ec = __shfl_sync(0xffffffffu, e, 4 * mine);
-        const int c = nt * 8 + mine;
-        f[2 * nt + j] = scalbnf(p.scale * kLog2e, ec);
-        const int pos = s.T - s.n + (rt * RT + c) / p.G;
-        hi[2 * nt + j] = c >= rows ? -1 : p.causal ? pos : s.T - 1;
-        lo[2 * nt + j] = p.window > 0 ? pos - p.window + 1 : 0;
-      }
-    }
-    if (S::q_smem) __syncthreads();
-    // positions that every row of the unit sees
-    const int all_hi = p.causal ? s.T - s.n + (rt * RT) / p.G : s.T - 1;
-    const int all_lo = p.window > 0 ? s.T - s.n + (rt * RT + rows - 1) / p.G - p.window + 1 : 0;
+      // positions that every row of the unit sees
+      const int all_hi = p.causal ? s.T - s.n + token_of(p, row0) : s.T - 1;
+      const int all_lo = p.window > 0 ? s.T - s.n + token_of(p, row0 + rows - 1) - p.window + 1 : 0;
 
-    // ---- tiles: copies run kStages ahead, page numbers 32 tiles ahead ----
-    const int mine = len > warp ? (len - warp + kWarps - 1) / kWarps : 0;   // this warp's tiles
-    const int tile0 = s.lo + a + warp;
-    int pages = -1;
-    unsigned missing = 0;                                          // stages whose tile has no page
-    auto issue = [&](int i) {
-      if (i < mine) {
-        if ((i & 31) == 0 && i + lane < mine) pages = kv4_page(p.c, b, tile0 + (i + lane) * kWarps);
-        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-        missing = (missing & ~(1u << (i % kStages))) | (page < 0 ? 1u << (i % kStages) : 0u);
-        if (page >= 0) {
-          const uint8_t* src = p.c.cache + kv4_tile_offset(p.c, page, h, tile0 + i * kWarps);
-          uint8_t* dst = ring + (i % kStages) * kTileBytes;
+      float o[NR][8][4];
+      float ref[2 * NR], l[2 * NR];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) cp_async_16(dst + j * 512 + lane * 16, src + j * 512 + lane * 16);
-          if (lane < 16) cp_async_16(dst + kOffScale + lane * 16, src + kOffScale + lane * 16);
-        }
+      for (int j = 0; j < 2 * NR; ++j) {
+        ref[j] = -1e30f;
+        l[j] = 0.f;
       }
-      cp_async_commit();
-    };
-    float o[NR][8][4];
-    float ref[2 * NR], l[2 * NR];
-#pragma unroll
-    for (int j = 0; j < 2 * NR; ++j) {
-      ref[j] = -1e30f;
-      l[j] = 0.f;
-    }
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-
-    for (int i = 0; i < kStages - 1; ++i) issue(i);
-    for (int i = 0; i < mine; ++i) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      const bool present = !((missing >> (i % kStages)) & 1u);
-      issue(i + kStages - 1);
-      const uint8_t* tile = ring + (i % kStages) * kTileBytes;
-      const int pos = (tile0 + i * kWarps) * kTileTok;
-      const uint4 k0 = reinterpret_cast<const uint4*>(tile)[lane];
-      const uint4 k1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
-      const uint4 v0 = reinterpret_cast<const uint4*>(tile + kOffV)[lane];
-      const uint4 v1 = reinterpret_cast<const uint4*>(tile + kOffV + 512)[lane];
-      const uint2 sc = reinterpret_cast<const uint2*>(tile + kOffScale)[lane];
-      // ---- S^T = K q^T ----
-      float sacc[NR][4];
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sacc[nt][j] = 0.f;
-      {
-        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+        for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t x[4], y[4];
-          e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
-          e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
-          const uint32_t s0 = scale_both(sc.x, w >> 1), s1 = scale_both(sc.x, 2 + (w >> 1));
+          for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
+
+#pragma unroll 1
+      for (int i = 0; i < len; ++i) {
+        cp_async_wait<S::stages - 2>();
+        __syncwarp();
+        const int st = i % S::stages;
+        const unsigned absent = (missing >> (2 * st)) & 3u;
+        issue(i + S::stages - 1);
+        const uint8_t* stage = ring + st * kStepBytes;
+        const int pos = (tile0 + i * kStep) * kTileTok;
+        // ---- S^T = K q^T ----
+        float sacc[kStep][NR][4];
+        uint2 sc[kStep];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = hmul2(x[j], s0);
-            y[j] = hmul2(y[j], s1);
+        for (int u = 0; u < kStep; ++u) {
+          const uint8_t* tile = stage + u * kTileBytes;
+          const uint4 k0 = reinterpret_cast<const uint4*>(tile)[lane];
+          const uint4 k1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
+          sc[u] = reinterpret_cast<const uint2*>(tile + kOffScale)[lane];
+          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+          for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sacc[u][nt][j] = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t x[4], y[4];
+            e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
+            e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
+            const uint32_t s0 = scale_both(sc[u].x, w >> 1), s1 = scale_both(sc[u].x, 2 + (w >> 1));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[j] = hmul2(x[j], s0);
+              y[j] = hmul2(y[j], s1);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+              const int i8 = 2 * w + kk;
+#pragma unroll
+              for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+                for (int part_q = 0; part_q < (M == kHiLo ? 2 : 1); ++part_q) {
+                  const int fr = M == kHiLo ? 2 * nt + part_q : nt;
+                  uint2 bq;
+                  if (S::q_smem) bq = qs[(fr * 8 + i8) * 32 + lane];
+                  else bq = make_uint2(qf[S::q_smem ? 0 : fr][2 * i8], qf[S::q_smem ? 0 : fr][2 * i8 + 1]);
+                  mma_f16_16816(sacc[u][nt], x[2 * kk], y[2 * kk], x[2 * kk + 1], y[2 * kk + 1], bq.x, bq.y);
+                }
+              }
+            }
           }
+          if (M == kPack) {
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
-            const int i8 = 2 * w + kk;
+            for (int j = 0; j < 4; ++j) sacc[u][0][j] += __shfl_xor_sync(0xffffffffu, sacc[u][0][j], 2);
+          }
+        }
+        // ---- masks ----
+        uint32_t vs[kStep][2];
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt) {
+        for (int u = 0; u < kStep; ++u) {
+          vs[u][0] = scale_pair(sc[u].y, 0);
+          vs[u][1] = scale_pair(sc[u].y, 2);
+        }
+        const bool whole = absent == 0u && pos + kStepTok - 1 <= all_hi && pos >= all_lo;
+        if (!whole) {
 #pragma unroll
-              for (int part_q = 0; part_q < (M == kHiLo ? 2 : 1); ++part_q) {
-                const int fr = M == kHiLo ? 2 * nt + part_q : nt;
-                uint2 bq;
-                if (S::q_smem) bq = qs[(fr * 8 + i8) * 32 + lane];
-                else bq = make_uint2(qf[S::q_smem ? 0 : fr][2 * i8], qf[S::q_smem ? 0 : fr][2 * i8 + 1]);
-                mma_f16_16816(sacc[nt], x[2 * kk], y[2 * kk], x[2 * kk + 1], y[2 * kk + 1], bq.x, bq.y);
+          for (int u = 0; u < kStep; ++u) {
+            const int pu = pos + u * kTileTok;
+            const bool present = !((absent >> u) & 1u);
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int tp = pu + r + 8 * (j >> 1), c = 2 * nt + (j & 1);
+                // times f it is -inf, whatever f's sign
+                if (tp > hi[c] || tp < lo[c] || !present) sacc[u][nt][j] = f[c] < 0.f ? INFINITY : -INFINITY;
+              }
+            // A zero weight must not meet a NaN or an infinity: tokens past the end hold anything.
+            const int left = present ? s.T - (pu + 2 * t) : 0;   // tokens from this lane's first on
+            vs[u][0] &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+            vs[u][1] &= (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+            // Values that are not finite count for the rows that see their token, and for no other:
+            // taken out of the product, and added as NaN to those rows' sums of the block's dims.
+            const unsigned bad = ((vs[u][0] & 0x7c00u) == 0x7c00u ? 1u : 0u) |
+                                 ((vs[u][0] & 0x7c000000u) == 0x7c000000u ? 2u : 0u) |
+                                 ((vs[u][1] & 0x7c00u) == 0x7c00u ? 256u : 0u) |
+                                 ((vs[u][1] & 0x7c000000u) == 0x7c000000u ? 512u : 0u);
+            if (__any_sync(0xffffffffu, bad != 0u)) {
+              vs[u][0] &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
+              vs[u][1] &= (bad & 256u ? 0u : 0xffffu) | (bad & 512u ? 0u : 0xffff0000u);
+              unsigned all = bad << (2 * t);                       // bit: token of the tile
+              all |= __shfl_xor_sync(0xffffffffu, all, 1);
+              all |= __shfl_xor_sync(0xffffffffu, all, 2);
+#pragma unroll
+              for (int c = 0; c < 2 * NR; ++c) {
+                const int from = max(0, lo[c] - pu), to = min(kTileTok - 1, hi[c] - pu);
+                const bool seen = from <= to && (all & ((2u << to) - (1u << from))) != 0u;
+#pragma unroll
+                for (int i8 = 0; i8 < 8; ++i8) {
+                  if (seen) o[c >> 1][i8][c & 1] = o[c >> 1][i8][(c & 1) + 2] = __int_as_float(0x7fffffff);
+                }
               }
             }
           }
         }
-      }
-      if (M == kPack) {
+        // ---- online softmax: weights 2^(s f - ref) ----
+        float y[kStep][NR][4], top = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sacc[0][j] += __shfl_xor_sync(0xffffffffu, sacc[0][j], 2);
-      }
-      // ---- logits in log2 units, masks ----
-      const bool whole = present && pos + kTileTok - 1 <= all_hi && pos >= all_lo;
-      uint32_t vs0 = scale_pair(sc.y, 0), vs1 = scale_pair(sc.y, 2);
+        for (int u = 0; u < kStep; ++u)
 #pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
+          for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sacc[nt][j] *= f[2 * nt + (j & 1)];
-      if (!whole) {
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int tp = pos + r + 8 * (j >> 1), c = 2 * nt + (j & 1);
-            if (tp > hi[c] || tp < lo[c] || !present) sacc[nt][j] = -INFINITY;
-          }
-        // A zero weight must not meet a NaN or an infinity: tokens past the end hold anything.
-        const int left = present ? s.T - (pos + 2 * t) : 0;   // tokens from this lane's first on
-        vs0 &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-        vs1 &= (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
-        // Values that are not finite count for the rows that see their token, and for no other:
-        // taken out of the product, and added as NaN to those rows' sums of the block's dims.
-        const unsigned bad = ((vs0 & 0x7c00u) == 0x7c00u ? 1u : 0u) | ((vs0 & 0x7c000000u) == 0x7c000000u ? 2u : 0u) |
-                             ((vs1 & 0x7c00u) == 0x7c00u ? 256u : 0u) | ((vs1 & 0x7c000000u) == 0x7c000000u ? 512u : 0u);
-        if (__any_sync(0xffffffffu, bad != 0u)) {
-          vs0 &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
-          vs1 &= (bad & 256u ? 0u : 0xffffu) | (bad & 512u ? 0u : 0xffff0000u);
-          unsigned all = bad << (2 * t);                       // bit: token of the tile
-          all |= __shfl_xor_sync(0xffffffffu, all, 1);
-          all |= __shfl_xor_sync(0xffffffffu, all, 2);
+            for (int j = 0; j < 4; ++j) {
+              // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
+              sacc[u][nt][j] = __fmul_rn(sacc[u][nt][j], f[2 * nt + (j & 1)]);
+              y[u][nt][j] = __fsub_rn(sacc[u][nt][j], ref[2 * nt + (j & 1)]);
+              top = fmaxf(top, y[u][nt][j]);
+            }
+        if (__any_sync(0xffffffffu, top > kHead + kGrow)) {
 #pragma unroll
           for (int c = 0; c < 2 * NR; ++c) {
-            const int first = max(0, lo[c] - pos), last = min(kTileTok - 1, hi[c] - pos);
-            const bool seen = first <= last && (all & ((2u << last) - (1u << first))) != 0u;
+            float mx = -INFINITY;
 #pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8) {
-              if (seen) o[c >> 1][i8][c & 1] = o[c >> 1][i8][(c & 1) + 2] = __int_as_float(0x7fffffff);
-            }
-          }
-        }
-      }
-      // ---- online softmax ----
-      bool grow = false;
+            for (int u = 0; u < kStep; ++u)
 #pragma unroll
-      for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          grow |= fmaxf(sacc[nt][j], sacc[nt][j + 2]) > ref[2 * nt + j] + (kHead + kGrow);
-      if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int c = 2 * nt + j;
-            float mx = fmaxf(sacc[nt][j], sacc[nt][j + 2]);
+              for (int j = 0; j < 2; ++j) mx = fmaxf(mx, sacc[u][c >> 1][(c & 1) + 2 * j]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -460,128 +582,169 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1) kv4_attend_kernel(K
             l[c] *= shrink;
 #pragma unroll
             for (int i8 = 0; i8 < 8; ++i8) {
-              o[nt][i8][j] *= shrink;
-              o[nt][i8][j + 2] *= shrink;
+              o[c >> 1][i8][c & 1] *= shrink;
+              o[c >> 1][i8][(c & 1) + 2] *= shrink;
+            }
+#pragma unroll
+            for (int u = 0; u < kStep; ++u)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                y[u][c >> 1][(c & 1) + 2 * j] = __fsub_rn(sacc[u][c >> 1][(c & 1) + 2 * j], next);
+          }
+        }
+        // ---- O^T += V^T P ----
+#pragma unroll
+        for (int u = 0; u < kStep; ++u) {
+          uint32_t ph[NR][2], pl[NR][2];
+#pragma unroll
+          for (int nt = 0; nt < NR; ++nt) {
+            float pr[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int c = 2 * nt + (j & 1);
+              pr[j] = fast_exp2(y[u][nt][j]);
+              l[c] += pr[j];
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
+              if (M != kHi) {
+                const float2 back = unpack_f16x2(hi2);
+                const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
+                if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
+                else pl[nt][half] = transpose8x8(lo2);
+              }
+              ph[nt][half] = transpose8x8(hi2);
             }
           }
+          const uint8_t* tile = stage + u * kTileBytes + kOffV;
+          const uint4 v0 = reinterpret_cast<const uint4*>(tile)[lane];
+          const uint4 v1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
+          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t x[4], y[4];
+            e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
+            e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[j] = hmul2(x[j], vs[u][0]);
+              y[j] = hmul2(y[j], vs[u][1]);
+            }
+#pragma unroll
+            for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+              for (int nt = 0; nt < NR; ++nt) {
+                mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
+                              ph[nt][1]);
+                if (M == kHiLo)
+                  mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0],
+                                pl[nt][1]);
+              }
+            }
+          }
+        }
       }
-      uint32_t ph[NR][2], pl[NR][2];
+      cp_async_wait<0>();
+
+      // ---- end of a segment: the result, or a partial to be joined ----
+      const bool done = a == 0 && len == s.nt;
+      const bool last = g + len >= g_end;
+      float* slot = last ? reinterpret_cast<float*>(ring) : first_slot;
+      const int pitch = last ? kPitch : kD;
+      if (!done) __syncwarp();   // the ring has been read
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt) {
-        float pr[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          pr[j] = fast_exp2(sacc[nt][j] - ref[2 * nt + (j & 1)]);
-          l[2 * nt + (j & 1)] += pr[j];
-        }
+        for (int j = 0; j < 2; ++j) {
+          const int c = 2 * nt + j;
+          l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
+          l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
+          l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
+          float v[16];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
-          if (M != kHi) {
-            const float2 back = unpack_f16x2(hi2);
-            const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
-            if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
-            else pl[nt][half] = transpose8x8(lo2);
+          for (int i8 = 0; i8 < 8; ++i8) {
+            v[2 * i8] = o[nt][i8][j];
+            v[2 * i8 + 1] = o[nt][i8][j + 2];
           }
-          ph[nt][half] = transpose8x8(hi2);
-        }
-      }
-      // ---- O^T += V^T P ----
-      {
-        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
+          if (M == kPack) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t x[4], y[4];
-          e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
-          e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = hmul2(x[j], vs0);
-            y[j] = hmul2(y[j], vs1);
+            for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
           }
+          const int col = nt * 8 + 2 * t + j;
+          if (col >= rows) continue;
+          if (done) {
+            const size_t at = head_row(p, s.r0, h, row0 + col);
 #pragma unroll
-          for (int kk = 0; kk < 2; ++kk) {
+            for (int i = 0; i < 4; ++i)
+              finish<T>(p, at, 4 * r + i, ref[c], l[c], make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+          } else {
+            float* row = slot + 2 * RT + col * pitch + 16 * r;
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt) {
-              mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
-                            ph[nt][1]);
-              if (M == kHiLo)
-                mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0],
-                              pl[nt][1]);
+            for (int i = 0; i < 4; ++i)
+              reinterpret_cast<float4*>(row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            if (r == 0) {
+              slot[col] = ref[c];
+              slot[RT + col] = l[c];
             }
           }
         }
       }
-    }
-    cp_async_wait<0>();
-
-    // ---- join the warps ----
-#pragma unroll
-    for (int nt = 0; nt < NR; ++nt) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int c = 2 * nt + j;
-        l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
-        l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
-        l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
-        float v[16];
-#pragma unroll
-        for (int i8 = 0; i8 < 8; ++i8) {
-          v[2 * i8] = o[nt][i8][j];
-          v[2 * i8 + 1] = o[nt][i8][j + 2];
-        }
-        if (M == kPack) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
-        }
-        const int col = nt * 8 + 2 * t + j;
-        if (M != kPack || t < 2) {
-          float* row = part + (warp * RT + col) * kPitch + 16 * r;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<float4*>(row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          if (r == 0) {
-            part_m[warp * RT + col] = ref[c];
-            part_l[warp * RT + col] = l[c];
-          }
-        }
+      if (!done && lane == 0) {
+        segs[2 * warp + (last ? 1 : 0)] =
+            Segment{unit, b, h, s.r0, row0, rows,
+                    (a == 0 ? 1 : 0) | (a + len == s.nt ? 2 : 0) | (g == block_g ? 4 : 0)};
       }
+      g += len;
     }
-    __syncthreads();
-    const bool done = a == 0 && len == s.nt;
-    float* slot = p.parts + static_cast<size_t>(2 * blockIdx.x + (first_segment ? 0 : 1)) * RT * (kD + 2);
-    for (int i = tid; i < rows * 32; i += kThreads) {
-      const int row = i >> 5, d4 = i & 31;
-      float m = -1e30f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, part_m[w * RT + row]);
-      float lt = 0.f;
+  }
+  __syncthreads();
+
+  // ---- join the warps' partials, unit by unit; a warp takes rows warp, warp + kWarps, ... ----
+  for (int e = 0; e < 2 * kWarps;) {
+    const Segment head = segs[e];
+    if (head.unit < 0) {
+      ++e;
+      continue;
+    }
+    // lane i: whether segment i is one of this unit's (they stand together, but for gaps)
+    const bool mine = lane < 2 * kWarps && lane >= e && segs[lane].unit == head.unit && segs[lane].b == head.b;
+    const unsigned set = __ballot_sync(0xffffffffu, mine);
+    const int final = 31 - __clz(set);
+    const bool done = (head.open & 1) && (segs[final].open & 2);
+    const float* slot = lane & 1 ? reinterpret_cast<const float*>(smem + (lane >> 1) * S::ring)
+                                 : p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * kWarps + (lane >> 1)) * kSlot;
+    float* out_slot = p.parts + static_cast<size_t>(2 * blockIdx.x + ((head.open & 5) == 1 ? 1 : 0)) * kSlot;
+    for (int row = warp; row < head.rows; row += kWarps) {
+      const float m1 = mine ? slot[row] : -INFINITY;
+      const float l1 = mine ? slot[RT + row] : 0.f;
+      const float m = warp_max(m1);
+      const float w = mine ? fast_exp2(m1 - m) : 0.f;   // NaN where a row is NaN
+      const float l = warp_sum(w * l1);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float x = fast_exp2(part_m[w * RT + row] - m);
-        const float4 v = *reinterpret_cast<const float4*>(part + (w * RT + row) * kPitch + d4 * 4);
-        lt = fmaf(x, part_l[w * RT + row], lt);
-        acc.x = fmaf(x, v.x, acc.x);
-        acc.y = fmaf(x, v.y, acc.y);
-        acc.z = fmaf(x, v.z, acc.z);
-        acc.w = fmaf(x, v.w, acc.w);
+#pragma unroll 8
+      for (unsigned left = set; left; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        const float* si = i & 1 ? reinterpret_cast<const float*>(smem + (i >> 1) * S::ring) + row * kPitch
+                                : p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * kWarps + (i >> 1)) * kSlot + row * kD;
+        const float4 v = *reinterpret_cast<const float4*>(si + 2 * RT + lane * 4);
+        acc.x = fmaf(wi, v.x, acc.x);
+        acc.y = fmaf(wi, v.y, acc.y);
+        acc.z = fmaf(wi, v.z, acc.z);
+        acc.w = fmaf(wi, v.w, acc.w);
       }
       if (done) {
-        const int qrow = rt * RT + row;
-        const size_t at = (static_cast<size_t>(s.r0) + qrow / p.G) * p.c.Hq + static_cast<size_t>(h) * p.G + qrow % p.G;
-        finish<T>(p, at, d4, m, lt, acc);
+        finish<T>(p, head_row(p, head.r0, head.h, head.row0 + row), lane, m, l, acc);
       } else {
-        if (d4 == 0) {
-          slot[row] = m;
-          slot[RT + row] = lt;
+        if (lane == 0) {
+          out_slot[row] = m;
+          out_slot[RT + row] = l;
         }
-        *reinterpret_cast<float4*>(slot + 2 * RT + row * kD + d4 * 4) = acc;
+        *reinterpret_cast<float4*>(out_slot + 2 * RT + row * kD + lane * 4) = acc;
       }
     }
-    __syncthreads();
-    g += len;
-    first_segment = false;
+    e = final + 1;
   }
 }
 
@@ -589,68 +752,73 @@ __global__ void __launch_bounds__(kThreads, NR == 1 ? 2 : 1) kv4_attend_kernel(K
 // writes the rows of sequences without tokens.
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4AttendParams p, int RT, int blocks) {
-  __shared__ float4 acc_s[kMergeThreads / 32][32];
-  __shared__ float ml_s[2][kMergeThreads / 32];
-  pdl_wait();
+  __shared__ float4 acc_s[kMergeWarps][32];
+  __shared__ float max_s[kMergeWarps], sum_s[kMergeWarps];
+  __shared__ float weight[kKv4MaxSms];
+  static_assert(kKv4MaxSms <= kMergeThreads, "a thread for each part");
+  // Lengths and row offsets may be read at once: the attention kernel lets this one start only after it has
+  // itself waited for all that came before it.
   pdl_launch_dependents();
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Seq s = sequence(p, b, RT);
   const int rows_all = s.n * p.G;                       // query rows of a head
   const int h = blockIdx.x % p.c.Hkv;
   long long before = 0;
-  long long W = -1;
-  int N = 1;
+  const Line line(line_length(p, RT, b, &before), blocks);
+  pdl_wait();
   for (int qrow = blockIdx.x / p.c.Hkv; qrow < rows_all; qrow += gridDim.x / p.c.Hkv) {
-    const size_t at = (static_cast<size_t>(s.r0) + qrow / p.G) * p.c.Hq + static_cast<size_t>(h) * p.G + qrow % p.G;
+    const size_t at = head_row(p, s.r0, h, qrow);
     if (s.nt == 0) {
       if (warp == 0) finish<T>(p, at, lane, 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
       continue;
     }
-    if (W < 0) {
-      W = line_length(p, RT, b, &before);
-      N = static_cast<int>(min(static_cast<long long>(blocks), W));
-    }
     const int rt = qrow / RT, row = qrow % RT;
     const long long u0 = before + (static_cast<long long>(h) * s.nrt + rt) * s.nt;
-    const int c0 = share_of(W, N, u0), c1 = share_of(W, N, u0 + s.nt - 1);
+    const int c0 = line.block_of(u0), c1 = line.block_of(u0 + s.nt - 1);
     if (c0 == c1) continue;
-    const int late = share_begin(W, N, c0) == u0 ? 0 : 1;   // the unit is its first block's last segment
-    float m = -1e30f, l = 0.f;
+    const int late = line.begin(c0) == u0 ? 0 : 1;   // the unit is its first block's last segment
+    const float* slots = p.parts + static_cast<size_t>(2 * c0) * RT * (kD + 2);
+    const int parts = c1 - c0 + 1;                   // at most kKv4MaxSms
+    auto slot_of = [&](int i) { return slots + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * RT * (kD + 2); };
+    float mi = -INFINITY, li = 0.f;
+    if (tid < parts) {
+      mi = slot_of(tid)[row];
+      li = slot_of(tid)[RT + row];
+    }
+    const float wm = warp_max(mi);
+    if (lane == 0) max_s[warp] = wm;
+    __syncthreads();
+    float m = max_s[0];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, max_s[w]);
+    const float x = tid < parts ? fast_exp2(mi - m) : 0.f;
+    if (tid < parts) weight[tid] = x;
+    const float ls = warp_sum(x * li);
+    if (lane == 0) sum_s[warp] = ls;
+    __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = c0 + warp; c <= c1; c += kMergeThreads / 32) {
-      const float* slot = p.parts + static_cast<size_t>(2 * c + (c == c0 ? late : 0)) * RT * (kD + 2);
-      const float mc = slot[row], lc = slot[RT + row];
-      const float4 v = *reinterpret_cast<const float4*>(slot + 2 * RT + row * kD + lane * 4);
-      const float next = fmaxf(m, mc);
-      const float x = fast_exp2(m - next), y = fast_exp2(mc - next);
-      m = next;
-      l = fmaf(l, x, lc * y);
-      acc.x = fmaf(acc.x, x, v.x * y);
-      acc.y = fmaf(acc.y, x, v.y * y);
-      acc.z = fmaf(acc.z, x, v.z * y);
-      acc.w = fmaf(acc.w, x, v.w * y);
+#pragma unroll 5
+    for (int i = warp; i < parts; i += kMergeWarps) {
+      const float4 v = *reinterpret_cast<const float4*>(slot_of(i) + 2 * RT + row * kD + lane * 4);
+      const float y = weight[i];
+      acc.x = fmaf(v.x, y, acc.x);
+      acc.y = fmaf(v.y, y, acc.y);
+      acc.z = fmaf(v.z, y, acc.z);
+      acc.w = fmaf(v.w, y, acc.w);
     }
     acc_s[warp][lane] = acc;
-    if (lane == 0) {
-      ml_s[0][warp] = m;
-      ml_s[1][warp] = l;
-    }
     __syncthreads();
     if (warp == 0) {
-      m = ml_s[0][0];
-#pragma unroll
-      for (int w = 1; w < kMergeThreads / 32; ++w) m = fmaxf(m, ml_s[0][w]);
-      l = 0.f;
+      float l = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kMergeThreads / 32; ++w) {
-        const float x = fast_exp2(ml_s[0][w] - m);
+      for (int w = 0; w < kMergeWarps; ++w) {
         const float4 v = acc_s[w][lane];
-        l = fmaf(x, ml_s[1][w], l);
-        acc.x = fmaf(x, v.x, acc.x);
-        acc.y = fmaf(x, v.y, acc.y);
-        acc.z = fmaf(x, v.z, acc.z);
-        acc.w = fmaf(x, v.w, acc.w);
+        l += sum_s[w];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
       }
       finish<T>(p, at, lane, m, l, acc);
     }
@@ -673,16 +841,16 @@ cudaLaunchConfig_t launch_config(dim3 grid, int threads, size_t smem, cudaStream
 }
 
 template <typename T, int NR, Mode M>
-cudaError_t launch_attend_t(const Kv4AttendParams& p, int sms, long long tiles, int max_rows, cudaStream_t stream,
+cudaError_t launch_attend_t(const Kv4AttendParams& p, int sms, long long steps, long long units, int max_rows, cudaStream_t stream,
                             bool pdl) {
   using S = Shape<NR, M>;
   cudaError_t e = ensure_dyn_smem<kv4_attend_kernel<T, NR, M>>(S::total);
   if (e != cudaSuccess) return e;
-  const long long most = static_cast<long long>(std::min(sms, kKv4MaxSms)) * (NR == 1 ? 2 : 1);
-  // a share of at least one tile a warp
-  const int blocks = static_cast<int>(std::max(1ll, std::min(most, (tiles + kWarps - 1) / kWarps)));
+  const long long most = std::min(sms, kKv4MaxSms);
+  // a share of at least one step a warp, but of no more units than there are SMs for
+  const int blocks = static_cast<int>(std::max(1ll, std::min(most, std::max(units, (steps + S::warps - 1) / S::warps))));
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = launch_config(dim3(blocks), kThreads, S::total, stream, attr, pdl);
+  cudaLaunchConfig_t cfg = launch_config(dim3(blocks), S::warps * 32, S::total, stream, attr, pdl);
   e = cudaLaunchKernelEx(&cfg, kv4_attend_kernel<T, NR, M>, p);
   if (e != cudaSuccess) return e;
   cfg = launch_config(dim3(p.c.Hkv * std::max(1, max_rows), p.c.B), kMergeThreads, 0, stream, attr, pdl);
@@ -690,38 +858,40 @@ cudaError_t launch_attend_t(const Kv4AttendParams& p, int sms, long long tiles, 
 }
 
 template <typename T>
-cudaError_t launch_16(int rows, const Kv4AttendParams& p, int sms, long long tiles, int max_rows, cudaStream_t stream,
+cudaError_t launch_16(int rows, const Kv4AttendParams& p, int sms, long long steps, long long units, int max_rows, cudaStream_t stream,
                       bool pdl) {
   switch (rows) {
-    case 8: return launch_attend_t<T, 1, kHi>(p, sms, tiles, max_rows, stream, pdl);
-    case 16: return launch_attend_t<T, 2, kHi>(p, sms, tiles, max_rows, stream, pdl);
-    case 32: return launch_attend_t<T, 4, kHi>(p, sms, tiles, max_rows, stream, pdl);
+    case 8: return launch_attend_t<T, 1, kHi>(p, sms, steps, units, max_rows, stream, pdl);
+    case 16: return launch_attend_t<T, 2, kHi>(p, sms, steps, units, max_rows, stream, pdl);
+    case 32: return launch_attend_t<T, 4, kHi>(p, sms, steps, units, max_rows, stream, pdl);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
+int kv4_attend_step_tokens() { return kStepTok; }
+
 int kv4_attend_rows(int dtype, int max_rows) {
-  if (dtype == HSA_F32 && max_rows <= 4) return 4;
+  if (dtype == HSA_F32) return max_rows <= 4 ? 4 : max_rows <= 8 ? 8 : 16;
   return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32;
 }
 
-size_t kv4_attend_part_bytes() {   // two slots a block: of 8 rows with two blocks an SM, of up to 32 with one
-  return static_cast<size_t>(2) * kKv4MaxSms * 32 * (kD + 2) * sizeof(float);
+// Two slots a block and one a warp: of 8 rows with 16 warps, of up to 32 with 8.
+size_t kv4_attend_part_bytes() {
+  return static_cast<size_t>(2 + 8) * kKv4MaxSms * 32 * (kD + 2) * sizeof(float);
 }
 
-cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long tiles, int max_rows,
+cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long steps, long long units, int max_rows,
                               cudaStream_t stream, bool pdl) {
   switch (dtype) {
-    case HSA_BF16: return launch_16<__nv_bfloat16>(rows, p, sms, tiles, max_rows, stream, pdl);
-    case HSA_F16: return launch_16<__half>(rows, p, sms, tiles, max_rows, stream, pdl);
+    case HSA_BF16: return launch_16<__nv_bfloat16>(rows, p, sms, steps, units, max_rows, stream, pdl);
+    case HSA_F16: return launch_16<__half>(rows, p, sms, steps, units, max_rows, stream, pdl);
     case HSA_F32:
       switch (rows) {
-        case 4: return launch_attend_t<float, 1, kPack>(p, sms, tiles, max_rows, stream, pdl);
-        case 8: return launch_attend_t<float, 1, kHiLo>(p, sms, tiles, max_rows, stream, pdl);
-        case 16: return launch_attend_t<float, 2, kHiLo>(p, sms, tiles, max_rows, stream, pdl);
-        case 32: return launch_attend_t<float, 4, kHiLo>(p, sms, tiles, max_rows, stream, pdl);
+        case 4: return launch_attend_t<float, 1, kPack>(p, sms, steps, units, max_rows, stream, pdl);
+        case 8: return launch_attend_t<float, 1, kHiLo>(p, sms, steps, units, max_rows, stream, pdl);
+        case 16: return launch_attend_t<float, 2, kHiLo>(p, sms, steps, units, max_rows, stream, pdl);
       }
       return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
