@@ -103,14 +103,20 @@ struct Kv4AttendParams {
   int causal, window, G;
   uint32_t inv_G;             // ceil(2^32 / G)
   float scale;
+  int solo;                   // set by the launcher: no unit crosses blocks
 };
 // Rows (query tokens x heads of a group) of one unit of work; max_rows: the most that a sequence has for one KV head.
 int kv4_attend_rows(int dtype, int max_rows);
 size_t kv4_attend_part_bytes();
-// Steps (of kv4_attend_step_tokens tokens) and units of the whole call.
 int kv4_attend_step_tokens();
-cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long steps, long long units,
-                              int max_rows, cudaStream_t stream, bool pdl);
+// The work of a call: steps of kv4_attend_step_tokens tokens, and units, of all sequences together, the steps of the
+// longest unit, and the most query rows that a sequence has for one KV head.
+struct Kv4Load {
+  long long steps, units, longest;
+  int max_rows;
+};
+cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, const Kv4Load& load, int sms,
+                              cudaStream_t stream, bool pdl);
 
 // api.cu
 int device_sms();      // multiprocessors of the current device, 0 on an error

@@ -39,7 +39,7 @@ hsa_status check_kv4(const hsa_kv4_cache* kv) {
   return HSA_OK;
 }
 
-size_t workspace_bytes() { return align_up(sizeof(WsHeader), 256) + align_up(kv4_attend_part_bytes(), 256); }
+size_t workspace_bytes() { return sizeof(WsHeader) + align_up(kv4_attend_part_bytes(), 256); }
 
 hsa_status check_workspace(const void* ws, size_t bytes) {
   return !ws || !aligned(ws, 256) || bytes < workspace_bytes() ? HSA_ERR_WORKSPACE : HSA_OK;
@@ -126,7 +126,7 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   p.out = static_cast<uint8_t*>(out);
   p.lse = lse;
   p.cu = cu;
-  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + align_up(sizeof(WsHeader), 256));
+  p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
   p.n_rows = n_rows;
   p.causal = causal;
   p.window = window;
@@ -134,17 +134,19 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   p.inv_G = static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G);   // not used for G = 1
   p.scale = scale;
   const int rows = kv4_attend_rows(dtype, most * p.G);
-  long long steps = 0, units = 0;   // the kernel's warps take equal shares of all units' steps
+  Kv4Load load = {0, 0, 0, most * p.G};
   const int step = kv4_attend_step_tokens();
   for (int b = 0; b < kv->B; ++b) {
     const long long T = kv->seq_lens_host[b], n = cu_host ? cu_host[b + 1] - cu_host[b] : 1;
-    if (n == 0) continue;
+    if (n == 0 || T == 0) continue;
     const long long lo = window > 0 ? std::max(0ll, T - n - window + 1) / step : 0;
-    const long long u = (n * p.G + rows - 1) / rows * kv->Hkv;
-    steps += ((T + step - 1) / step - lo) * u;
-    units += u;
+    const long long of_unit = (T + step - 1) / step - lo, units = (n * p.G + rows - 1) / rows * kv->Hkv;
+    load.steps += of_unit * units;
+    load.units += units;
+    load.longest = std::max(load.longest, of_unit);
   }
-  const cudaError_t err = launch_kv4_attend(dtype, rows, p, sms, steps, units, most * p.G, stream, pdl_enabled());
+  if (load.steps >= (1LL << 30)) return HSA_ERR_UNSUPPORTED;
+  const cudaError_t err = launch_kv4_attend(dtype, rows, p, load, sms, stream, pdl_enabled());
   return err == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
 }
 

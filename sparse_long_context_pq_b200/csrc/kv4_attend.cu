@@ -9,9 +9,10 @@
 // two units. A warp works through its share unit by unit (a segment each). Units that lie
 // within one warp's share are finished there. Of the others a warp has at most two, its
 // first and its last: the first goes to a slot in the workspace, the last to shared memory,
-// and after the block's only barrier its warps join them. Units that cross blocks leave one
-// partial (m, l, acc) a block, and the merge kernel joins those. Shares follow from the
-// device lengths alone.
+// and after a barrier the block's warps join them. Units that cross blocks leave one
+// partial (m, l, acc) a block, and the merge kernel joins those. Where whole units load the
+// blocks evenly enough, shares end with units and there is nothing to merge ("solo"). Shares
+// follow from the device lengths alone.
 //
 // Mathematics of a tile, on mma.sync m16n8k16 (fp16 in, fp32 sums): S^T = K q^T with the 16
 // tokens as rows and 8 query rows as columns, P = 2^(S f - ref), O^T += V^T P with dims as
@@ -38,9 +39,11 @@ constexpr int kStep = 2;            // tiles a step
 constexpr int kStepTok = kStep * kTileTok;
 constexpr int kStepBytes = kStep * kTileBytes;
 constexpr float kHead = 11.f, kGrow = 4.f;
+constexpr int kSoloSteps = 32;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kPitch = kD + 4;      // floats a row of a warp's partial in shared memory
+constexpr int kQPitch = 2 * kD + 16; // bytes a row of q in shared memory
 
 enum Mode { kHi, kHiLo, kPack };
 
@@ -49,15 +52,21 @@ struct Shape {
   static constexpr int RT = M == kPack ? 4 : 8 * NR;             // query rows of a unit
   static constexpr int QF = NR * (M == kHiLo ? 2 : 1);           // q fragments
   static constexpr bool q_smem = NR > 1;                         // in shared memory, a set a warp
-  static constexpr int warps = NR == 1 ? 16 : 8;                 // one block an SM: 128 or 255 registers a thread
-  static constexpr int stages = NR == 1 ? 3 : 4;
+  // One block an SM. Its warps: what registers (128 to 255 a thread) and shared memory allow.
+  static constexpr int max_warps = NR == 1 ? 16 : 8;
+  static constexpr int stages = NR == 2 ? 2 : NR == 4 ? 4 : 3;
+  static constexpr int U = 2;                                    // tiles worked on at once
   static constexpr size_t ring = static_cast<size_t>(stages) * kStepBytes;      // a warp's
   static constexpr size_t part = static_cast<size_t>(RT) * (kPitch + 2) * sizeof(float);
   static_assert(part <= ring, "a warp's last partial lies over its ring");
-  static constexpr size_t qbytes = q_smem ? static_cast<size_t>(QF) * 8 * 32 * 8 : 0;
-  static constexpr size_t total = warps * (ring + qbytes);
-  static_assert(total + 2048 <= 227 * 1024, "shared memory of a block");
-  static_assert(2 * warps <= 32, "a lane for each segment that is joined");
+  // q in fp16 [hi, lo][row], 272 bytes a row; with NR = 1 it passes through the ring's last stage into registers
+  static constexpr int q_rows = 8 * QF;
+  static constexpr size_t qspace = static_cast<size_t>(q_rows) * kQPitch;
+  static constexpr size_t qbytes = q_smem ? qspace : 0;
+  static_assert(q_smem || qspace <= kStepBytes, "a stage holds the rows of q");
+  static constexpr size_t of_warp = ring + qbytes;
+  static_assert(max_warps * of_warp + 2048 <= 227 * 1024, "shared memory of a block");
+  static_assert(2 * max_warps <= 32, "a lane for each segment that is joined");
 };
 
 __device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -67,6 +76,18 @@ __device__ __forceinline__ void mma_f16_16816(float* d, uint32_t a0, uint32_t a1
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 16-byte asynchronous copy of data that is read once: the first to leave L2, so that a long
+// cache does not push out what the next kernels need.
+__device__ __forceinline__ uint64_t read_once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void cp_async_16_hint(void* dst, const void* src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src),
+               "l"(policy)
+               : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t d;
@@ -85,7 +106,7 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22floa
 struct Seq {
   int T, n, r0;          // tokens, query tokens, first query token's row
   int lo, nt, nrt;       // first step, steps, row tiles
-  long long count;       // steps on the line
+  int count;             // steps on the line
 };
 
 __device__ __forceinline__ Seq sequence(const Kv4AttendParams& p, int b, int RT) {
@@ -95,16 +116,16 @@ __device__ __forceinline__ Seq sequence(const Kv4AttendParams& p, int b, int RT)
   s.n = p.cu ? p.cu[b + 1] - s.r0 : 1;
   s.n = max(0, min(s.n, p.n_rows - s.r0));
   if (s.r0 < 0) s.n = 0;
-  const long long first = static_cast<long long>(s.T) - s.n - p.window + 1;   // leftmost position of a window
-  s.lo = p.window > 0 && first > 0 ? static_cast<int>(first / kStepTok) : 0;
+  const int first = s.T - s.n - p.window + 1;   // leftmost position of a window (all below 2^31)
+  s.lo = p.window > 0 && first > 0 ? first / kStepTok : 0;
   const int hi = (s.T + kStepTok - 1) / kStepTok;
   s.nt = s.n > 0 ? hi - s.lo : 0;
   s.nrt = (s.n * p.G + RT - 1) / RT;
-  s.count = static_cast<long long>(s.nt) * s.nrt * p.c.Hkv;
+  s.count = s.nt * s.nrt * p.c.Hkv;
   return s;
 }
 
-// Query token and head of the group of a query row; p.inv_G = ceil(2^32 / G), exact for rows below 2^25.
+// Query token of a query row of a head; p.inv_G = ceil(2^32 / G), exact for rows below 2^25.
 __device__ __forceinline__ int token_of(const Kv4AttendParams& p, int row) {
   return p.G == 1 ? row : static_cast<int>(__umulhi(static_cast<uint32_t>(row), p.inv_G));
 }
@@ -113,79 +134,77 @@ __device__ __forceinline__ size_t head_row(const Kv4AttendParams& p, int r0, int
   return (static_cast<size_t>(r0) + i) * p.c.Hq + static_cast<size_t>(h) * p.G + (qrow - i * p.G);
 }
 
-// Quotient of numbers that hardly ever need 64 bits.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
-}
-
-// The line of all steps and its equal shares: the first `rest` blocks take one step more.
+// The line of all steps (fewer than 2^30, as the host checks) and its equal shares: the first
+// `rest` blocks take one step more.
 struct Line {
-  long long W, each, rest;
-  int N;
-  __device__ __forceinline__ Line(long long w, int blocks) : W(w) {
-    N = static_cast<int>(min(static_cast<long long>(blocks), w));
-    each = N > 0 ? quotient(w, N) : 0;
+  int W, N, each, rest;
+  __device__ __forceinline__ Line(int w, int blocks) : W(w) {
+    N = min(blocks, w);
+    each = N > 0 ? static_cast<int>(static_cast<unsigned>(w) / static_cast<unsigned>(N)) : 0;
     rest = w - each * N;
   }
-  __device__ __forceinline__ long long begin(int c) const { return each * c + min(static_cast<long long>(c), rest); }
-  __device__ __forceinline__ int block_of(long long g) const {
-    const long long big = rest * (each + 1);
-    return static_cast<int>(g < big ? quotient(g, each + 1) : rest + quotient(g - big, each));
+  __device__ __forceinline__ int begin(int c) const { return each * c + min(c, rest); }
+  __device__ __forceinline__ int block_of(int g) const {
+    const int big = rest * (each + 1);
+    return g < big ? g / (each + 1) : rest + (g - big) / each;
   }
 };
 
 // Inclusive sum over the lanes of a warp.
-__device__ __forceinline__ long long lane_sums(long long n) {
+__device__ __forceinline__ int lane_sums(int x) {
   const int lane = threadIdx.x & 31;
-  if (__all_sync(0xffffffffu, n < (1 << 26))) {
-    int x = static_cast<int>(n);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  }
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, n, o);
-    if (lane >= o) n += y;
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  return n;
+  return x;
 }
 
-// Steps of all sequences, and of those before sequence b, by a whole warp.
-__device__ __forceinline__ long long line_length(const Kv4AttendParams& p, int RT, int b, long long* before) {
-  const int lane = threadIdx.x & 31;
-  long long base = 0;
-  *before = 0;
-  for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-    const long long n = b0 + lane < p.c.B ? sequence(p, b0 + lane, RT).count : 0;
-    const long long x = lane_sums(n);
-    if (b >= b0 && b < b0 + 32) *before = base + __shfl_sync(0xffffffffu, x - n, b - b0);
-    base += __shfl_sync(0xffffffffu, x, 31);
+// A place on the line, by a whole warp: a sequence with the steps and units before it.
+struct Spot {
+  int b, steps, units;
+};
+// Totals of all sequences (b = B).
+__device__ __forceinline__ Spot line_totals(const Kv4AttendParams& p, int RT) {
+  Spot t = {p.c.B, 0, 0};
+#pragma unroll 1
+  for (int b = threadIdx.x & 31; b - (threadIdx.x & 31) < p.c.B; b += 32) {
+    Seq s = {};
+    if (b < p.c.B) s = sequence(p, b, RT);
+    t.steps += __reduce_add_sync(0xffffffffu, s.count);
+    t.units += __reduce_add_sync(0xffffffffu, s.count ? s.nrt * p.c.Hkv : 0);
   }
-  return base;
+  return t;
 }
-
-// Sequence that holds step g of the line and the steps before it, by a whole warp.
-__device__ __forceinline__ int locate(const Kv4AttendParams& p, int RT, long long g, long long* before) {
+// The sequence that holds the key-th step (or unit).
+__device__ __forceinline__ Spot locate(const Kv4AttendParams& p, int RT, int key, bool by_unit) {
   const int lane = threadIdx.x & 31;
-  long long base = 0;
+  Spot at = {0, 0, 0};
+#pragma unroll 1
   for (int b0 = 0; b0 < p.c.B; b0 += 32) {
-    const long long n = b0 + lane < p.c.B ? sequence(p, b0 + lane, RT).count : 0;
-    const long long x = lane_sums(n);
-    const unsigned past = __ballot_sync(0xffffffffu, base + x > g);
+    Seq s = {};
+    if (b0 + lane < p.c.B) s = sequence(p, b0 + lane, RT);
+    const int u = s.count ? s.nrt * p.c.Hkv : 0;
+    const int xs = lane_sums(s.count), xu = lane_sums(u);
+    const unsigned past = __ballot_sync(0xffffffffu, (by_unit ? at.units + xu : at.steps + xs) > key);
     if (past) {
       const int l = __ffs(past) - 1;
-      *before = base + __shfl_sync(0xffffffffu, x - n, l);
-      return b0 + l;
+      at.b = b0 + l;
+      at.steps += __shfl_sync(0xffffffffu, xs - s.count, l);
+      at.units += __shfl_sync(0xffffffffu, xu - u, l);
+      return at;
     }
-    base += __shfl_sync(0xffffffffu, x, 31);
+    at.steps += __shfl_sync(0xffffffffu, xs, 31);
+    at.units += __shfl_sync(0xffffffffu, xu, 31);
   }
-  *before = base;
-  return p.c.B;
+  at.b = p.c.B;
+  return at;
+}
+// First step of a unit, by a whole warp; the end of the line for a number past the last unit.
+__device__ __forceinline__ int unit_step(const Kv4AttendParams& p, int RT, int unit) {
+  const Spot at = locate(p, RT, unit, true);
+  return at.b < p.c.B ? at.steps + (unit - at.units) * sequence(p, at.b, RT).nt : at.steps;
 }
 
 // 2^e for e in [-126, 127].
@@ -211,55 +230,32 @@ __device__ __forceinline__ void store_out<__half>(uint8_t* out, size_t at, float
 // Result of one row's four dims: acc / l, zeros for a row whose mask left nothing.
 template <typename T>
 __device__ __forceinline__ void finish(const Kv4AttendParams& p, size_t head_row, int d4, float m, float l, float4 a) {
-  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float inv = l == 0.f ? 0.f : __frcp_rn(l);
   a.x *= inv;
   a.y *= inv;
   a.z *= inv;
   a.w *= inv;
   store_out<T>(p.out, head_row * kD + d4 * 4, a);
-  if (p.lse && d4 == 0) p.lse[head_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  if (p.lse && d4 == 0) p.lse[head_row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
 }
 
-// 32 consecutive values of q (one row, 32 dims) as fp32.
+// Four consecutive values of q as fp32.
 template <typename T>
-__device__ __forceinline__ void load_q32(const uint8_t* row, float* x);
+__device__ __forceinline__ float4 load_q4(const uint8_t* at);
 template <>
-__device__ __forceinline__ void load_q32<float>(const uint8_t* row, float* x) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float4 v = reinterpret_cast<const float4*>(row)[i];
-    x[4 * i] = v.x;
-    x[4 * i + 1] = v.y;
-    x[4 * i + 2] = v.z;
-    x[4 * i + 3] = v.w;
-  }
+__device__ __forceinline__ float4 load_q4<float>(const uint8_t* at) {
+  return __ldg(reinterpret_cast<const float4*>(at));
 }
 template <>
-__device__ __forceinline__ void load_q32<__nv_bfloat16>(const uint8_t* row, float* x) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = reinterpret_cast<const uint4*>(row)[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = bf16lo(w[j]);
-      x[8 * i + 2 * j + 1] = bf16hi(w[j]);
-    }
-  }
+__device__ __forceinline__ float4 load_q4<__nv_bfloat16>(const uint8_t* at) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
 }
 template <>
-__device__ __forceinline__ void load_q32<__half>(const uint8_t* row, float* x) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint4 v = reinterpret_cast<const uint4*>(row)[i];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = unpack_f16x2(w[j]);
-      x[8 * i + 2 * j] = f.x;
-      x[8 * i + 2 * j + 1] = f.y;
-    }
-  }
+__device__ __forceinline__ float4 load_q4<__half>(const uint8_t* at) {
+  const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+  const float2 a = unpack_f16x2(v.x), b = unpack_f16x2(v.y);
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // A segment that is joined with others of its unit.
@@ -270,68 +266,61 @@ struct Segment {
 };
 
 template <typename T, int NR, Mode M>
-__global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel(Kv4AttendParams p) {
+__global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_kernel(const __grid_constant__ Kv4AttendParams p) {
   using S = Shape<NR, M>;
   constexpr int RT = S::RT;
-  constexpr int kWarps = S::warps;
+  const int warps = blockDim.x >> 5;
   constexpr int kSlot = RT * (kD + 2);             // floats of a slot in the workspace
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ Segment segs[2 * kWarps];             // a warp's first and last
+  __shared__ Segment segs[2 * S::max_warps];             // a warp's first and last
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, t = lane & 3;
   uint8_t* ring = smem + warp * S::ring;
-  uint2* qs = reinterpret_cast<uint2*>(smem + kWarps * S::ring + warp * S::qbytes);   // [fragment][8][lane]
+  uint8_t* qs = S::q_smem ? smem + warps * S::ring + warp * S::qbytes : ring + (S::stages - 1) * kStepBytes;
   if (lane < 2) segs[2 * warp + lane].unit = -1;
   __syncwarp();
 
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- this block's and this warp's share of the line ----
-  Seq s = {};
-  long long before = 0, W, sums = 0;
-  const bool few = p.c.B <= 32;                    // one sequence a lane, read once
-  if (few) {
-    if (lane < p.c.B) s = sequence(p, lane, RT);
-    sums = lane_sums(s.count);
-    W = __shfl_sync(0xffffffffu, sums, 31);
-  } else {
-    W = line_length(p, RT, 0, &before);
+  const uint64_t policy = read_once_policy();
+  // ---- rows of sequences without tokens: sequence b by block b, b + blocks, ... ----
+#pragma unroll 1
+  for (int b = blockIdx.x; b < p.c.B; b += gridDim.x) {
+    const Seq e = sequence(p, b, RT);
+    if (e.n == 0 || e.nt > 0) continue;
+    for (long long i = warp; i < static_cast<long long>(e.n) * p.c.Hq; i += warps)
+      finish<T>(p, static_cast<size_t>(e.r0) * p.c.Hq + i, lane, 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
   }
-  const Line line(W, gridDim.x);
+
+  // ---- this block's and this warp's share of the line ----
+  const Spot all = line_totals(p, RT);
+  const Line line(p.solo ? all.units : all.steps, gridDim.x);
   if (static_cast<int>(blockIdx.x) >= line.N) return;
-  const long long block_g = line.begin(blockIdx.x);
-  const int block_len = static_cast<int>(line.begin(blockIdx.x + 1) - block_g);
-  long long g = block_g + static_cast<long long>(block_len) * warp / kWarps;
-  const long long g_end = block_g + static_cast<long long>(block_len) * (warp + 1) / kWarps;
-  float* first_slot = p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * kWarps + warp) * kSlot;
+  int block_g = line.begin(blockIdx.x), block_end = line.begin(blockIdx.x + 1);
+  if (p.solo) {
+    block_g = unit_step(p, RT, block_g);
+    block_end = unit_step(p, RT, block_end);
+  }
+  const int block_len = block_end - block_g;
+  // warps: as the blocks, the first ones a step more
+  int g = block_g + block_len / warps * warp + min(warp, block_len % warps);
+  const int g_end = g + block_len / warps + (warp < block_len % warps ? 1 : 0);
+  float* first_slot = p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * warps + warp) * kSlot;
 
   if (g < g_end) {
-    int b;
-    if (few) {
-      b = __ffs(__ballot_sync(0xffffffffu, sums > g)) - 1;
-      before = __shfl_sync(0xffffffffu, sums - s.count, b);
-      s.T = __shfl_sync(0xffffffffu, s.T, b);
-      s.n = __shfl_sync(0xffffffffu, s.n, b);
-      s.r0 = __shfl_sync(0xffffffffu, s.r0, b);
-      s.lo = __shfl_sync(0xffffffffu, s.lo, b);
-      s.nt = __shfl_sync(0xffffffffu, s.nt, b);
-      s.nrt = __shfl_sync(0xffffffffu, s.nrt, b);
-      s.count = __shfl_sync(0xffffffffu, s.count, b);
-    } else {
-      b = locate(p, RT, g, &before);
-      s = sequence(p, b, RT);
-    }
+    const Spot at = locate(p, RT, g, false);
+    int b = at.b, before = at.steps;
+    Seq s = sequence(p, b, RT);
     while (g < g_end && b < p.c.B) {
       if (g - before >= s.count) {   // next sequence with work
         before += s.count;
         if (++b < p.c.B) s = sequence(p, b, RT);
         continue;
       }
-      const long long in_seq = g - before;
-      const int unit = static_cast<int>(quotient(in_seq, s.nt));                    // h * nrt + row tile
-      const int a = static_cast<int>(in_seq - static_cast<long long>(unit) * s.nt); // first step of the segment
-      const int len = static_cast<int>(min(static_cast<long long>(s.nt - a), g_end - g));
+      const int unit = static_cast<int>(static_cast<unsigned>(g - before) / static_cast<unsigned>(s.nt));   // h * nrt + row tile
+      const int a = g - before - unit * s.nt;                    // first step of the segment
+      const int len = min(s.nt - a, g_end - g);
       const int h = s.nrt == 1 ? unit : unit / s.nrt, rt = unit - h * s.nrt;
       const int row0 = rt * RT;
       const int rows = min(RT, s.n * p.G - row0);                // valid query rows
@@ -360,8 +349,8 @@ __global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel
               const uint8_t* src = p.c.cache + static_cast<size_t>(static_cast<uint32_t>(w)) * kTileBytes + lane * 16;
               uint8_t* dst = ring + st * kStepBytes + u * kTileBytes + lane * 16;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) cp_async_16(dst + j * 512, src + j * 512);
-              if (lane < 16) cp_async_16(dst + kOffScale, src + kOffScale);
+              for (int j = 0; j < 4; ++j) cp_async_16_hint(dst + j * 512, src + j * 512, policy);
+              if (lane < 16) cp_async_16_hint(dst + kOffScale, src + kOffScale, policy);
             } else {
               missing |= 1u << (2 * st + u);
             }
@@ -370,72 +359,93 @@ __global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel
         cp_async_commit();
       };
       __syncwarp();
-#pragma unroll
+#pragma unroll 1
       for (int i = 0; i < S::stages - 1; ++i) issue(i);
 
       // ---- query fragments and the bounds of each of this lane's columns ----
-      uint32_t qf[S::q_smem ? 1 : S::QF][16];
-      float f[2 * NR];
-      int hi[2 * NR], lo[2 * NR];
+      // Row by row, four values a lane: q over a power of two that takes its largest element to [0.5, 1).
+      int e_mine[NR];               // lane r: exponent of rows r, 8 + r, ... (of four and four: row r & 3)
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt) {
-        const int col = M == kPack ? (r & 3) : nt * 8 + r;
-        float x[32];
-        float top = 0.f;
-        if (col < rows) {
-          const int i = token_of(p, row0 + col);
-          load_q32<T>(p.q + (static_cast<long long>(s.r0) + i) * p.q_tok +
-                          (static_cast<size_t>(h) * p.G + (row0 + col - i * p.G)) * kD * sizeof(T) + t * 32 * sizeof(T),
-                      x);
+        e_mine[nt] = 0;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, fabsf(x[i]));
-        } else {
+        for (int c0 = 0; c0 < (M == kPack ? 4 : 8); c0 += 4) {
+          if (nt * 8 + c0 >= rows) {   // no rows: zeros
 #pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = 0.f;
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^e > top >= 2^(e - 1) for normal numbers; out of range or not finite: as it is
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
-        e = e > 126 ? 0 : max(e, -126);
-        const float down = pow2i(-e);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float x0 = x[2 * i] * down, x1 = x[2 * i + 1] * down;
-          const uint32_t hi2 = pack_f16x2(x0, x1);
-          uint32_t lo2 = 0u;
-          if (M != kHi) {
-            const float2 back = unpack_f16x2(hi2);
-            lo2 = pack_f16x2(x0 - back.x, x1 - back.y);
+            for (int k = 0; k < 4; ++k) {
+              const int at = (M == kHiLo ? 2 * nt : nt) * 8 + c0 + k;
+              *reinterpret_cast<uint2*>(qs + at * kQPitch + lane * 8) = make_uint2(0u, 0u);
+              if (M == kHiLo) *reinterpret_cast<uint2*>(qs + (at + 8) * kQPitch + lane * 8) = make_uint2(0u, 0u);
+              if (M == kPack) *reinterpret_cast<uint2*>(qs + (at + 4) * kQPitch + lane * 8) = make_uint2(0u, 0u);
+            }
+            continue;
           }
-          const uint32_t v = M == kPack && r >= 4 ? lo2 : hi2;
-          if (S::q_smem) {
-            reinterpret_cast<uint32_t*>(qs + ((M == kHiLo ? 2 * nt : nt) * 8 + i / 2) * 32 + lane)[i & 1] = v;
-            if (M == kHiLo) reinterpret_cast<uint32_t*>(qs + ((2 * nt + 1) * 8 + i / 2) * 32 + lane)[i & 1] = lo2;
-          } else {
-            qf[0][i] = v;
-            if (M == kHiLo) qf[S::QF - 1][i] = lo2;
-          }
-        }
+          float4 x[4];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int mine = M == kPack ? ((2 * t + j) & 3) : 2 * t + j;
-          const int ec = __shfl_sync(0xffffffffu, e, 4 * mine);
-          const int c = nt * 8 + mine;
-          // never so small that a masked logit, -inf times f, is NaN; logits under 2^-80 are as good as 0
-          const float fc = p.scale * kLog2e * pow2i(ec);
-          f[2 * nt + j] = fabsf(fc) < 1e-36f ? copysignf(1e-36f, fc) : fc;
-          const int pos = s.T - s.n + token_of(p, row0 + c);
-          hi[2 * nt + j] = c >= rows ? -1 : p.causal ? pos : s.T - 1;
-          lo[2 * nt + j] = p.window > 0 ? pos - p.window + 1 : 0;
+          for (int k = 0; k < 4; ++k) {
+            const int row = min(nt * 8 + c0 + k, rows - 1);
+            const int i = token_of(p, row0 + row);
+            x[k] = load_q4<T>(p.q + (static_cast<long long>(s.r0) + i) * p.q_tok +
+                              (static_cast<size_t>(h) * p.G + (row0 + row - i * p.G)) * kD * sizeof(T) + lane * 4 * sizeof(T));
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float top =
+                warp_max_f32(fmaxf(fmaxf(fabsf(x[k].x), fabsf(x[k].y)), fmaxf(fabsf(x[k].z), fabsf(x[k].w))));
+            // 2^e > top >= 2^(e - 1) for normal numbers; out of range or not finite: as it is
+            int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
+            e = e > 126 ? 0 : max(e, -126);
+            const float down = pow2i(-e);
+            const int at = (M == kHiLo ? 2 * nt : nt) * 8 + c0 + k;
+            const uint32_t h0 = pack_f16x2(x[k].x * down, x[k].y * down), h1 = pack_f16x2(x[k].z * down, x[k].w * down);
+            *reinterpret_cast<uint2*>(qs + at * kQPitch + lane * 8) = make_uint2(h0, h1);
+            if (M != kHi) {
+              const float2 b0 = unpack_f16x2(h0), b1 = unpack_f16x2(h1);
+              *reinterpret_cast<uint2*>(qs + (at + (M == kPack ? 4 : 8)) * kQPitch + lane * 8) =
+                  make_uint2(pack_f16x2(x[k].x * down - b0.x, x[k].y * down - b0.y),
+                             pack_f16x2(x[k].z * down - b1.x, x[k].w * down - b1.y));
+            }
+            if ((M == kPack ? (lane & 3) : (lane & 7)) == c0 + k) e_mine[nt] = e;
+          }
         }
       }
+      __syncwarp();
+      uint4 qf[S::q_smem ? 1 : S::QF][4];   // lane: dims [32 t, +32) of row r
+      if (!S::q_smem) {
+#pragma unroll
+        for (int k = 0; k < S::QF; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            qf[S::q_smem ? 0 : k][j] = *reinterpret_cast<const uint4*>(qs + (k * 8 + r) * kQPitch + t * 64 + j * 16);
+        __syncwarp();                       // before the stage is filled
+      }
+      float f[2 * NR];
+#pragma unroll
+      for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int own = M == kPack ? ((2 * t + j) & 3) : 2 * t + j;
+          // never so small that a masked logit, -inf times f, is NaN; logits under 2^-80 are as good as 0
+          const float fc = p.scale * kLog2e * pow2i(__shfl_sync(0xffffffffu, e_mine[nt], own));
+          f[2 * nt + j] = fabsf(fc) < 1e-36f ? copysignf(1e-36f, fc) : fc;
+        }
+      }
+      // last and first position that this lane's column c sees
+      auto column = [&](int c) { return M == kPack ? ((2 * t + c) & 3) : (c >> 1) * 8 + 2 * t + (c & 1); };
+      auto last_seen = [&](int c) {
+        const int col = column(c);
+        return col >= rows ? -1 : p.causal ? s.T - s.n + token_of(p, row0 + col) : s.T - 1;
+      };
+      auto first_seen = [&](int c) {
+        return p.window > 0 ? s.T - s.n + token_of(p, row0 + column(c)) - p.window + 1 : 0;
+      };
       // positions that every row of the unit sees
       const int all_hi = p.causal ? s.T - s.n + token_of(p, row0) : s.T - 1;
       const int all_lo = p.window > 0 ? s.T - s.n + token_of(p, row0 + rows - 1) - p.window + 1 : 0;
 
       float o[NR][8][4];
       float ref[2 * NR], l[2 * NR];
+      unsigned poison = 0;          // bit c: column c saw a value of this lane's dims that is not finite
 #pragma unroll
       for (int j = 0; j < 2 * NR; ++j) {
         ref[j] = -1e30f;
@@ -453,193 +463,198 @@ __global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel
         cp_async_wait<S::stages - 2>();
         __syncwarp();
         const int st = i % S::stages;
-        const unsigned absent = (missing >> (2 * st)) & 3u;
+        const unsigned missing_now = (missing >> (2 * st)) & 3u;
         issue(i + S::stages - 1);
-        const uint8_t* stage = ring + st * kStepBytes;
-        const int pos = (tile0 + i * kStep) * kTileTok;
-        // ---- S^T = K q^T ----
-        float sacc[kStep][NR][4];
-        uint2 sc[kStep];
+#pragma unroll 1
+        for (int u0 = 0; u0 < kStep; u0 += S::U) {
+          const uint8_t* stage = ring + st * kStepBytes + u0 * kTileBytes;
+          const int pos = (tile0 + i * kStep + u0) * kTileTok;
+          const unsigned absent = (missing_now >> u0) & ((1u << S::U) - 1u);
+          // ---- S^T = K q^T ----
+          float sacc[S::U][NR][4];
+          uint2 sc[S::U];
 #pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-          const uint8_t* tile = stage + u * kTileBytes;
-          const uint4 k0 = reinterpret_cast<const uint4*>(tile)[lane];
-          const uint4 k1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
-          sc[u] = reinterpret_cast<const uint2*>(tile + kOffScale)[lane];
-          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+          for (int u = 0; u < S::U; ++u) {
+            const uint8_t* tile = stage + u * kTileBytes;
+            const uint4 k0 = reinterpret_cast<const uint4*>(tile)[lane];
+            const uint4 k1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
+            sc[u] = reinterpret_cast<const uint2*>(tile + kOffScale)[lane];
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-          for (int nt = 0; nt < NR; ++nt)
+            for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sacc[u][nt][j] = 0.f;
+              for (int j = 0; j < 4; ++j) sacc[u][nt][j] = 0.f;
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t x[4], y[4];
-            e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
-            e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
-            const uint32_t s0 = scale_both(sc[u].x, w >> 1), s1 = scale_both(sc[u].x, 2 + (w >> 1));
+            for (int w = 0; w < 4; ++w) {
+              uint32_t x[4], y[4];
+              e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
+              e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
+              const uint32_t s0 = scale_both(sc[u].x, w >> 1), s1 = scale_both(sc[u].x, 2 + (w >> 1));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[j] = hmul2(x[j], s0);
-              y[j] = hmul2(y[j], s1);
+              for (int j = 0; j < 4; ++j) {
+                x[j] = hmul2(x[j], s0);
+                y[j] = hmul2(y[j], s1);
+              }
+#pragma unroll
+              for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+                  for (int part_q = 0; part_q < (M == kHiLo ? 2 : 1); ++part_q) {
+                    const int fr = M == kHiLo ? 2 * nt + part_q : nt;
+                    const uint4 bq = S::q_smem ? *reinterpret_cast<const uint4*>(qs + (fr * 8 + r) * kQPitch + t * 64 + w * 16)
+                                               : qf[S::q_smem ? 0 : fr][w];
+                    mma_f16_16816(sacc[u][nt], x[2 * kk], y[2 * kk], x[2 * kk + 1], y[2 * kk + 1], kk ? bq.z : bq.x,
+                                  kk ? bq.w : bq.y);
+                  }
+                }
+              }
+            }
+            if (M == kPack) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) sacc[u][0][j] += __shfl_xor_sync(0xffffffffu, sacc[u][0][j], 2);
+            }
+          }
+          // ---- masks ----
+          uint32_t vs[S::U][2];
+#pragma unroll
+          for (int u = 0; u < S::U; ++u) {
+            vs[u][0] = scale_pair(sc[u].y, 0);
+            vs[u][1] = scale_pair(sc[u].y, 2);
+          }
+          const bool whole = absent == 0u && pos + S::U * kTileTok - 1 <= all_hi && pos >= all_lo;
+          if (!whole) {
+            int hi[2 * NR], lo[2 * NR];
+#pragma unroll
+            for (int c = 0; c < 2 * NR; ++c) {
+              hi[c] = last_seen(c);
+              lo[c] = first_seen(c);
             }
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-              const int i8 = 2 * w + kk;
+            for (int u = 0; u < S::U; ++u) {
+              const int pu = pos + u * kTileTok;
+              const bool present = !((absent >> u) & 1u);
 #pragma unroll
-              for (int nt = 0; nt < NR; ++nt) {
+              for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                for (int part_q = 0; part_q < (M == kHiLo ? 2 : 1); ++part_q) {
-                  const int fr = M == kHiLo ? 2 * nt + part_q : nt;
-                  uint2 bq;
-                  if (S::q_smem) bq = qs[(fr * 8 + i8) * 32 + lane];
-                  else bq = make_uint2(qf[S::q_smem ? 0 : fr][2 * i8], qf[S::q_smem ? 0 : fr][2 * i8 + 1]);
-                  mma_f16_16816(sacc[u][nt], x[2 * kk], y[2 * kk], x[2 * kk + 1], y[2 * kk + 1], bq.x, bq.y);
+                for (int j = 0; j < 4; ++j) {
+                  const int tp = pu + r + 8 * (j >> 1), c = 2 * nt + (j & 1);
+                  // times f it is -inf, whatever f's sign
+                  if (tp > hi[c] || tp < lo[c] || !present) sacc[u][nt][j] = f[c] < 0.f ? INFINITY : -INFINITY;
+                }
+              // A zero weight must not meet a NaN or an infinity: tokens past the end hold anything.
+              const int left = present ? s.T - (pu + 2 * t) : 0;   // tokens from this lane's first on
+              vs[u][0] &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+              vs[u][1] &= (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+              // Values that are not finite count for the rows that see their token, and for no other:
+              // taken out of the product, and the block's dims of those rows become NaN in the end.
+              const unsigned bad = ((vs[u][0] & 0x7c00u) == 0x7c00u ? 1u : 0u) |
+                                   ((vs[u][0] & 0x7c000000u) == 0x7c000000u ? 2u : 0u) |
+                                   ((vs[u][1] & 0x7c00u) == 0x7c00u ? 256u : 0u) |
+                                   ((vs[u][1] & 0x7c000000u) == 0x7c000000u ? 512u : 0u);
+              if (__any_sync(0xffffffffu, bad != 0u)) {
+                vs[u][0] &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
+                vs[u][1] &= (bad & 256u ? 0u : 0xffffu) | (bad & 512u ? 0u : 0xffff0000u);
+                unsigned all = bad << (2 * t);                       // bit: token of the tile
+                all |= __shfl_xor_sync(0xffffffffu, all, 1);
+                all |= __shfl_xor_sync(0xffffffffu, all, 2);
+#pragma unroll
+                for (int c = 0; c < 2 * NR; ++c) {
+                  const int from = max(0, lo[c] - pu), to = min(kTileTok - 1, hi[c] - pu);
+                  if (from <= to && (all & ((2u << to) - (1u << from))) != 0u) poison |= 1u << c;
                 }
               }
             }
           }
-          if (M == kPack) {
+          // ---- online softmax: weights 2^(s f - ref) ----
+          float y[S::U][NR][4], top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sacc[u][0][j] += __shfl_xor_sync(0xffffffffu, sacc[u][0][j], 2);
-          }
-        }
-        // ---- masks ----
-        uint32_t vs[kStep][2];
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-          vs[u][0] = scale_pair(sc[u].y, 0);
-          vs[u][1] = scale_pair(sc[u].y, 2);
-        }
-        const bool whole = absent == 0u && pos + kStepTok - 1 <= all_hi && pos >= all_lo;
-        if (!whole) {
-#pragma unroll
-          for (int u = 0; u < kStep; ++u) {
-            const int pu = pos + u * kTileTok;
-            const bool present = !((absent >> u) & 1u);
+          for (int u = 0; u < S::U; ++u)
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                const int tp = pu + r + 8 * (j >> 1), c = 2 * nt + (j & 1);
-                // times f it is -inf, whatever f's sign
-                if (tp > hi[c] || tp < lo[c] || !present) sacc[u][nt][j] = f[c] < 0.f ? INFINITY : -INFINITY;
+                // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
+                sacc[u][nt][j] = __fmul_rn(sacc[u][nt][j], f[2 * nt + (j & 1)]);
+                y[u][nt][j] = __fsub_rn(sacc[u][nt][j], ref[2 * nt + (j & 1)]);
+                top = fmaxf(top, y[u][nt][j]);
               }
-            // A zero weight must not meet a NaN or an infinity: tokens past the end hold anything.
-            const int left = present ? s.T - (pu + 2 * t) : 0;   // tokens from this lane's first on
-            vs[u][0] &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-            vs[u][1] &= (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
-            // Values that are not finite count for the rows that see their token, and for no other:
-            // taken out of the product, and added as NaN to those rows' sums of the block's dims.
-            const unsigned bad = ((vs[u][0] & 0x7c00u) == 0x7c00u ? 1u : 0u) |
-                                 ((vs[u][0] & 0x7c000000u) == 0x7c000000u ? 2u : 0u) |
-                                 ((vs[u][1] & 0x7c00u) == 0x7c00u ? 256u : 0u) |
-                                 ((vs[u][1] & 0x7c000000u) == 0x7c000000u ? 512u : 0u);
-            if (__any_sync(0xffffffffu, bad != 0u)) {
-              vs[u][0] &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
-              vs[u][1] &= (bad & 256u ? 0u : 0xffffu) | (bad & 512u ? 0u : 0xffff0000u);
-              unsigned all = bad << (2 * t);                       // bit: token of the tile
-              all |= __shfl_xor_sync(0xffffffffu, all, 1);
-              all |= __shfl_xor_sync(0xffffffffu, all, 2);
+          if (__any_sync(0xffffffffu, top > kHead + kGrow)) {
 #pragma unroll
-              for (int c = 0; c < 2 * NR; ++c) {
-                const int from = max(0, lo[c] - pu), to = min(kTileTok - 1, hi[c] - pu);
-                const bool seen = from <= to && (all & ((2u << to) - (1u << from))) != 0u;
+            for (int c = 0; c < 2 * NR; ++c) {
+              float mx = -INFINITY;
 #pragma unroll
-                for (int i8 = 0; i8 < 8; ++i8) {
-                  if (seen) o[c >> 1][i8][c & 1] = o[c >> 1][i8][(c & 1) + 2] = __int_as_float(0x7fffffff);
+              for (int u = 0; u < S::U; ++u)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) mx = fmaxf(mx, sacc[u][c >> 1][(c & 1) + 2 * j]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float next = fmaxf(ref[c], mx - kHead);
+              const float shrink = fast_exp2(ref[c] - next);
+              ref[c] = next;
+              l[c] *= shrink;
+#pragma unroll
+              for (int i8 = 0; i8 < 8; ++i8) {
+                o[c >> 1][i8][c & 1] *= shrink;
+                o[c >> 1][i8][(c & 1) + 2] *= shrink;
+              }
+#pragma unroll
+              for (int u = 0; u < S::U; ++u)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  y[u][c >> 1][(c & 1) + 2 * j] = __fsub_rn(sacc[u][c >> 1][(c & 1) + 2 * j], next);
+            }
+          }
+          // ---- O^T += V^T P ----
+#pragma unroll
+          for (int u = 0; u < S::U; ++u) {
+            uint32_t ph[NR][2], pl[NR][2];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt) {
+              float pr[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int c = 2 * nt + (j & 1);
+                pr[j] = fast_exp2(y[u][nt][j]);
+                l[c] += pr[j];
+              }
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
+                if (M != kHi) {
+                  const float2 back = unpack_f16x2(hi2);
+                  const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
+                  if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
+                  else pl[nt][half] = transpose8x8(lo2);
                 }
+                ph[nt][half] = transpose8x8(hi2);
               }
             }
-          }
-        }
-        // ---- online softmax: weights 2^(s f - ref) ----
-        float y[kStep][NR][4], top = -INFINITY;
+            const uint8_t* tile = stage + u * kTileBytes + kOffV;
+            const uint4 v0 = reinterpret_cast<const uint4*>(tile)[lane];
+            const uint4 v1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
+            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-        for (int u = 0; u < kStep; ++u)
+            for (int w = 0; w < 4; ++w) {
+              uint32_t x[4], y[4];
+              e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
+              e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
 #pragma unroll
-          for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
-              sacc[u][nt][j] = __fmul_rn(sacc[u][nt][j], f[2 * nt + (j & 1)]);
-              y[u][nt][j] = __fsub_rn(sacc[u][nt][j], ref[2 * nt + (j & 1)]);
-              top = fmaxf(top, y[u][nt][j]);
-            }
-        if (__any_sync(0xffffffffu, top > kHead + kGrow)) {
-#pragma unroll
-          for (int c = 0; c < 2 * NR; ++c) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < kStep; ++u)
-#pragma unroll
-              for (int j = 0; j < 2; ++j) mx = fmaxf(mx, sacc[u][c >> 1][(c & 1) + 2 * j]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float next = fmaxf(ref[c], mx - kHead);
-            const float shrink = fast_exp2(ref[c] - next);
-            ref[c] = next;
-            l[c] *= shrink;
-#pragma unroll
-            for (int i8 = 0; i8 < 8; ++i8) {
-              o[c >> 1][i8][c & 1] *= shrink;
-              o[c >> 1][i8][(c & 1) + 2] *= shrink;
-            }
-#pragma unroll
-            for (int u = 0; u < kStep; ++u)
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                y[u][c >> 1][(c & 1) + 2 * j] = __fsub_rn(sacc[u][c >> 1][(c & 1) + 2 * j], next);
-          }
-        }
-        // ---- O^T += V^T P ----
-#pragma unroll
-        for (int u = 0; u < kStep; ++u) {
-          uint32_t ph[NR][2], pl[NR][2];
-#pragma unroll
-          for (int nt = 0; nt < NR; ++nt) {
-            float pr[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int c = 2 * nt + (j & 1);
-              pr[j] = fast_exp2(y[u][nt][j]);
-              l[c] += pr[j];
-            }
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
-              if (M != kHi) {
-                const float2 back = unpack_f16x2(hi2);
-                const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
-                if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
-                else pl[nt][half] = transpose8x8(lo2);
+              for (int j = 0; j < 4; ++j) {
+                x[j] = hmul2(x[j], vs[u][0]);
+                y[j] = hmul2(y[j], vs[u][1]);
               }
-              ph[nt][half] = transpose8x8(hi2);
-            }
-          }
-          const uint8_t* tile = stage + u * kTileBytes + kOffV;
-          const uint4 v0 = reinterpret_cast<const uint4*>(tile)[lane];
-          const uint4 v1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
-          const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t x[4], y[4];
-            e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
-            e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
+              for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              x[j] = hmul2(x[j], vs[u][0]);
-              y[j] = hmul2(y[j], vs[u][1]);
-            }
-#pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-#pragma unroll
-              for (int nt = 0; nt < NR; ++nt) {
-                mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
-                              ph[nt][1]);
-                if (M == kHiLo)
-                  mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0],
-                                pl[nt][1]);
+                for (int nt = 0; nt < NR; ++nt) {
+                  mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
+                                ph[nt][1]);
+                  if (M == kHiLo)
+                    mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0],
+                                  pl[nt][1]);
+                }
               }
             }
           }
@@ -647,12 +662,9 @@ __global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel
       }
       cp_async_wait<0>();
 
-      // ---- end of a segment: the result, or a partial to be joined ----
-      const bool done = a == 0 && len == s.nt;
-      const bool last = g + len >= g_end;
-      float* slot = last ? reinterpret_cast<float*>(ring) : first_slot;
-      const int pitch = last ? kPitch : kD;
-      if (!done) __syncwarp();   // the ring has been read
+      // ---- end of a segment: through shared memory, into the result or a partial to be joined ----
+      __syncwarp();   // the ring has been read
+      float* mine = reinterpret_cast<float*>(ring);
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
@@ -661,37 +673,47 @@ __global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel
           l[c] += __shfl_xor_sync(0xffffffffu, l[c], 4);
           l[c] += __shfl_xor_sync(0xffffffffu, l[c], 8);
           l[c] += __shfl_xor_sync(0xffffffffu, l[c], 16);
-          float v[16];
-#pragma unroll
-          for (int i8 = 0; i8 < 8; ++i8) {
-            v[2 * i8] = o[nt][i8][j];
-            v[2 * i8 + 1] = o[nt][i8][j + 2];
-          }
           if (M == kPack) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 2);
+            for (int i8 = 0; i8 < 8; ++i8) {
+              o[nt][i8][j] += __shfl_xor_sync(0xffffffffu, o[nt][i8][j], 2);
+              o[nt][i8][j + 2] += __shfl_xor_sync(0xffffffffu, o[nt][i8][j + 2], 2);
+            }
           }
           const int col = nt * 8 + 2 * t + j;
-          if (col >= rows) continue;
+          if (M == kPack && t >= 2) continue;
+          float* row = mine + 2 * RT + col * kPitch + 16 * r;
+          const float add = (poison >> c) & 1u ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<float4*>(row)[i] = make_float4(o[nt][2 * i][j] + add, o[nt][2 * i][j + 2] + add,
+                                                            o[nt][2 * i + 1][j] + add, o[nt][2 * i + 1][j + 2] + add);
+          if (r == 0) {
+            mine[col] = ref[c];
+            mine[RT + col] = l[c];
+          }
+        }
+      }
+      __syncwarp();
+      const bool done = a == 0 && len == s.nt;
+      if (done || g + len < g_end) {
+#pragma unroll 1
+        for (int row = 0; row < rows; ++row) {
+          const float4 v = *reinterpret_cast<const float4*>(mine + 2 * RT + row * kPitch + lane * 4);
+          const float m = mine[row], sum = mine[RT + row];
           if (done) {
-            const size_t at = head_row(p, s.r0, h, row0 + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              finish<T>(p, at, 4 * r + i, ref[c], l[c], make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+            finish<T>(p, head_row(p, s.r0, h, row0 + row), lane, m, sum, v);
           } else {
-            float* row = slot + 2 * RT + col * pitch + 16 * r;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<float4*>(row)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            if (r == 0) {
-              slot[col] = ref[c];
-              slot[RT + col] = l[c];
+            if (lane == 0) {
+              first_slot[row] = m;
+              first_slot[RT + row] = sum;
             }
+            *reinterpret_cast<float4*>(first_slot + 2 * RT + row * kD + lane * 4) = v;
           }
         }
       }
       if (!done && lane == 0) {
-        segs[2 * warp + (last ? 1 : 0)] =
+        segs[2 * warp + (g + len < g_end ? 0 : 1)] =
             Segment{unit, b, h, s.r0, row0, rows,
                     (a == 0 ? 1 : 0) | (a + len == s.nt ? 2 : 0) | (g == block_g ? 4 : 0)};
       }
@@ -700,62 +722,75 @@ __global__ void __launch_bounds__(Shape<NR, M>::warps * 32, 1) kv4_attend_kernel
   }
   __syncthreads();
 
-  // ---- join the warps' partials, unit by unit; a warp takes rows warp, warp + kWarps, ... ----
-  for (int e = 0; e < 2 * kWarps;) {
+  // ---- join the warps' partials; a warp takes every warps-th row of all the units together ----
+  const int unit = lane < 2 * warps ? segs[lane].unit : -1, unit_b = lane < 2 * warps ? segs[lane].b : 0;
+  const unsigned valid = __ballot_sync(0xffffffffu, unit >= 0);
+  const unsigned earlier = valid & ((1u << lane) - 1u);
+  const int prev = earlier ? 31 - __clz(earlier) : lane;
+  const int prev_unit = __shfl_sync(0xffffffffu, unit, prev), prev_b = __shfl_sync(0xffffffffu, unit_b, prev);
+  unsigned starts = __ballot_sync(0xffffffffu, unit >= 0 && (!earlier || prev_unit != unit || prev_b != unit_b));
+  int item = warp;   // rows still to skip before this warp's next
+#pragma unroll 1
+  for (; starts; starts &= starts - 1) {
+    const int e = __ffs(starts) - 1;
+    const unsigned next = starts & (starts - 1);
+    const unsigned set = valid & ~((1u << e) - 1u) & (next ? (next & -next) - 1u : 0xffffffffu);
     const Segment head = segs[e];
-    if (head.unit < 0) {
-      ++e;
-      continue;
-    }
-    // lane i: whether segment i is one of this unit's (they stand together, but for gaps)
-    const bool mine = lane < 2 * kWarps && lane >= e && segs[lane].unit == head.unit && segs[lane].b == head.b;
-    const unsigned set = __ballot_sync(0xffffffffu, mine);
-    const int final = 31 - __clz(set);
-    const bool done = (head.open & 1) && (segs[final].open & 2);
-    const float* slot = lane & 1 ? reinterpret_cast<const float*>(smem + (lane >> 1) * S::ring)
-                                 : p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * kWarps + (lane >> 1)) * kSlot;
+    const bool mine = (set >> lane) & 1u;
+    const bool done = (head.open & 1) && (segs[31 - __clz(set)].open & 2);
     float* out_slot = p.parts + static_cast<size_t>(2 * blockIdx.x + ((head.open & 5) == 1 ? 1 : 0)) * kSlot;
-    for (int row = warp; row < head.rows; row += kWarps) {
-      const float m1 = mine ? slot[row] : -INFINITY;
-      const float l1 = mine ? slot[RT + row] : 0.f;
-      const float m = warp_max(m1);
-      const float w = mine ? fast_exp2(m1 - m) : 0.f;   // NaN where a row is NaN
+    auto slot_of = [&](int i) -> const float* {
+      return i & 1 ? reinterpret_cast<const float*>(smem + (i >> 1) * S::ring)
+                   : p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * warps + (i >> 1)) * kSlot;
+    };
+#pragma unroll 1
+    for (; item < head.rows; item += warps) {
+      const float m1 = mine ? slot_of(lane)[item] : -INFINITY;
+      const float l1 = mine ? slot_of(lane)[RT + item] : 0.f;
+      const float m = warp_max_f32(m1);
+      const float w = mine ? fast_exp2(m1 - m) : 0.f;
       const float l = warp_sum(w * l1);
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (unsigned left = set; left; left &= left - 1) {
-        const int i = __ffs(left) - 1;
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        const float* si = i & 1 ? reinterpret_cast<const float*>(smem + (i >> 1) * S::ring) + row * kPitch
-                                : p.parts + static_cast<size_t>(2 * gridDim.x + blockIdx.x * kWarps + (i >> 1)) * kSlot + row * kD;
-        const float4 v = *reinterpret_cast<const float4*>(si + 2 * RT + lane * 4);
-        acc.x = fmaf(wi, v.x, acc.x);
-        acc.y = fmaf(wi, v.y, acc.y);
-        acc.z = fmaf(wi, v.z, acc.z);
-        acc.w = fmaf(wi, v.w, acc.w);
+#pragma unroll 1
+      for (unsigned left = set; left;) {
+        float4 v[4];
+        float wi[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = left ? __ffs(left) - 1 : e;
+          wi[k] = left ? __shfl_sync(0xffffffffu, w, i) : 0.f;
+          v[k] = left ? *reinterpret_cast<const float4*>(slot_of(i) + 2 * RT + item * (i & 1 ? kPitch : kD) + lane * 4)
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+          left &= left - 1;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc.x = fmaf(wi[k], v[k].x, acc.x);
+          acc.y = fmaf(wi[k], v[k].y, acc.y);
+          acc.z = fmaf(wi[k], v[k].z, acc.z);
+          acc.w = fmaf(wi[k], v[k].w, acc.w);
+        }
       }
       if (done) {
-        finish<T>(p, head_row(p, head.r0, head.h, head.row0 + row), lane, m, l, acc);
+        finish<T>(p, head_row(p, head.r0, head.h, head.row0 + item), lane, m, l, acc);
       } else {
         if (lane == 0) {
-          out_slot[row] = m;
-          out_slot[RT + row] = l;
+          out_slot[item] = m;
+          out_slot[RT + item] = l;
         }
-        *reinterpret_cast<float4*>(out_slot + 2 * RT + row * kD + lane * 4) = acc;
+        *reinterpret_cast<float4*>(out_slot + 2 * RT + item * kD + lane * 4) = acc;
       }
     }
-    e = final + 1;
+    item -= head.rows;
   }
 }
 
-// One block a query row of a unit: joins the partials of a unit that several blocks shared, and
-// writes the rows of sequences without tokens.
+// One block a query row of a unit: joins the partials of a unit that several blocks shared.
 template <typename T>
-__global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4AttendParams p, int RT, int blocks) {
+__global__ void __launch_bounds__(kMergeThreads)
+    kv4_merge_kernel(const __grid_constant__ Kv4AttendParams p, int RT, int blocks) {
   __shared__ float4 acc_s[kMergeWarps][32];
   __shared__ float max_s[kMergeWarps], sum_s[kMergeWarps];
-  __shared__ float weight[kKv4MaxSms];
-  static_assert(kKv4MaxSms <= kMergeThreads, "a thread for each part");
   // Lengths and row offsets may be read at once: the attention kernel lets this one start only after it has
   // itself waited for all that came before it.
   pdl_launch_dependents();
@@ -763,64 +798,83 @@ __global__ void __launch_bounds__(kMergeThreads) kv4_merge_kernel(Kv4AttendParam
   const Seq s = sequence(p, b, RT);
   const int rows_all = s.n * p.G;                       // query rows of a head
   const int h = blockIdx.x % p.c.Hkv;
-  long long before = 0;
-  const Line line(line_length(p, RT, b, &before), blocks);
+  int before = 0, W = 0;
+#pragma unroll 1
+  for (int i = lane; i - lane < p.c.B; i += 32) {
+    const int n = i < p.c.B ? sequence(p, i, RT).count : 0;
+    W += __reduce_add_sync(0xffffffffu, n);
+    before += __reduce_add_sync(0xffffffffu, i < b ? n : 0);
+  }
+  const Line line(W, blocks);
   pdl_wait();
-  for (int qrow = blockIdx.x / p.c.Hkv; qrow < rows_all; qrow += gridDim.x / p.c.Hkv) {
-    const size_t at = head_row(p, s.r0, h, qrow);
-    if (s.nt == 0) {
-      if (warp == 0) finish<T>(p, at, lane, 0.f, 0.f, make_float4(0.f, 0.f, 0.f, 0.f));
-      continue;
-    }
+#pragma unroll 1
+  for (int qrow = blockIdx.x / p.c.Hkv; qrow < rows_all && s.nt > 0; qrow += gridDim.x / p.c.Hkv) {
     const int rt = qrow / RT, row = qrow % RT;
-    const long long u0 = before + (static_cast<long long>(h) * s.nrt + rt) * s.nt;
+    const int u0 = before + (h * s.nrt + rt) * s.nt;
     const int c0 = line.block_of(u0), c1 = line.block_of(u0 + s.nt - 1);
     if (c0 == c1) continue;
     const int late = line.begin(c0) == u0 ? 0 : 1;   // the unit is its first block's last segment
     const float* slots = p.parts + static_cast<size_t>(2 * c0) * RT * (kD + 2);
-    const int parts = c1 - c0 + 1;                   // at most kKv4MaxSms
+    const int parts = c1 - c0 + 1;
     auto slot_of = [&](int i) { return slots + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * RT * (kD + 2); };
-    float mi = -INFINITY, li = 0.f;
-    if (tid < parts) {
-      mi = slot_of(tid)[row];
-      li = slot_of(tid)[RT + row];
-    }
-    const float wm = warp_max(mi);
-    if (lane == 0) max_s[warp] = wm;
-    __syncthreads();
-    float m = max_s[0];
-#pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, max_s[w]);
-    const float x = tid < parts ? fast_exp2(mi - m) : 0.f;
-    if (tid < parts) weight[tid] = x;
-    const float ls = warp_sum(x * li);
-    if (lane == 0) sum_s[warp] = ls;
-    __syncthreads();
+    // a warp takes every eighth part, four in flight
+    float m = -1e30f, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 5
-    for (int i = warp; i < parts; i += kMergeWarps) {
-      const float4 v = *reinterpret_cast<const float4*>(slot_of(i) + 2 * RT + row * kD + lane * 4);
-      const float y = weight[i];
-      acc.x = fmaf(v.x, y, acc.x);
-      acc.y = fmaf(v.y, y, acc.y);
-      acc.z = fmaf(v.z, y, acc.z);
-      acc.w = fmaf(v.w, y, acc.w);
+#pragma unroll 1
+    for (int i0 = warp; i0 < parts; i0 += 4 * kMergeWarps) {
+      float mi[4], li[4];
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = i0 + k * kMergeWarps;
+        const float* slot = slot_of(min(i, parts - 1));
+        mi[k] = slot[row];
+        li[k] = slot[RT + row];
+        v[k] = *reinterpret_cast<const float4*>(slot + 2 * RT + row * kD + lane * 4);
+        if (i >= parts) mi[k] = -INFINITY;
+      }
+      const float next = fmaxf(fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])), m);
+      const float old = fast_exp2(m - next);
+      m = next;
+      l *= old;
+      acc.x *= old;
+      acc.y *= old;
+      acc.z *= old;
+      acc.w *= old;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (i0 + k * kMergeWarps >= parts) break;
+        const float y = fast_exp2(mi[k] - m);
+        l = fmaf(li[k], y, l);
+        acc.x = fmaf(v[k].x, y, acc.x);
+        acc.y = fmaf(v[k].y, y, acc.y);
+        acc.z = fmaf(v[k].z, y, acc.z);
+        acc.w = fmaf(v[k].w, y, acc.w);
+      }
     }
     acc_s[warp][lane] = acc;
+    if (lane == 0) {
+      max_s[warp] = m;
+      sum_s[warp] = l;
+    }
     __syncthreads();
     if (warp == 0) {
-      float l = 0.f;
+      m = max_s[0];
+#pragma unroll
+      for (int w = 1; w < kMergeWarps; ++w) m = fmaxf(m, max_s[w]);
+      l = 0.f;
       acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kMergeWarps; ++w) {
+        const float y = fast_exp2(max_s[w] - m);
         const float4 v = acc_s[w][lane];
-        l += sum_s[w];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
+        l = fmaf(sum_s[w], y, l);
+        acc.x = fmaf(v.x, y, acc.x);
+        acc.y = fmaf(v.y, y, acc.y);
+        acc.z = fmaf(v.z, y, acc.z);
+        acc.w = fmaf(v.w, y, acc.w);
       }
-      finish<T>(p, at, lane, m, l, acc);
+      finish<T>(p, head_row(p, s.r0, h, qrow), lane, m, l, acc);
     }
     __syncthreads();
   }
@@ -841,29 +895,39 @@ cudaLaunchConfig_t launch_config(dim3 grid, int threads, size_t smem, cudaStream
 }
 
 template <typename T, int NR, Mode M>
-cudaError_t launch_attend_t(const Kv4AttendParams& p, int sms, long long steps, long long units, int max_rows, cudaStream_t stream,
-                            bool pdl) {
+cudaError_t launch_attend_t(Kv4AttendParams p, const Kv4Load& load, int sms, cudaStream_t stream, bool pdl) {
   using S = Shape<NR, M>;
-  cudaError_t e = ensure_dyn_smem<kv4_attend_kernel<T, NR, M>>(S::total);
+  cudaError_t e = ensure_dyn_smem<kv4_attend_kernel<T, NR, M>>(S::max_warps * S::of_warp);
   if (e != cudaSuccess) return e;
   const long long most = std::min(sms, kKv4MaxSms);
-  // a share of at least one step a warp, but of no more units than there are SMs for
-  const int blocks = static_cast<int>(std::max(1ll, std::min(most, std::max(units, (steps + S::warps - 1) / S::warps))));
+  // Solo: blocks take whole units. Their longest share is then longer than the mean by what is compared here,
+  // and the joint work is spared, which takes as long as about kSoloSteps steps of a block. Measured, solo and
+  // shared (us): 32 sequences x 8 heads of 500 tokens 11.8 and 17.6, 64 x 8 of 200 13.5 and 22.0, 13 x 8 of 1500
+  // 14.2 and 16.5, five rows a sequence on 16 x 8 of 5000 47 and 59; 8 units of 1000 are even.
+  const long long rounds = (load.units + most - 1) / most;
+  p.solo = rounds * load.longest - load.steps / most <= kSoloSteps ? 1 : 0;
+  // Steps are spread over the SMs before they are over the warps of one (a block's warps share its issue slots),
+  // and there are no more warps than steps.
+  const long long per_block = p.solo ? rounds * load.longest : (load.steps + most - 1) / most;
+  const int warps = static_cast<int>(std::max(1ll, std::min<long long>(S::max_warps, per_block)));
+  const int blocks =
+      static_cast<int>(std::max(1ll, std::min(most, p.solo ? load.units : (load.steps + warps - 1) / warps)));
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = launch_config(dim3(blocks), S::warps * 32, S::total, stream, attr, pdl);
+  cudaLaunchConfig_t cfg = launch_config(dim3(blocks), warps * 32, warps * S::of_warp, stream, attr, pdl);
   e = cudaLaunchKernelEx(&cfg, kv4_attend_kernel<T, NR, M>, p);
-  if (e != cudaSuccess) return e;
-  cfg = launch_config(dim3(p.c.Hkv * std::max(1, max_rows), p.c.B), kMergeThreads, 0, stream, attr, pdl);
+  if (e != cudaSuccess || p.solo) return e;
+  cfg = launch_config(dim3(p.c.Hkv * std::max(1, load.max_rows), p.c.B), kMergeThreads, 0, stream, attr, pdl);
   return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<T>, p, static_cast<int>(S::RT), blocks);
 }
 
 template <typename T>
-cudaError_t launch_16(int rows, const Kv4AttendParams& p, int sms, long long steps, long long units, int max_rows, cudaStream_t stream,
+cudaError_t launch_16(int rows, const Kv4AttendParams& p, const Kv4Load& load, int sms, cudaStream_t stream,
                       bool pdl) {
   switch (rows) {
-    case 8: return launch_attend_t<T, 1, kHi>(p, sms, steps, units, max_rows, stream, pdl);
-    case 16: return launch_attend_t<T, 2, kHi>(p, sms, steps, units, max_rows, stream, pdl);
-    case 32: return launch_attend_t<T, 4, kHi>(p, sms, steps, units, max_rows, stream, pdl);
+    case 8: return launch_attend_t<T, 1, kHi>(p, load, sms, stream, pdl);
+    case 16: return launch_attend_t<T, 2, kHi>(p, load, sms, stream, pdl);
+    case 24: return launch_attend_t<T, 3, kHi>(p, load, sms, stream, pdl);
+    case 32: return launch_attend_t<T, 4, kHi>(p, load, sms, stream, pdl);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -874,24 +938,24 @@ int kv4_attend_step_tokens() { return kStepTok; }
 
 int kv4_attend_rows(int dtype, int max_rows) {
   if (dtype == HSA_F32) return max_rows <= 4 ? 4 : max_rows <= 8 ? 8 : 16;
-  return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 32;
+  return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 24 ? 24 : 32;
 }
 
-// Two slots a block and one a warp: of 8 rows with 16 warps, of up to 32 with 8.
+// Two slots a block and one a warp: 18 of 8 rows, 14 of 16, 12 of 24, 10 of 32.
 size_t kv4_attend_part_bytes() {
   return static_cast<size_t>(2 + 8) * kKv4MaxSms * 32 * (kD + 2) * sizeof(float);
 }
 
-cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, int sms, long long steps, long long units, int max_rows,
+cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, const Kv4Load& load, int sms,
                               cudaStream_t stream, bool pdl) {
   switch (dtype) {
-    case HSA_BF16: return launch_16<__nv_bfloat16>(rows, p, sms, steps, units, max_rows, stream, pdl);
-    case HSA_F16: return launch_16<__half>(rows, p, sms, steps, units, max_rows, stream, pdl);
+    case HSA_BF16: return launch_16<__nv_bfloat16>(rows, p, load, sms, stream, pdl);
+    case HSA_F16: return launch_16<__half>(rows, p, load, sms, stream, pdl);
     case HSA_F32:
       switch (rows) {
-        case 4: return launch_attend_t<float, 1, kPack>(p, sms, steps, units, max_rows, stream, pdl);
-        case 8: return launch_attend_t<float, 1, kHiLo>(p, sms, steps, units, max_rows, stream, pdl);
-        case 16: return launch_attend_t<float, 2, kHiLo>(p, sms, steps, units, max_rows, stream, pdl);
+        case 4: return launch_attend_t<float, 1, kPack>(p, load, sms, stream, pdl);
+        case 8: return launch_attend_t<float, 1, kHiLo>(p, load, sms, stream, pdl);
+        case 16: return launch_attend_t<float, 2, kHiLo>(p, load, sms, stream, pdl);
       }
       return cudaErrorInvalidValue;
     default: return cudaErrorInvalidValue;
