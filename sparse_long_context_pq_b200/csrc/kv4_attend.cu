@@ -39,7 +39,7 @@ constexpr int kStep = 2;            // tiles a step
 constexpr int kStepTok = kStep * kTileTok;
 constexpr int kStepBytes = kStep * kTileBytes;
 constexpr float kHead = 11.f, kGrow = 4.f;
-constexpr int kSoloSteps = 32;
+constexpr int kSoloSteps = 16;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kPitch = kD + 4;      // floats a row of a warp's partial in shared memory
@@ -901,11 +901,11 @@ cudaError_t launch_attend_t(Kv4AttendParams p, const Kv4Load& load, int sms, cud
   if (e != cudaSuccess) return e;
   const long long most = std::min(sms, kKv4MaxSms);
   // Solo: blocks take whole units. Their longest share is then longer than the mean by what is compared here,
-  // and the joint work is spared, which takes as long as about kSoloSteps steps of a block. Measured, solo and
-  // shared (us): 32 sequences x 8 heads of 500 tokens 11.8 and 17.6, 64 x 8 of 200 13.5 and 22.0, 13 x 8 of 1500
-  // 14.2 and 16.5, five rows a sequence on 16 x 8 of 5000 47 and 59; 8 units of 1000 are even.
+  // and the joint work is spared, which takes as long as about kSoloSteps steps of a block for eight rows. Measured,
+  // solo and shared (us): 32 sequences x 8 heads of 500 tokens 11.8 and 17.6, 64 x 8 of 200 13.5 and 22.0, 13 x 8 of
+  // 1500 14.2 and 16.5, 20 rows on 16 x 8 of 5000 47 and 59; but 8 units of 1000 12.0 and 8.9, of 512 9.9 and 9.4.
   const long long rounds = (load.units + most - 1) / most;
-  p.solo = rounds * load.longest - load.steps / most <= kSoloSteps ? 1 : 0;
+  p.solo = rounds * load.longest - load.steps / most <= kSoloSteps * NR ? 1 : 0;
   // Steps are spread over the SMs before they are over the warps of one (a block's warps share its issue slots),
   // and there are no more warps than steps.
   const long long per_block = p.solo ? rounds * load.longest : (load.steps + most - 1) / most;
