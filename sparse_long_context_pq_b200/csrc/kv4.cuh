@@ -118,6 +118,10 @@ struct Kv4Load {
 cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, const Kv4Load& load, int sms,
                               cudaStream_t stream, bool pdl);
 
+// Many query rows a KV head, 16-bit types (kv4_prefill.cu); p.cu is not null.
+size_t kv4_prefill_part_bytes();
+cudaError_t launch_kv4_prefill(int dtype, const Kv4AttendParams& p, int sms, cudaStream_t stream, bool pdl);
+
 // api.cu
 int device_sms();      // multiprocessors of the current device, 0 on an error
 bool pdl_enabled();

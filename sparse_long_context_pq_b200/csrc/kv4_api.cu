@@ -15,6 +15,7 @@ namespace {
 
 constexpr int kMaxGroup = 128;      // query heads a KV head
 constexpr int kMaxBatch = 65535;    // grid rows
+constexpr int kFewRows = 32;        // query rows a KV head up to which the streaming kernel is used
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -39,7 +40,9 @@ hsa_status check_kv4(const hsa_kv4_cache* kv) {
   return HSA_OK;
 }
 
-size_t workspace_bytes() { return sizeof(WsHeader) + align_up(kv4_attend_part_bytes(), 256); }
+size_t workspace_bytes() {
+  return sizeof(WsHeader) + align_up(std::max(kv4_attend_part_bytes(), kv4_prefill_part_bytes()), 256);
+}
 
 hsa_status check_workspace(const void* ws, size_t bytes) {
   return !ws || !aligned(ws, 256) || bytes < workspace_bytes() ? HSA_ERR_WORKSPACE : HSA_OK;
@@ -133,6 +136,8 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   p.G = kv->Hq / kv->Hkv;
   p.inv_G = static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G);   // not used for G = 1
   p.scale = scale;
+  if (cu && dtype != HSA_F32 && most * p.G > kFewRows)
+    return launch_kv4_prefill(dtype, p, sms, stream, pdl_enabled()) == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
   const int rows = kv4_attend_rows(dtype, most * p.G);
   Kv4Load load = {0, 0, 0, most * p.G};
   const int step = kv4_attend_step_tokens();
