@@ -6,23 +6,27 @@
 // every block, one an SM, takes an equal share of it; units that cross blocks leave a partial a
 // block, which the merge kernel joins.
 //
-// A block has 17 warps:
-//   warps 0-3, 4-7    softmax of rows 0-127 and 128-255, one row a thread: S from TMEM, weights
-//                     2^(S f - ref) as fp16 back into TMEM over S, now and then O scaled down;
-//   warps 8-11, 12-15 keys and values: codes x scales to fp16 (exact) in 128-byte-swizzled shared
-//                     memory, two stages of 128 tokens each, the next tokens' codes in registers;
-//   warp 16           one lane issues the MMAs: S = Q K^T (both operands in shared memory, K-major)
-//                     and O += P V (P in TMEM, V with dims contiguous), M = N = 128, the two row
-//                     halves in turn, so that one's products run under the other's softmax.
+// A block has 13 warps, each walking through the block's segments for itself:
+//   warps 0-3, 4-7  softmax of rows 0-127 and 128-255, one row a thread: S from TMEM, weights
+//                   2^(S f - ref) as fp16 back into TMEM over S, now and then O scaled down;
+//   warps 8-11      keys and values: codes x scales to fp16 (exact) in 128-byte-swizzled shared
+//                   memory, two stages of 128 tokens each, the next tokens' codes in registers;
+//   warp 12         one lane issues the MMAs: S = Q K^T (both operands in shared memory, K-major)
+//                   and O += P V (P in TMEM, V with dims contiguous), M = N = 128, the two row
+//                   halves in turn, so that one's products run under the other's softmax.
+// A unit of at most 128 rows gives both halves the same rows, one the even steps and one the odd
+// ones; their sums are joined at the end.
 // TMEM: S of both halves (128 columns each; P takes the first 64), O of both (128 each).
 // The MMAs of a block run in the order of their issue: P V of a half is issued before the next
 // S of that half overwrites P, and S full means that every earlier P V has been added to O.
 //
 // What bounds it: the tensor cores need 2048 clocks for a step (4 x 128 x 128 x 128 products),
-// ex2 as many (256 x 128 at 16 a clock), shared memory about 2000 (operands and dequantised tiles).
+// ex2 as many (256 x 128 at 16 a clock; a quarter of the weights is therefore a polynomial on the
+// FMA pipes), shared memory about 2000 (operands and dequantised tiles).
 //
 // q, weights and their accuracy are those of kv4_attend.cu for 16-bit calls: q over a power of two
-// in fp16, P in fp16 up to 2^(kHead + kGrow), sums and statistics in fp32.
+// in fp16, P in fp16 up to 2^(kHead + kGrow), sums and statistics in fp32. ref moves by whole
+// numbers, so that weights and sums made before are scaled exactly.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -36,8 +40,10 @@ namespace {
 constexpr int kRows = 256;                      // query rows of a unit
 constexpr int kStepTok = 128;
 constexpr int kStepTiles = kStepTok / kTileTok;
-constexpr int kThreads = 17 * 32;
+constexpr int kMmaWarp = 12;
+constexpr int kThreads = 13 * 32;
 constexpr float kHead = 11.f, kGrow = 4.f;
+constexpr int kPolyPair = 0;                    // of four pairs of weights, the one by poly_exp2
 constexpr uint32_t kOperand = 128 * kD * 2;     // 32 KB: 128 rows of 128 fp16
 constexpr uint32_t kHalfOp = kOperand / 2;      // one 64-element half (128 bytes a row)
 constexpr int kSlot = kRows * (kD + 2);         // floats of a partial: m, l, acc
@@ -46,8 +52,7 @@ struct Smem {
   static constexpr uint32_t q = 0;              // two halves of rows
   static constexpr uint32_t k = 2 * kOperand;   // two stages
   static constexpr uint32_t v = k + 2 * kOperand;
-  static constexpr uint32_t factor = v + 2 * kOperand;          // float [256]: logits from S, in log2 units
-  static constexpr uint32_t poison = factor + kRows * 4;        // u32 [4 steps][8 dim groups][4 x 32 tokens]
+  static constexpr uint32_t poison = v + 2 * kOperand;          // u32 [4 steps][8 dim groups][4 x 32 tokens]
   static constexpr uint32_t flags = poison + 4 * 8 * 4 * 4;     // u32 [4 steps][4 warps]
   static constexpr uint32_t bars = flags + 4 * 4 * 4;
   static constexpr uint32_t total = bars + 32 * 8;
@@ -118,6 +123,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -127,9 +140,73 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// As mbar_wait_warp, the hardware holding the polling lane for up to 20 us at a time.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* err) {
+  uint64_t t0 = 0;
+  while (true) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+    const uint64_t t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) break;
+  }
+  record_error(err, HSA_DEVERR_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, int32_t* err) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_long(bar, parity, err);
+  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+// Largest of three, NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two floats as the register pair that the f32x2 instructions take, and back (moves that the allocator removes).
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(unsigned long long v) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fmul2_rn(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 2^y of two numbers up to 127 without ex2: y = n + r with n whole and |r| <= 1/2, 2^r by a polynomial of degree
+// four (least relative error on that interval, fitted for this: 2.6e-6, against 2^-12 of the fp16 it is rounded
+// to), n added to its exponent. Numbers below -126 count as -126.
+__device__ __forceinline__ float2 poly_exp2(float2 y) {
+  const unsigned long long v = pair(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f));
+  const unsigned long long t = fadd2_rn(v, pair(12582912.f, 12582912.f));   // the whole part in its last bits
+  const unsigned long long n = fadd2_rn(t, pair(-12582912.f, -12582912.f));
+  const unsigned long long r = ffma2_rn(n, pair(-1.f, -1.f), v);
+  unsigned long long e = ffma2_rn(r, pair(0.009570102207362652f, 0.009570102207362652f),
+                                  pair(0.05591785907745361f, 0.05591785907745361f));
+  e = ffma2_rn(r, e, pair(0.240247443318367f, 0.240247443318367f));
+  e = ffma2_rn(r, e, pair(0.6931217908859253f, 0.6931217908859253f));
+  e = ffma2_rn(r, e, pair(0.9999992847442627f, 0.9999992847442627f));
+  const float2 ee = unpair(e), tt = unpair(t);
+  return make_float2(__int_as_float(__float_as_int(ee.x) + (__float_as_int(tt.x) << 23)),
+                     __int_as_float(__float_as_int(ee.y) + (__float_as_int(tt.y) << 23)));
+}
+
 template <typename T>
-__device__ __forceinline__ float4 load_q4(const uint8_t* at) {
-  const uint2 v = __ldg(reinterpret_cast<const uint2*>(at));
+__device__ __forceinline__ float4 q4_of(uint2 v) {
   if (sizeof(T) == 2 && __is_same(T, __nv_bfloat16)) return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&v.x));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
@@ -183,12 +260,81 @@ __device__ __forceinline__ int head_steps(const Kv4AttendParams& p, const Seq& s
 
 // A piece of a unit: what a block works on at a time.
 struct Segment {
-  int b, h, rt;
+  int b, h;
   int T, n, r0, row0, rows;
   int k0, k1;            // steps of the sequence
   int open;              // bits: begins at its unit's first step, ends at its last
   int slot;              // of the workspace, where it is not the whole unit
-  int valid;
+};
+
+// A block's share of the line, walked through segment by segment by a whole warp.
+struct Walk {
+  int g, end, b, h, rt, in_unit, count;
+  Seq s;
+  __device__ __forceinline__ Walk(const Kv4AttendParams& p) : b(0), h(0), rt(0), in_unit(0), count(0) {
+    int W = 0;
+#pragma unroll 1
+    for (int i = 0; i < p.c.B; ++i) W += head_steps(p, sequence(p, i)) * p.c.Hkv;
+    const int N = min(static_cast<int>(gridDim.x), W), c = blockIdx.x;
+    if (c >= N) {
+      g = end = 0;
+      return;
+    }
+    const int each = W / N, rest = W - each * N;
+    g = each * c + min(c, rest);
+    end = g + each + (c < rest ? 1 : 0);
+    int left = g;
+#pragma unroll 1
+    for (;; ++b) {
+      s = sequence(p, b);
+      const int of_head = head_steps(p, s);
+      if (left < of_head * p.c.Hkv) {
+        h = left / of_head;
+        left -= h * of_head;
+        break;
+      }
+      left -= of_head * p.c.Hkv;
+    }
+#pragma unroll 1
+    for (;; ++rt) {
+      const int2 u = unit_steps(p, s, rt);
+      if (left < u.y - u.x) break;
+      left -= u.y - u.x;
+    }
+    in_unit = left;
+  }
+  __device__ __forceinline__ bool next(const Kv4AttendParams& p, Segment& n) {
+    if (g >= end) return false;
+    int2 u = unit_steps(p, s, rt);
+#pragma unroll 1
+    while (in_unit >= u.y - u.x) {   // next unit with steps
+      in_unit = 0;
+      if (++rt >= s.nrt) {
+        rt = 0;
+        if (++h >= p.c.Hkv) {
+          h = 0;
+          if (++b >= p.c.B) return false;
+          s = sequence(p, b);
+        }
+      }
+      u = s.nrt ? unit_steps(p, s, rt) : make_int2(0, 0);
+    }
+    n.b = b;
+    n.h = h;
+    n.T = s.T;
+    n.n = s.n;
+    n.r0 = s.r0;
+    n.row0 = rt * kRows;
+    n.rows = min(kRows, s.n * p.G - n.row0);
+    n.k0 = u.x + in_unit;
+    n.k1 = min(u.y, n.k0 + end - g);
+    n.open = (in_unit == 0 ? 1 : 0) | (n.k1 == u.y ? 2 : 0);
+    n.slot = 2 * static_cast<int>(blockIdx.x) + (n.open == 1 && count > 0 ? 1 : 0);
+    ++count;
+    g += n.k1 - n.k0;
+    in_unit += n.k1 - n.k0;
+    return true;
+  }
 };
 
 // What the merge kernel knows of a slot.
@@ -204,10 +350,10 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_constant__ Kv4AttendParams p) {
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-  __shared__ Segment seg;
   __shared__ uint32_t tmem_slot;
-  __shared__ int failed;
-  float* factor = reinterpret_cast<float*>(sm + Smem::factor);
+  __shared__ float factor[kRows];     // logits from S, in log2 units
+  __shared__ float2 other[128];       // ref and l of the odd steps' half
+  __shared__ unsigned other_poison[128];
   uint32_t* poison_s = reinterpret_cast<uint32_t*>(sm + Smem::poison);
   uint32_t* flags_s = reinterpret_cast<uint32_t*>(sm + Smem::flags);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Smem::bars);
@@ -218,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   uint64_t* s_full = bars + 8;        // [2 halves] commit
   uint64_t* p_full = bars + 10;       // [2 halves] four warps
   uint64_t* o_full = bars + 12;       // commit, once a segment
-  uint64_t* drained = bars + 13;      // commit, at the end
+  uint64_t* q_full = bars + 13;       // eight warps, once a segment
+  uint64_t* drained = bars + 14;      // commit, at the end
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -231,22 +378,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       mbar_init(p_full + i, 4);
     }
     mbar_init(o_full, 1);
+    mbar_init(q_full, 8);
     mbar_init(drained, 1);
     fence_mbar_init();
-    failed = 0;
   }
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                  "r"(512u)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  pdl_wait();
+  pdl_launch_dependents();
+  SlotInfo* info =
+      reinterpret_cast<SlotInfo*>(p.parts + static_cast<size_t>(2 * kKv4MaxSms) * kSlot) + 2 * blockIdx.x;
+  if (tid < 2) info[tid].used = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  pdl_wait();
-  pdl_launch_dependents();
 
   // ---- rows that see nothing: the first n - T query tokens, or all of an empty sequence ----
 #pragma unroll 1
@@ -261,228 +411,227 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     }
   }
 
-  // ---- this block's share of the line (every warp for itself; few sequences, few row tiles) ----
-  int W = 0;
+  Walk walk(p);
+  Segment cur;
+  if (warp < 8) {
+    // ================= q, and softmax: one row a thread =================
+    const int half = warp >> 2;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
+    int done = 0;         // this half's steps so far: phase of its barriers
+    int it = 0;           // the block's steps so far: place of their flags
+    bool ok = true;       // a wait gave up: from there on only the barriers, which all eight warps pass
 #pragma unroll 1
-  for (int b = 0; b < p.c.B; ++b) W += head_steps(p, sequence(p, b)) * p.c.Hkv;
-  const int N = min(static_cast<int>(gridDim.x), W);
-  const int each = N > 0 ? W / N : 0, rest = W - each * N;
-  const int c = blockIdx.x;
-  int g = c < N ? each * c + min(c, rest) : 0;
-  const int g_end = c < N ? g + each + (c < rest ? 1 : 0) : 0;
-  SlotInfo* info = reinterpret_cast<SlotInfo*>(p.parts + static_cast<size_t>(2 * kKv4MaxSms) * kSlot) + 2 * c;
-  if (tid < 2) info[tid].used = 0;
-
-  // Warp 0 walks the line; the others read the segment it leaves.
-  int b = 0, before = 0, of_head = 0, h = 0, rt = 0, in_unit = 0;   // unit and step within it
-  Seq s = {};
-  if (warp == 0 && g < g_end) {
-    for (;; ++b) {
-      s = sequence(p, b);
-      of_head = head_steps(p, s);
-      if (g - before < of_head * p.c.Hkv) break;
-      before += of_head * p.c.Hkv;
-    }
-    h = (g - before) / of_head;
-    in_unit = g - before - h * of_head;
-    for (;; ++rt) {
-      const int2 u = unit_steps(p, s, rt);
-      if (in_unit < u.y - u.x) break;
-      in_unit -= u.y - u.x;
-    }
-  }
-
-  int it = 0;           // steps done by the block: stages and phases
-  int segments = 0;
+    for (int segments = 0; walk.next(p, cur); ++segments) {
+      const int steps = cur.k1 - cur.k0;
+      const bool split = cur.rows <= 128;
+      // ---- q: rows over a power of two (with the scale's sign), fp16, K-major swizzled ----
+      const int mine = split ? 16 : 32;       // rows of this warp
 #pragma unroll 1
-  for (;; ++segments) {
-    if (warp == 0) {
-      Segment n = {};
-      if (g < g_end) {
-        int2 u = unit_steps(p, s, rt);
-        while (in_unit >= u.y - u.x) {   // next unit with steps
-          in_unit = 0;
-          if (++rt == s.nrt) {
-            rt = 0;
-            if (++h == p.c.Hkv) {
-              h = 0;
-              do {
-                s = sequence(p, ++b);
-              } while (b + 1 < p.c.B && s.nrt == 0);
-            }
-          }
-          u = s.nrt ? unit_steps(p, s, rt) : make_int2(0, 0);
+      for (int base = 0; base < mine; base += 8) {
+        uint2 x8[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = min(warp * mine + base + k, cur.rows - 1);
+          const int i = token_of(p, cur.row0 + row);
+          x8[k] = __ldg(reinterpret_cast<const uint2*>(
+              p.q + (static_cast<long long>(cur.r0) + i) * p.q_tok +
+              (static_cast<size_t>(cur.h) * p.G + (cur.row0 + row - i * p.G)) * kD * sizeof(T) + lane * 4 * sizeof(T)));
         }
-        n.b = b;
-        n.h = h;
-        n.rt = rt;
-        n.T = s.T;
-        n.n = s.n;
-        n.r0 = s.r0;
-        n.row0 = rt * kRows;
-        n.rows = min(kRows, s.n * p.G - n.row0);
-        n.k0 = u.x + in_unit;
-        n.k1 = min(u.y, n.k0 + g_end - g);
-        n.open = (in_unit == 0 ? 1 : 0) | (n.k1 == u.y ? 2 : 0);
-        n.slot = 2 * c + (n.open == 1 && segments > 0 ? 1 : 0);
-        n.valid = 1;
-        g += n.k1 - n.k0;
-        in_unit += n.k1 - n.k0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int row = warp * mine + base + k;
+          const float4 x = q4_of<T>(x8[k]);
+          const float top = warp_max_f32(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+          int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
+          e = e > 126 ? 0 : max(e, -126);
+          const float down = copysignf(__int_as_float((127 - e) << 23), p.scale);
+          const int r = row & 127, chunk = (lane & 15) >> 1;
+          *reinterpret_cast<uint2*>(sm + Smem::q + (row >> 7) * kOperand + (lane >> 4) * kHalfOp + r * 128 +
+                                    ((chunk ^ (r & 7)) << 4) + (lane & 1) * 8) =
+              make_uint2(pack_f16x2(x.x * down, x.y * down), pack_f16x2(x.z * down, x.w * down));
+          // never so small that a masked logit, -inf times f, is NaN
+          if (lane == 0) factor[row] = fmaxf(fabsf(p.scale * kLog2e * __int_as_float((e + 127) << 23)), 1e-36f);
+        }
       }
-      if (lane == 0) seg = n;
-    }
-    __syncthreads();
-    if (!seg.valid || failed) break;
-    const Segment cur = seg;
-    const int steps = cur.k1 - cur.k0;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // the factors
 
-    // ---- q: rows over a power of two, fp16, K-major swizzled ----
-#pragma unroll 2
-    for (int row = warp; row < kRows; row += 17) {
-      uint2 w = make_uint2(0u, 0u);
-      float f = 0.f;
-      if (row < cur.rows) {
-        const int i = token_of(p, cur.row0 + row);
-        const float4 x = load_q4<T>(p.q + (static_cast<long long>(cur.r0) + i) * p.q_tok +
-                                    (static_cast<size_t>(cur.h) * p.G + (cur.row0 + row - i * p.G)) * kD * sizeof(T) +
-                                    lane * 4 * sizeof(T));
-        const float top = warp_max_f32(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-        int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
-        e = e > 126 ? 0 : max(e, -126);
-        const float down = __int_as_float((127 - e) << 23);
-        w = make_uint2(pack_f16x2(x.x * down, x.y * down), pack_f16x2(x.z * down, x.w * down));
-        f = p.scale * kLog2e * __int_as_float((e + 127) << 23);
-      }
-      const int r = row & 127, chunk = (lane & 15) >> 1;
-      *reinterpret_cast<uint2*>(sm + Smem::q + (row >> 7) * kOperand + (lane >> 4) * kHalfOp + r * 128 +
-                                ((chunk ^ (r & 7)) << 4) + (lane & 1) * 8) = w;
-      if (lane == 0) factor[row] = f;
-    }
-    fence_proxy_async_smem();
-    __syncthreads();
-
-    if (warp < 8) {
-      // ================= softmax: one row a thread =================
-      const int half = warp >> 2;
-      const int row = tid;                                    // 0 .. 255
-      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
+      const int row = split ? tid & 127 : tid;
       const float f = factor[row];
       const bool real = row < cur.rows;
       const int pos = cur.T - cur.n + token_of(p, cur.row0 + (real ? row : 0));
       const int hi = !real ? -1 : p.causal ? pos : cur.T - 1;
       const int lo = p.window > 0 ? pos - p.window + 1 : 0;
-      float ref = -1e30f, l = 0.f;
-      unsigned poison = 0;
-      bool ok = true;
+      const unsigned long long f2 = pair(f, f);
+      float ref = -1e30f;
+      unsigned long long l2[2] = {0, 0};
+      unsigned poison = 0;          // bits 0-7: dim groups with a value that is not finite, bit 8: the whole row
+      const int first = split ? half : 0, by = split ? 2 : 1;
 #pragma unroll 1
-      for (int j = 0; j < steps; ++j) {
-        if (!mbar_wait_warp(s_full + half, (it + j) & 1, p.c.err)) {
-          ok = false;
-          break;
-        }
+      for (int j = first; ok && j < steps; j += by, ++done) {
+        ok = wait_long_warp(s_full + half, done & 1, p.c.err);
+        if (!ok) break;
         tc_fence_after();
         const int k0 = (cur.k0 + j) * kStepTok;
         const uint4 fl = *reinterpret_cast<const uint4*>(flags_s + ((it + j) & 3) * 4);
         const unsigned flags = fl.x | fl.y | fl.z | fl.w;     // bits 0-7: tiles without a page, bit 8: poison
-        // weight of token j of the step, in the row's reach or not
-        const int from = max(0, lo - k0), to_ = min(kStepTok - 1, hi - k0);   // tokens of the step that the row sees
-        const bool part = from > 0 || to_ < kStepTok - 1 || (flags & 0xffu);
-        const bool masked = __any_sync(0xffffffffu, part);
-        uint32_t x[32];
-        float top = -INFINITY;
-        auto mask32 = [&](int c0) -> uint32_t {   // visible tokens among [c0, c0 + 32)
-          const int a = max(from - c0, 0), z = min(to_ - c0, 31);
+        const int from = max(0, lo - k0), upto = min(kStepTok - 1, hi - k0);   // tokens of the step that the row sees
+        const bool masked = __any_sync(0xffffffffu, from > 0 || upto < kStepTok - 1 || (flags & 0xffu));
+        auto seen32 = [&](int c0) -> uint32_t {   // those among [c0, c0 + 32)
+          const int a = max(from - c0, 0), z = min(upto - c0, 31);
           uint32_t m = a <= z ? (0xffffffffu >> (31 - z)) & (0xffffffffu << a) : 0u;
           const unsigned gone = (flags >> (c0 / kTileTok)) & 3u;
           if (gone & 1u) m &= 0xffff0000u;
           if (gone & 2u) m &= 0x0000ffffu;
           return m;
         };
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld32(ts + q * 32, x);
-          tmem_wait_ld();
-          if (masked) {
-            const uint32_t m = mask32(q * 32);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = __fmul_rn(__uint_as_float(x[i]), f);
-              top = fmaxf(top, (m >> i) & 1u ? y : -INFINITY);
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) top = fmaxf(top, __fmul_rn(__uint_as_float(x[i]), f));
-          }
-        }
-        const bool grow = top > ref + (kHead + kGrow);
-        if (__any_sync(0xffffffffu, grow)) {
-          const float next = grow ? top - kHead : ref;
-          const float shrink = grow ? fast_exp2(ref - next) : 1.f;
-          ref = next;
-          l *= shrink;
-          if (j > 0) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              tmem_ld32(to + q * 32, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * shrink);
-              tmem_st32(to + q * 32, x);
-            }
-            tmem_wait_st();
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          tmem_ld32(ts + q * 32, x);
-          tmem_wait_ld();
-          const uint32_t m = masked ? mask32(q * 32) : 0xffffffffu;
-          uint32_t w[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float y0 = fast_exp2(__fsub_rn(__fmul_rn(__uint_as_float(x[2 * i]), f), ref));
-            float y1 = fast_exp2(__fsub_rn(__fmul_rn(__uint_as_float(x[2 * i + 1]), f), ref));
-            if (masked) {
-              y0 = (m >> (2 * i)) & 1u ? y0 : 0.f;
-              y1 = (m >> (2 * i + 1)) & 1u ? y1 : 0.f;
-            }
-            l += y0 + y1;
-            w[i] = pack_f16x2(y0, y1);
-          }
-          tmem_st16(ts + q * 16, w);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + half);
-        if (flags & 0x100u) {   // values that are not finite, in blocks of 16 dims that the row sees
+        if (flags & 0x100u) {   // values that are not finite, in blocks of 16 dims
           const uint32_t* words = poison_s + ((it + j) & 3) * 32;
 #pragma unroll 1
           for (int gr = 0; gr < 8; ++gr) {
             uint32_t seen = 0;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) seen |= words[gr * 4 + q] & mask32(q * 32);
+            for (int q = 0; q < 4; ++q) seen |= words[gr * 4 + q] & seen32(q * 32);
             if (seen) poison |= 1u << gr;
           }
         }
+        // in two pieces of 64 tokens
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t x[64];
+          tmem_ld32(ts + q * 64, x);
+          tmem_ld32(ts + q * 64 + 32, x + 32);
+          tmem_wait_ld();
+          if (masked) {
+            const uint32_t m0 = seen32(q * 64), m1 = seen32(q * 64 + 32);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              x[i] = (m0 >> i) & 1u ? x[i] : 0xff800000u;
+              x[32 + i] = (m1 >> i) & 1u ? x[32 + i] : 0xff800000u;
+            }
+          }
+          float top = __uint_as_float(x[0]), top1 = __uint_as_float(x[32]);
+#pragma unroll
+          for (int i = 1; i < 31; i += 2) {
+            top = max3_nan(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+            top1 = max3_nan(top1, __uint_as_float(x[32 + i]), __uint_as_float(x[33 + i]));
+          }
+          top = max3_nan(top, __uint_as_float(x[31]), top1);
+          top = __fmul_rn(max3_nan(top, __uint_as_float(x[63]), top1), f);
+          if (__any_sync(0xffffffffu, !(__fsub_rn(top, ref) <= kHead + kGrow))) {
+            if (isnan(top)) poison |= 0x100u;
+            const bool grow = top > ref + (kHead + kGrow);
+            const float next = grow ? ceilf(top) - kHead : ref;
+            const float down = fmaxf(ref - next, -127.f);              // a whole number
+            const float shrink = __int_as_float((static_cast<int>(down) + 127) << 23);   // 0 for 2^-127 and less
+            ref = next;
+            l2[0] = fmul2_rn(l2[0], pair(shrink, shrink));
+            l2[1] = fmul2_rn(l2[1], pair(shrink, shrink));
+            uint32_t y[16];
+            if (j > first) {
+#pragma unroll 1
+              for (int k = 0; k < 8; ++k) {
+                tmem_ld16(to + k * 16, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * shrink);
+                tmem_st16(to + k * 16, y);
+              }
+            }
+            const uint32_t s2 = pack_f16x2(shrink, shrink);
+#pragma unroll 1
+            for (int k = 0; k < 2 * q; ++k) {     // weights of this step that are written already
+              tmem_ld16(ts + k * 16, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = hmul2(y[i], s2);
+              tmem_st16(ts + k * 16, y);
+            }
+          }
+          const unsigned long long ref2 = pair(-ref, -ref);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
+            const float2 y = unpair(fadd2_rn(fmul2_rn(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2), ref2));
+            const float2 e = i % 4 == kPolyPair ? poly_exp2(y) : make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            l2[i & 1] = fadd2_rn(l2[i & 1], pair(e.x, e.y));
+            x[i] = pack_f16x2(e.x, e.y);
+          }
+          tmem_st32(ts + q * 32, x);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + half);
       }
-      if (ok && !mbar_wait_warp(o_full, segments & 1, p.c.err)) ok = false;
-      if (ok) {
-        tc_fence_after();
-        const bool whole = cur.open == 3;
-        const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+      it += steps;
+      ok = ok && wait_long_warp(o_full, segments & 1, p.c.err);
+      tc_fence_after();
+      // ---- the result, or a partial ----
+      const float2 l01 = unpair(fadd2_rn(l2[0], l2[1]));
+      float l = l01.x + l01.y;
+      float mine_w = 1.f, other_w = 0.f;
+      float4* staged = reinterpret_cast<float4*>(sm + Smem::q);   // [32 pieces][128 rows]; the products with q are done
+      const bool none = half >= steps && split;                   // no step: O holds nothing of this segment
+      if (split) {
+        if (half == 1 && ok) {
+          other[row] = make_float2(none ? -1e30f : ref, none ? 0.f : l);
+          other_poison[row] = poison;
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t x[32];
+            tmem_ld32(to + q * 32, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              staged[(q * 8 + i) * 128 + row] =
+                  none ? make_float4(0.f, 0.f, 0.f, 0.f)
+                       : make_float4(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1]),
+                                     __uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3]));
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (half == 0 && ok) {
+          const float2 o = other[row];
+          poison |= other_poison[row];
+          const float m = fmaxf(ref, o.x);
+          mine_w = fast_exp2(ref - m);
+          other_w = fast_exp2(o.x - m);
+          ref = m;
+          l = l * mine_w + o.y * other_w;
+        }
+      }
+      if (ok && (!split || half == 0)) {
+        const bool whole = cur.open == 3, empty = l < 1.f;   // the largest weight is 2^(kHead - 1) or more
+        if (empty) l = 0.f;
+        if (poison & 0x100u) l = __int_as_float(0x7fffffff);
+        const float inv = !whole ? 1.f : empty ? 0.f : __frcp_rn(l);
+        mine_w *= inv;
+        other_w *= inv;
         float* slot = p.parts + static_cast<size_t>(cur.slot) * kSlot;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t x[32];
           tmem_ld32(to + q * 32, x);
           tmem_wait_ld();
-          const float a0 = (poison >> (2 * q)) & 1u ? __int_as_float(0x7fffffff) : 0.f;
-          const float a1 = (poison >> (2 * q + 1)) & 1u ? __int_as_float(0x7fffffff) : 0.f;
+          const float a0 = (poison >> (2 * q)) & 0x101u ? __int_as_float(0x7fffffff) : 0.f;
+          const float a1 = (poison >> (2 * q + 1)) & 0x81u ? __int_as_float(0x7fffffff) : 0.f;
           float y[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(x[i]) * (whole ? inv : 1.f) + (i < 16 ? a0 : a1);
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(x[i]) * mine_w + (i < 16 ? a0 : a1);
+          if (split) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 v = staged[(q * 8 + i) * 128 + row];
+              y[4 * i] = fmaf(v.x, other_w, y[4 * i]);
+              y[4 * i + 1] = fmaf(v.y, other_w, y[4 * i + 1]);
+              y[4 * i + 2] = fmaf(v.z, other_w, y[4 * i + 2]);
+              y[4 * i + 3] = fmaf(v.w, other_w, y[4 * i + 3]);
+            }
+          }
           if (!real) continue;
           if (whole) {
             write_row<T>(p, cur.r0, cur.h, cur.row0 + row, q * 32, y);
@@ -505,23 +654,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         }
         if (!whole && tid == 0)
           info[cur.slot & 1] = SlotInfo{cur.h, cur.r0, cur.row0, cur.rows, cur.open & 1, cur.open >> 1, 1, 0};
-        tc_fence_before();   // O has been read: the next segment's MMAs may overwrite it
-      } else if (lane == 0) {
-        failed = 1;
       }
-    } else if (warp < 16) {
-      // ================= keys (warps 8-11) and values (12-15) =================
-      const bool keys = warp < 12;
-      const int w = warp & 3;                    // tiles 2w, 2w + 1 of a step
-      const int r = lane >> 2, t = lane & 3;
-      uint64_t* full = keys ? k_full : v_full;
-      uint64_t* empty = keys ? k_empty : v_empty;
+      tc_fence_before();
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // O, factors and staged sums have been read
+    }
+  } else if (warp < kMmaWarp) {
+    // ================= keys and values =================
+    const int w = warp & 3;                    // tiles 2w, 2w + 1 of a step
+    const int r = lane >> 2, t = lane & 3;
+    int it = 0;
+    bool ok = true;
+#pragma unroll 1
+    while (ok && walk.next(p, cur)) {
+      const int steps = cur.k1 - cur.k0;
       const int last_tile = (cur.T - 1) / kTileTok;
       int where = -1;                            // lane: cache tile of tile 32 * batch + lane of the segment
-      uint4 code[2][2];
+      int at[2];                                 // cache tiles of the step that is loaded next
+      uint4 kc[2][2], vc[2][2];
       uint2 sc[2];
-      unsigned gone = 0;                         // bits: tiles 2w, 2w + 1 of the loaded step without a page
-      auto load = [&](int j) {
+      auto find = [&](int j) {
         if ((j & 3) == 0) {
           const int tl = (cur.k0 + j) * kStepTiles + lane;
           where = -1;
@@ -530,185 +681,222 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             if (page >= 0) where = static_cast<int>(kv4_tile_index(p.c, page, cur.h, tl));
           }
         }
-        gone = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) at[u] = __shfl_sync(0xffffffffu, where, (j & 3) * kStepTiles + 2 * w + u);
+      };
+      auto fetch = [&](uint4 (&c)[2][2], int off) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int at = __shfl_sync(0xffffffffu, where, (j & 3) * kStepTiles + 2 * w + u);
-          if (at >= 0) {
-            const uint8_t* tile = p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at)) * kTileBytes;
-            const uint4* src = reinterpret_cast<const uint4*>(tile + (keys ? 0 : kOffV)) + lane;
-            code[u][0] = __ldg(src);
-            code[u][1] = __ldg(src + 32);
-            sc[u] = __ldg(reinterpret_cast<const uint2*>(tile + kOffScale) + lane);
-          } else {
-            gone |= 1u << u;
-            code[u][0] = code[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            sc[u] = make_uint2(0u, 0u);
-          }
+          const uint4* src = reinterpret_cast<const uint4*>(
+                                 p.c.cache + static_cast<size_t>(static_cast<uint32_t>(max(at[u], 0))) * kTileBytes + off) +
+                             lane;
+          c[u][0] = at[u] >= 0 ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
+          c[u][1] = at[u] >= 0 ? __ldg(src + 32) : make_uint4(0u, 0u, 0u, 0u);
         }
       };
-      bool ok = true;
-      load(0);
+      auto fetch_scales = [&]() {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          sc[u] = at[u] >= 0 ? __ldg(reinterpret_cast<const uint2*>(p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at[u])) * kTileBytes + kOffScale) + lane)
+                             : make_uint2(0u, 0u);
+      };
+      find(0);
+      fetch(kc, 0);
+      fetch(vc, kOffV);
+      fetch_scales();
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
-        const int stage = (it + j) & 1;
-        uint4 now[2][2] = {{code[0][0], code[0][1]}, {code[1][0], code[1][1]}};
+        const int i_step = it + j, stage = i_step & 1;
+        const uint32_t parity = ((i_step >> 1) & 1) ^ 1;
+        const int left = cur.T - (cur.k0 + j) * kStepTok;   // tokens from the step's first on
         const uint2 scale[2] = {sc[0], sc[1]};
-        const unsigned lost = gone;
-        if (j + 1 < steps) load(j + 1);
-        if (!mbar_wait_warp(empty + stage, (((it + j) >> 1) & 1) ^ 1, p.c.err)) {
+        unsigned bits = (at[0] < 0 ? 1u : 0u) | (at[1] < 0 ? 2u : 0u);
+        bits <<= 2 * w;
+        if (!wait_long_warp(k_empty + stage, parity, p.c.err)) {
           ok = false;
           break;
         }
-        uint8_t* dst = sm + (keys ? Smem::k : Smem::v) + stage * kOperand;
-        const int left = cur.T - (cur.k0 + j) * kStepTok;   // tokens from the step's first on
-        if (keys) {
-          // word i of a row's 16 bytes is dims 32 t + 8 i ..: one 16-byte piece. Lanes with t >= 2 start at word 2:
-          // the eight lanes that store together then meet eight different pieces of the banks.
+        // Word i of a row's 16 bytes is dims 32 t + 8 i ..: one 16-byte piece. Lanes with t >= 2 start at word 2:
+        // the eight lanes that store together then meet eight different pieces of the banks.
+        uint8_t* dst = sm + Smem::k + stage * kOperand;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int row = (2 * w + u) * kTileTok + half * 8 + r;
-              const uint32_t cw[4] = {now[u][half].x, now[u][half].y, now[u][half].z, now[u][half].w};
-              const uint32_t sa = scale_both(scale[u].x, 2 * half), sb = scale_both(scale[u].x, 2 * half + 1);
-              uint8_t* base = dst + (t >> 1) * kHalfOp + row * 128;
+          for (int half = 0; half < 2; ++half) {
+            const int row = (2 * w + u) * kTileTok + half * 8 + r;
+            const uint32_t cw[4] = {kc[u][half].x, kc[u][half].y, kc[u][half].z, kc[u][half].w};
+            const uint32_t sa = scale_both(scale[u].x, 2 * half), sb = scale_both(scale[u].x, 2 * half + 1);
+            uint8_t* base = dst + (t >> 1) * kHalfOp + row * 128;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t word = t & 2 ? cw[i ^ 2] : cw[i];
-                const uint32_t s1 = ((i & 2) != 0) != ((t & 2) != 0) ? sb : sa;
-                const int piece = (t & 1) * 4 + (i ^ (t & 2));
-                uint32_t x[4];
-                e2m1_to_f16x2(word, x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<uint4*>(base + ((piece ^ (row & 7)) << 4)) =
-                    make_uint4(hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1), hmul2(x[3], s1));
-              }
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t word = t & 2 ? cw[i ^ 2] : cw[i];
+              const uint32_t s1 = ((i & 2) != 0) != ((t & 2) != 0) ? sb : sa;
+              const int piece = (t & 1) * 4 + (i ^ (t & 2));
+              uint32_t x[4];
+              e2m1_to_f16x2(word, x[0], x[1], x[2], x[3]);
+              *reinterpret_cast<uint4*>(base + ((piece ^ (row & 7)) << 4)) =
+                  make_uint4(hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1), hmul2(x[3], s1));
             }
           }
-          // what the softmax has to know of the step
-          unsigned info_bits = lost << (2 * w);
-          unsigned bad = 0;
+        }
+        // what the softmax has to know of the step
+        unsigned bad = 0;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t y = scale[u].y;   // values' scales: bytes 248 and up are not finite
-            bad |= y & (y << 1) & (y << 2) & (y << 3) & (y << 4) & 0x80808080u;
-          }
-          if (__any_sync(0xffffffffu, bad != 0u)) {
-            uint32_t word = 0;               // group r: bit = token of this warp's 32
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t y = scale[u].y;   // values' scales: bytes 248 and up are not finite
+          bad |= y & (y << 1) & (y << 2) & (y << 3) & (y << 4) & 0x80808080u;
+        }
+        if (__any_sync(0xffffffffu, bad != 0u)) {
+          uint32_t word = 0;               // group r: bit = token of this warp's 32
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (((scale[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
-            word |= __shfl_xor_sync(0xffffffffu, word, 1);
-            word |= __shfl_xor_sync(0xffffffffu, word, 2);
-            if (t == 0) poison_s[((it + j) & 3) * 32 + r * 4 + w] = word;
-            info_bits |= 0x100u;
-          } else if (t == 0) {
-            poison_s[((it + j) & 3) * 32 + r * 4 + w] = 0u;
-          }
-          if (lane == 0) flags_s[((it + j) & 3) * 4 + w] = info_bits;
-        } else {
-          // the two tokens of a byte part ways; lanes of odd r store the odd token first, against bank conflicts
-          const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
+            for (int i = 0; i < 4; ++i)
+              if (((scale[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
+          word |= __shfl_xor_sync(0xffffffffu, word, 1);
+          word |= __shfl_xor_sync(0xffffffffu, word, 2);
+          if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
+          bits |= 0x100u;
+        } else if (t == 0) {
+          poison_s[(i_step & 3) * 32 + r * 4 + w] = 0u;
+        }
+        if (lane == 0) flags_s[(i_step & 3) * 4 + w] = bits;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + stage);
+        if (j + 1 < steps) {
+          find(j + 1);
+          fetch(kc, 0);
+          fetch_scales();
+        }
+        if (!wait_long_warp(v_empty + stage, parity, p.c.err)) {
+          ok = false;
+          break;
+        }
+        // The two tokens of a byte part ways; lanes of odd r store the odd token first, against bank conflicts.
+        dst = sm + Smem::v + stage * kOperand + (r >> 2) * kHalfOp;
+        const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
-              uint32_t s2 = scale_pair(scale[u].y, 2 * half);
-              if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;         // not finite, or past the end
-              if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
-              const uint32_t cw[4] = {now[u][half].x, now[u][half].y, now[u][half].z, now[u][half].w};
-              uint32_t x[16];
+          for (int half = 0; half < 2; ++half) {
+            const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
+            uint32_t s2 = scale_pair(scale[u].y, 2 * half);
+            if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;         // not finite, or past the end
+            if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
+            const uint32_t cw[4] = {vc[u][half].x, vc[u][half].y, vc[u][half].z, vc[u][half].w};
+            uint32_t x[16];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                e2m1_to_f16x2(cw[i], x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+            for (int i = 0; i < 4; ++i) {
+              e2m1_to_f16x2(cw[i], x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) x[4 * i + q] = hmul2(x[4 * i + q], s2);
-              }
-              uint8_t* base = dst + (r >> 2) * kHalfOp;
+              for (int q = 0; q < 4; ++q) x[4 * i + q] = hmul2(x[4 * i + q], s2);
+            }
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int row = tok + (e ^ (r & 1));
-                const uint32_t sel = e ? sel1 : sel0;
+            for (int e = 0; e < 2; ++e) {
+              const int row = tok + (e ^ (r & 1));
+              const uint32_t sel = e ? sel1 : sel0;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const int piece = (r & 3) * 2 + q;
-                  *reinterpret_cast<uint4*>(base + row * 128 + ((piece ^ (row & 7)) << 4)) =
-                      make_uint4(__byte_perm(x[8 * q], x[8 * q + 1], sel), __byte_perm(x[8 * q + 2], x[8 * q + 3], sel),
-                                 __byte_perm(x[8 * q + 4], x[8 * q + 5], sel), __byte_perm(x[8 * q + 6], x[8 * q + 7], sel));
-                }
+              for (int q = 0; q < 2; ++q) {
+                const int piece = (r & 3) * 2 + q;
+                *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ (row & 7)) << 4)) =
+                    make_uint4(__byte_perm(x[8 * q], x[8 * q + 1], sel), __byte_perm(x[8 * q + 2], x[8 * q + 3], sel),
+                               __byte_perm(x[8 * q + 4], x[8 * q + 5], sel), __byte_perm(x[8 * q + 6], x[8 * q + 7], sel));
               }
             }
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + stage);
+        if (lane == 0) mbar_arrive(v_full + stage);
+        if (j + 1 < steps) fetch(vc, kOffV);
       }
-      if (!ok && lane == 0) failed = 1;
-    } else if (lane == 0) {
-      // ================= MMAs =================
-      const uint32_t q_addr = smem_addr(sm + Smem::q);
-      bool ok = true;
-      auto qk = [&](int half, int stage) {
-        const uint32_t a = q_addr + half * kOperand, bk = smem_addr(sm + Smem::k) + stage * kOperand;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfOp + (kk & 3) * 32;
-          mma_ss(tmem + half * 128, desc_k_major(a + off), desc_k_major(bk + off), kk > 0 ? 1u : 0u);
-        }
-      };
-      auto pv = [&](int half, int stage, bool first) {
-        const uint32_t bv = smem_addr(sm + Smem::v) + stage * kOperand;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, desc_mn_major(bv + kk * 2048),
-                 first && kk == 0 ? 0u : 1u);
-      };
-#pragma unroll 1
-      for (int j = 0; ok && j <= steps; ++j) {
-        const int i = it + j;                      // step j's scores, step j - 1's products with the values
-        const int sk = i & 1, sv = (i - 1) & 1;
-        if (j < steps) {
-          ok = mbar_wait(k_full + sk, (i >> 1) & 1, p.c.err);
-        }
-        if (ok && j > 0) ok = mbar_wait(v_full + sv, ((i - 1) >> 1) & 1, p.c.err);
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (ok && j > 0) {
-            ok = mbar_wait(p_full + half, (i - 1) & 1, p.c.err);
-            tc_fence_after();
-            if (ok) pv(half, sv, j == 1);
-          }
-          if (!ok) break;
-          if (half == 1 && j > 0) tc_commit(v_empty + sv);
-          if (j < steps) {
-            tc_fence_after();
-            qk(half, sk);
-            tc_commit(s_full + half);
-          }
-        }
-        if (ok && j < steps) tc_commit(k_empty + sk);
-      }
-      if (ok) tc_commit(o_full);
-      else failed = 1;
+      it += steps;
     }
-    it += steps;
+  } else {
+    // ================= MMAs: one lane =================
+    const uint32_t q_addr = smem_addr(sm + Smem::q);
+    int it = 0;
+    int made[2] = {0, 0};      // weights waited for, by half
+    bool ok = true;
+    auto qk = [&](int half, int rows_half, int stage) {
+      const uint32_t a = q_addr + rows_half * kOperand, bk = smem_addr(sm + Smem::k) + stage * kOperand;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = (kk >> 2) * kHalfOp + (kk & 3) * 32;
+        mma_ss(tmem + half * 128, desc_k_major(a + off), desc_k_major(bk + off), kk > 0 ? 1u : 0u);
+      }
+      tc_commit(s_full + half);
+    };
+    // weights of a half times the values of step i (of the block), once both are there
+    auto pv = [&](int half, int i, bool fresh) -> bool {
+      if (!wait_long(v_full + (i & 1), (i >> 1) & 1, p.c.err)) return false;
+      if (!wait_long(p_full + half, made[half] & 1, p.c.err)) return false;
+      ++made[half];
+      tc_fence_after();
+      const uint32_t bv = smem_addr(sm + Smem::v) + (i & 1) * kOperand;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, desc_mn_major(bv + kk * 2048),
+               fresh && kk == 0 ? 0u : 1u);
+      return true;
+    };
+#pragma unroll 1
+    for (int segments = 0; walk.next(p, cur); ++segments) {
+      const int steps = cur.k1 - cur.k0;
+      const bool split = cur.rows <= 128;
+      if (lane == 0 && ok) {
+        ok = wait_long(q_full, segments & 1, p.c.err);
+        tc_fence_after();
+        if (split) {      // step j on half j % 2; its values two steps later
+#pragma unroll 1
+          for (int j = 0; ok && j < steps + 2; ++j) {
+            const int i = it + j;
+            if (j < steps && !wait_long(k_full + (i & 1), (i >> 1) & 1, p.c.err)) ok = false;
+            if (ok && j >= 2) {
+              ok = pv(j & 1, i - 2, j < 4);
+              if (ok) tc_commit(v_empty + (i & 1));
+            }
+            if (ok && j < steps) {
+              tc_fence_after();
+              qk(j & 1, 0, i & 1);
+              tc_commit(k_empty + (i & 1));
+            }
+          }
+        } else {          // both halves every step; its values one step later
+#pragma unroll 1
+          for (int j = 0; ok && j <= steps; ++j) {
+            const int i = it + j;
+            if (j < steps && !wait_long(k_full + (i & 1), (i >> 1) & 1, p.c.err)) ok = false;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (ok && j > 0) {
+                ok = pv(half, i - 1, j == 1);
+                if (ok && half == 1) tc_commit(v_empty + ((i - 1) & 1));
+              }
+              if (ok && j < steps) {
+                tc_fence_after();
+                qk(half, half, i & 1);
+              }
+            }
+            if (ok && j < steps) tc_commit(k_empty + (i & 1));
+          }
+        }
+        if (ok) tc_commit(o_full);
+      }
+      __syncwarp();
+      it += steps;
+    }
+    if (lane == 0) {
+      tc_commit(drained);
+      wait_long(drained, 0, p.c.err);   // nothing of ours still writes TMEM
+    }
     __syncwarp();
-    __syncthreads();
-    tc_fence_after();
   }
 
-  if (warp == 16 && lane == 0) {
-    tc_commit(drained);
-    mbar_wait(drained, 0, p.c.err);   // nothing of ours still writes TMEM
-  }
-  __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == 16) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
