@@ -105,16 +105,6 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -203,6 +193,20 @@ __device__ __forceinline__ float2 poly_exp2(float2 y) {
   const float2 ee = unpair(e), tt = unpair(t);
   return make_float2(__int_as_float(__float_as_int(ee.x) + (__float_as_int(tt.x) << 23)),
                      __int_as_float(__float_as_int(ee.y) + (__float_as_int(tt.y) << 23)));
+}
+
+// Loads that leave L1 alone: the cache's bytes pass once.
+__device__ __forceinline__ uint4 load_once16(const uint8_t* at) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 load_once8(const uint8_t* at) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(at));
+  return v;
 }
 
 template <typename T>
@@ -498,29 +502,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             if (seen) poison |= 1u << gr;
           }
         }
-        // in two pieces of 64 tokens
+        // in four pieces of 32 tokens: more at a time spill, and local memory is slow beside 200 KB of shared memory
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t x[64];
-          tmem_ld32(ts + q * 64, x);
-          tmem_ld32(ts + q * 64 + 32, x + 32);
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x[32];
+          tmem_ld32(ts + q * 32, x);
           tmem_wait_ld();
           if (masked) {
-            const uint32_t m0 = seen32(q * 64), m1 = seen32(q * 64 + 32);
+            const uint32_t m = seen32(q * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              x[i] = (m0 >> i) & 1u ? x[i] : 0xff800000u;
-              x[32 + i] = (m1 >> i) & 1u ? x[32 + i] : 0xff800000u;
-            }
+            for (int i = 0; i < 32; ++i) x[i] = (m >> i) & 1u ? x[i] : 0xff800000u;
           }
-          float top = __uint_as_float(x[0]), top1 = __uint_as_float(x[32]);
+          float top = __uint_as_float(x[0]), top1 = __uint_as_float(x[1]);
 #pragma unroll
-          for (int i = 1; i < 31; i += 2) {
+          for (int i = 2; i < 30; i += 4) {
             top = max3_nan(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            top1 = max3_nan(top1, __uint_as_float(x[32 + i]), __uint_as_float(x[33 + i]));
+            top1 = max3_nan(top1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
           }
-          top = max3_nan(top, __uint_as_float(x[31]), top1);
-          top = __fmul_rn(max3_nan(top, __uint_as_float(x[63]), top1), f);
+          top = max3_nan(top, __uint_as_float(x[30]), __uint_as_float(x[31]));
+          top = __fmul_rn(max3_nan(top, top1, top1), f);
           if (__any_sync(0xffffffffu, !(__fsub_rn(top, ref) <= kHead + kGrow))) {
             if (isnan(top)) poison |= 0x100u;
             const bool grow = top > ref + (kHead + kGrow);
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             }
             const uint32_t s2 = pack_f16x2(shrink, shrink);
 #pragma unroll 1
-            for (int k = 0; k < 2 * q; ++k) {     // weights of this step that are written already
+            for (int k = 0; k < q; ++k) {     // weights of this step that are written already
               tmem_ld16(ts + k * 16, y);
               tmem_wait_ld();
 #pragma unroll
@@ -553,14 +553,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           }
           const unsigned long long ref2 = pair(-ref, -ref);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
+          for (int i = 0; i < 16; ++i) {
             // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
             const float2 y = unpair(fadd2_rn(fmul2_rn(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2), ref2));
             const float2 e = i % 4 == kPolyPair ? poly_exp2(y) : make_float2(fast_exp2(y.x), fast_exp2(y.y));
             l2[i & 1] = fadd2_rn(l2[i & 1], pair(e.x, e.y));
             x[i] = pack_f16x2(e.x, e.y);
           }
-          tmem_st32(ts + q * 32, x);
+          tmem_st16(ts + q * 16, x);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -687,17 +687,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       auto fetch = [&](uint4 (&c)[2][2], int off) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint4* src = reinterpret_cast<const uint4*>(
-                                 p.c.cache + static_cast<size_t>(static_cast<uint32_t>(max(at[u], 0))) * kTileBytes + off) +
-                             lane;
-          c[u][0] = at[u] >= 0 ? __ldg(src) : make_uint4(0u, 0u, 0u, 0u);
-          c[u][1] = at[u] >= 0 ? __ldg(src + 32) : make_uint4(0u, 0u, 0u, 0u);
+          const uint8_t* src =
+              p.c.cache + static_cast<size_t>(static_cast<uint32_t>(max(at[u], 0))) * kTileBytes + off + lane * 16;
+          c[u][0] = c[u][1] = make_uint4(0u, 0u, 0u, 0u);
+          if (at[u] >= 0) {
+            c[u][0] = load_once16(src);
+            c[u][1] = load_once16(src + 512);
+          }
         }
       };
       auto fetch_scales = [&]() {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          sc[u] = at[u] >= 0 ? __ldg(reinterpret_cast<const uint2*>(p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at[u])) * kTileBytes + kOffScale) + lane)
+          sc[u] = at[u] >= 0 ? load_once8(p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at[u])) * kTileBytes +
+                                          kOffScale + lane * 8)
                              : make_uint2(0u, 0u);
       };
       find(0);
