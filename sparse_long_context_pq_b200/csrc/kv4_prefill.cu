@@ -6,19 +6,19 @@
 // every block, one an SM, takes an equal share of it; units that cross blocks leave a partial a
 // block, which the merge kernel joins.
 //
-// A block has 13 warps, each walking through the block's segments for itself:
-//   warps 0-3, 4-7  softmax of rows 0-127 and 128-255, one row a thread: S from TMEM, weights
-//                   2^(S f - ref) as fp16 back into TMEM over S, now and then O scaled down;
-//   warps 8-11      keys and values: codes x scales to fp16 (exact) in 128-byte-swizzled shared
-//                   memory, two stages of 128 tokens each, the next tokens' codes in registers;
-//   warp 12         one lane issues the MMAs: S = Q K^T (both operands in shared memory, K-major)
-//                   and O += P V (P in TMEM, V with dims contiguous), M = N = 128, the two row
-//                   halves in turn, so that one's products run under the other's softmax.
+// A block has 16 warps, each walking through the block's segments for itself:
+//   warps 0-3, 4-7    softmax of rows 0-127 and 128-255, one row a thread: S from TMEM, weights
+//                     2^(S f - ref) as fp16 back into TMEM over S, now and then O scaled down. One lane
+//                     of each four issues their MMAs: S = Q K^T (both operands in shared memory, K-major)
+//                     and O += P V (P in TMEM, V with dims contiguous), M = N = 128, so that one half's
+//                     products run under the other's softmax;
+//   warps 8-11, 12-15 keys and values: codes x scales to fp16 (exact) in 128-byte-swizzled shared
+//                     memory, two stages of 128 tokens each, the next tokens' codes in registers.
 // A unit of at most 128 rows gives both halves the same rows, one the even steps and one the odd
 // ones; their sums are joined at the end.
 // TMEM: S of both halves (128 columns each; P takes the first 64), O of both (128 each).
-// The MMAs of a block run in the order of their issue: P V of a half is issued before the next
-// S of that half overwrites P, and S full means that every earlier P V has been added to O.
+// The MMAs of a half are issued by one thread and run in that order: P V of a step before the next
+// S overwrites P, and S full means that every earlier P V has been added to O.
 //
 // What bounds it: the tensor cores need 2048 clocks for a step (4 x 128 x 128 x 128 products),
 // ex2 as many (256 x 128 at 16 a clock; a quarter of the weights is therefore a polynomial on the
@@ -40,9 +40,9 @@ namespace {
 constexpr int kRows = 256;                      // query rows of a unit
 constexpr int kStepTok = 128;
 constexpr int kStepTiles = kStepTok / kTileTok;
-constexpr int kMmaWarp = 12;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 16 * 32;
 constexpr float kHead = 11.f, kGrow = 4.f;
+constexpr int kPiece = 64;                      // tokens of a step that a softmax thread holds at a time
 constexpr int kPolyPair = 0;                    // of four pairs of weights, the one by poly_exp2
 constexpr uint32_t kOperand = 128 * kD * 2;     // 32 KB: 128 rows of 128 fp16
 constexpr uint32_t kHalfOp = kOperand / 2;      // one 64-element half (128 bytes a row)
@@ -130,22 +130,18 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
-// As mbar_wait_warp, the hardware holding the polling lane for up to 20 us at a time.
+// As mbar_wait, with fewer instructions a poll (the waiting warps share issue slots with the working ones): the
+// clock is read every 1024 polls.
 __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* err) {
   uint64_t t0 = 0;
-  while (true) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
-        : "memory");
-    if (done) return true;
-    const uint64_t t = global_ns();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitLimitNs) break;
+#pragma unroll 1
+  for (uint32_t n = 0;; ++n) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((n & 1023u) == 1023u) {
+      const uint64_t t = global_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > kWaitLimitNs) break;
+    }
   }
   record_error(err, HSA_DEVERR_TIMEOUT);
   return false;
@@ -154,6 +150,13 @@ __device__ __forceinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, i
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = wait_long(bar, parity, err);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+}
+// Barriers of the four warps of a half.
+__device__ __forceinline__ void half_barrier(int half) {
+  if (half == 0)
+    asm volatile("bar.sync 2, 128;" ::: "memory");
+  else
+    asm volatile("bar.sync 3, 128;" ::: "memory");
 }
 // Largest of three, NaN if one is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -275,7 +278,14 @@ struct Segment {
 struct Walk {
   int g, end, b, h, rt, in_unit, count;
   Seq s;
-  __device__ __forceinline__ Walk(const Kv4AttendParams& p) : b(0), h(0), rt(0), in_unit(0), count(0) {
+  __device__ __forceinline__ void start(const Kv4AttendParams& p) {
+    Walk w = {};
+    w.find(p);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) *this = w;
+    __syncwarp();
+  }
+  __device__ __forceinline__ void find(const Kv4AttendParams& p) {
     int W = 0;
 #pragma unroll 1
     for (int i = 0; i < p.c.B; ++i) W += head_steps(p, sequence(p, i)) * p.c.Hkv;
@@ -307,7 +317,20 @@ struct Walk {
     }
     in_unit = left;
   }
+  // The next segment into n (shared memory), by a whole warp; false at the end.
   __device__ __forceinline__ bool next(const Kv4AttendParams& p, Segment& n) {
+    Walk w = *this;
+    Segment x;
+    const bool more = w.step(p, x);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+      *this = w;
+      n = x;
+    }
+    __syncwarp();
+    return more;
+  }
+  __device__ __forceinline__ bool step(const Kv4AttendParams& p, Segment& n) {
     if (g >= end) return false;
     int2 u = unit_steps(p, s, rt);
 #pragma unroll 1
@@ -355,6 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint32_t tmem_slot;
+  __shared__ Walk walks[kThreads / 32];
+  __shared__ Segment segments_s[kThreads / 32];
   __shared__ float factor[kRows];     // logits from S, in log2 units
   __shared__ float2 other[128];       // ref and l of the odd steps' half
   __shared__ unsigned other_poison[128];
@@ -362,31 +387,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   uint32_t* flags_s = reinterpret_cast<uint32_t*>(sm + Smem::flags);
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Smem::bars);
   uint64_t* k_full = bars;            // [2] four warps
-  uint64_t* k_empty = bars + 2;       // [2] commit
+  uint64_t* k_empty = bars + 2;       // [2] commits of the halves that read the stage
   uint64_t* v_full = bars + 4;        // [2] four warps
-  uint64_t* v_empty = bars + 6;       // [2] commit
+  uint64_t* v_empty = bars + 6;       // [2] as k_empty
   uint64_t* s_full = bars + 8;        // [2 halves] commit
-  uint64_t* p_full = bars + 10;       // [2 halves] four warps
-  uint64_t* o_full = bars + 12;       // commit, once a segment
-  uint64_t* q_full = bars + 13;       // eight warps, once a segment
-  uint64_t* drained = bars + 14;      // commit, at the end
+  uint64_t* o_full = bars + 10;       // [2 halves] commit, once a segment
+  uint64_t* drained = bars + 12;      // [2 halves] commit, at the end
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 4);
-      mbar_init(k_empty + i, 1);
+      mbar_init(k_empty + i, 2);
       mbar_init(v_full + i, 4);
-      mbar_init(v_empty + i, 1);
+      mbar_init(v_empty + i, 2);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);
+      mbar_init(o_full + i, 1);
+      mbar_init(drained + i, 1);
     }
-    mbar_init(o_full, 1);
-    mbar_init(q_full, 8);
-    mbar_init(drained, 1);
     fence_mbar_init();
   }
-  if (warp == kMmaWarp) {
+  if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
                  "r"(512u)
                  : "memory");
@@ -415,8 +436,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     }
   }
 
-  Walk walk(p);
-  Segment cur;
+  // in shared memory, a copy a warp: the registers are wanted elsewhere
+  Walk& walk = walks[warp];
+  Segment& cur = segments_s[warp];
+  walk.start(p);
   if (warp < 8) {
     // ================= q, and softmax: one row a thread =================
     const int half = warp >> 2;
@@ -427,15 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     bool ok = true;       // a wait gave up: from there on only the barriers, which all eight warps pass
 #pragma unroll 1
     for (int segments = 0; walk.next(p, cur); ++segments) {
-      const int steps = cur.k1 - cur.k0;
+      const int first_step = cur.k0, steps = cur.k1 - first_step;
       const bool split = cur.rows <= 128;
       // ---- q: rows over a power of two (with the scale's sign), fp16, K-major swizzled ----
       const int mine = split ? 16 : 32;       // rows of this warp
 #pragma unroll 1
-      for (int base = 0; base < mine; base += 8) {
-        uint2 x8[8];
+      for (int base = 0; base < mine; base += 16) {
+        uint2 x8[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 16; ++k) {
           const int row = min(warp * mine + base + k, cur.rows - 1);
           const int i = token_of(p, cur.row0 + row);
           x8[k] = __ldg(reinterpret_cast<const uint2*>(
@@ -443,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
               (static_cast<size_t>(cur.h) * p.G + (cur.row0 + row - i * p.G)) * kD * sizeof(T) + lane * 4 * sizeof(T)));
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < 16; ++k) {
           const int row = warp * mine + base + k;
           const float4 x = q4_of<T>(x8[k]);
           const float top = warp_max_f32(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
@@ -459,9 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         }
       }
       fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-      asm volatile("bar.sync 1, 256;" ::: "memory");   // the factors
+      asm volatile("bar.sync 1, 256;" ::: "memory");   // q and its factors
 
       const int row = split ? tid & 127 : tid;
       const float f = factor[row];
@@ -474,12 +495,52 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       unsigned long long l2[2] = {0, 0};
       unsigned poison = 0;          // bits 0-7: dim groups with a value that is not finite, bit 8: the whole row
       const int first = split ? half : 0, by = split ? 2 : 1;
-#pragma unroll 1
-      for (int j = first; ok && j < steps; j += by, ++done) {
-        ok = wait_long_warp(s_full + half, done & 1, p.c.err);
-        if (!ok) break;
+      // ---- this half's MMAs, by one lane ----
+      auto qk = [&](int j) {        // S of step j; its keys are then free, for this half
+        const int i = it + j;
+        if (!wait_long(k_full + (i & 1), (i >> 1) & 1, p.c.err)) return false;
         tc_fence_after();
-        const int k0 = (cur.k0 + j) * kStepTok;
+        const uint32_t a = smem_addr(sm + Smem::q) + (split ? 0 : half) * kOperand;
+        const uint32_t bk = smem_addr(sm + Smem::k) + (i & 1) * kOperand;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * kHalfOp + (kk & 3) * 32;
+          mma_ss(tmem + half * 128, desc_k_major(a + off), desc_k_major(bk + off), kk > 0 ? 1u : 0u);
+        }
+        tc_commit(s_full + half);
+        tc_commit(k_empty + (i & 1));
+        if (split) mbar_arrive(k_empty + (i & 1));   // the other half does not read it
+        return true;
+      };
+      auto pv = [&](int j) {        // weights of step j times its values
+        const int i = it + j;
+        if (!wait_long(v_full + (i & 1), (i >> 1) & 1, p.c.err)) return false;
+        tc_fence_after();
+        const uint32_t bv = smem_addr(sm + Smem::v) + (i & 1) * kOperand;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, desc_mn_major(bv + kk * 2048),
+                 j == first && kk == 0 ? 0u : 1u);
+        tc_commit(v_empty + (i & 1));
+        if (split) mbar_arrive(v_empty + (i & 1));
+        return true;
+      };
+      const bool leader = (warp & 3) == 0 && lane == 0;
+      if (leader && ok) {
+        if (first < steps) ok = qk(first);
+        else tc_commit(o_full + half);
+      }
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+#pragma unroll 1
+      for (int j = first; j < steps; j += by, ++done) {
+        // a wait that gave up: no more work, but the barriers that the four warps share are still passed
+        if (ok) ok = wait_long_warp(s_full + half, done & 1, p.c.err);
+        if (!ok) {
+          half_barrier(half);
+          continue;
+        }
+        tc_fence_after();
+        const int k0 = (first_step + j) * kStepTok;
         const uint4 fl = *reinterpret_cast<const uint4*>(flags_s + ((it + j) & 3) * 4);
         const unsigned flags = fl.x | fl.y | fl.z | fl.w;     // bits 0-7: tiles without a page, bit 8: poison
         const int from = max(0, lo - k0), upto = min(kStepTok - 1, hi - k0);   // tokens of the step that the row sees
@@ -502,25 +563,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             if (seen) poison |= 1u << gr;
           }
         }
-        // in four pieces of 32 tokens: more at a time spill, and local memory is slow beside 200 KB of shared memory
+        // in pieces of kPiece tokens: more at a time spill, and local memory is slow beside 200 KB of shared memory
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t x[32];
-          tmem_ld32(ts + q * 32, x);
+        for (int q = 0; q < kStepTok / kPiece; ++q) {
+          uint32_t x[kPiece];
+#pragma unroll
+          for (int k = 0; k < kPiece; k += 32) tmem_ld32(ts + q * kPiece + k, x + k);
           tmem_wait_ld();
           if (masked) {
-            const uint32_t m = seen32(q * 32);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = (m >> i) & 1u ? x[i] : 0xff800000u;
-          }
-          float top = __uint_as_float(x[0]), top1 = __uint_as_float(x[1]);
+            for (int k = 0; k < kPiece; k += 32) {
+              const uint32_t m = seen32(q * kPiece + k);
 #pragma unroll
-          for (int i = 2; i < 30; i += 4) {
-            top = max3_nan(top, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-            top1 = max3_nan(top1, __uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+              for (int i = 0; i < 32; ++i) x[k + i] = (m >> i) & 1u ? x[k + i] : 0xff800000u;
+            }
           }
-          top = max3_nan(top, __uint_as_float(x[30]), __uint_as_float(x[31]));
-          top = __fmul_rn(max3_nan(top, top1, top1), f);
+          float tops[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tops[k] = max3_nan(__uint_as_float(x[k]), __uint_as_float(x[k + 4]), __uint_as_float(x[k + 8]));
+#pragma unroll
+          for (int i = 12; i + 8 <= kPiece; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = max3_nan(tops[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + 4 + k]));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tops[k] = max3_nan(tops[k], __uint_as_float(x[kPiece - 4 + k]), tops[k]);
+          const float top = __fmul_rn(max3_nan(max3_nan(tops[0], tops[1], tops[2]), tops[3], tops[3]), f);
           if (__any_sync(0xffffffffu, !(__fsub_rn(top, ref) <= kHead + kGrow))) {
             if (isnan(top)) poison |= 0x100u;
             const bool grow = top > ref + (kHead + kGrow);
@@ -543,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             }
             const uint32_t s2 = pack_f16x2(shrink, shrink);
 #pragma unroll 1
-            for (int k = 0; k < q; ++k) {     // weights of this step that are written already
+            for (int k = 0; k < q * (kPiece / 32); ++k) {     // weights of this step that are written already
               tmem_ld16(ts + k * 16, y);
               tmem_wait_ld();
 #pragma unroll
@@ -553,22 +620,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           }
           const unsigned long long ref2 = pair(-ref, -ref);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < kPiece / 2; ++i) {
             // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
             const float2 y = unpair(fadd2_rn(fmul2_rn(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2), ref2));
             const float2 e = i % 4 == kPolyPair ? poly_exp2(y) : make_float2(fast_exp2(y.x), fast_exp2(y.y));
             l2[i & 1] = fadd2_rn(l2[i & 1], pair(e.x, e.y));
             x[i] = pack_f16x2(e.x, e.y);
           }
-          tmem_st16(ts + q * 16, x);
+#pragma unroll
+          for (int k = 0; k < kPiece / 32; ++k) tmem_st16(ts + (q * kPiece / 32 + k) * 16, x + 16 * k);
         }
         tmem_wait_st();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + half);
+        half_barrier(half);   // this half's weights are there
+        if (leader) {
+          ok = pv(j);
+          if (ok && j + by < steps) ok = qk(j + by);
+          else if (ok) tc_commit(o_full + half);
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       it += steps;
-      ok = ok && wait_long_warp(o_full, segments & 1, p.c.err);
+      ok = ok && wait_long_warp(o_full + half, segments & 1, p.c.err);
       tc_fence_after();
       // ---- the result, or a partial ----
       const float2 l01 = unpair(fadd2_rn(l2[0], l2[1]));
@@ -577,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       float4* staged = reinterpret_cast<float4*>(sm + Smem::q);   // [32 pieces][128 rows]; the products with q are done
       const bool none = half >= steps && split;                   // no step: O holds nothing of this segment
       if (split) {
+        asm volatile("bar.sync 1, 256;" ::: "memory");   // both halves are done with q
         if (half == 1 && ok) {
           other[row] = make_float2(none ? -1e30f : ref, none ? 0.f : l);
           other_poison[row] = poison;
@@ -632,13 +706,33 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
               y[4 * i + 3] = fmaf(v.w, other_w, y[4 * i + 3]);
             }
           }
-          if (!real) continue;
-          if (whole) {
-            write_row<T>(p, cur.r0, cur.h, cur.row0 + row, q * 32, y);
-          } else {
-            float4* at = reinterpret_cast<float4*>(slot + 2 * kRows + row * kD + q * 32);
+          if (!whole) {        // [4 dims][row] of the slot
+            if (real)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) at[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+              for (int i = 0; i < 8; ++i)
+                reinterpret_cast<float4*>(slot + 2 * kRows)[(q * 8 + i) * kRows + row] =
+                    make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else if (split) {
+            if (real) write_row<T>(p, cur.r0, cur.h, cur.row0 + row, q * 32, y);
+          } else {             // through the place of q, a row's 16-byte pieces swizzled
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(sm + Smem::q + row * 256 + (((4 * q + i) ^ (row & 15)) << 4)) =
+                  make_uint4(pack2<T>(y[8 * i], y[8 * i + 1]), pack2<T>(y[8 * i + 2], y[8 * i + 3]),
+                             pack2<T>(y[8 * i + 4], y[8 * i + 5]), pack2<T>(y[8 * i + 6], y[8 * i + 7]));
+          }
+        }
+        if (whole && !split) {
+          __syncwarp();
+#pragma unroll 4
+          for (int k = 0; k < 16; ++k) {     // two rows an instruction
+            const int o = warp * 32 + 2 * k + (lane >> 4);
+            const uint4 v = *reinterpret_cast<const uint4*>(sm + Smem::q + o * 256 + (((lane & 15) ^ (o & 15)) << 4));
+            if (o < cur.rows) {
+              const int i = token_of(p, cur.row0 + o);
+              reinterpret_cast<uint4*>(p.out)[((static_cast<size_t>(cur.r0) + i) * p.c.Hq + cur.h * p.G +
+                                               (cur.row0 + o - i * p.G)) * (kD / 8) + (lane & 15)] = v;
+            }
           }
         }
         if (real) {
@@ -658,248 +752,158 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       tc_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");   // O, factors and staged sums have been read
     }
-  } else if (warp < kMmaWarp) {
-    // ================= keys and values =================
+    if ((warp & 3) == 0 && lane == 0) {
+      tc_commit(drained + half);
+      wait_long(drained + half, 0, p.c.err);   // nothing of ours still writes TMEM
+    }
+    __syncwarp();
+  } else {
+    // ================= keys (warps 8-11) and values (12-15) =================
+    const bool keys = warp < 12;
     const int w = warp & 3;                    // tiles 2w, 2w + 1 of a step
     const int r = lane >> 2, t = lane & 3;
+    uint64_t* full = keys ? k_full : v_full;
+    uint64_t* empty = keys ? k_empty : v_empty;
     int it = 0;
     bool ok = true;
 #pragma unroll 1
     while (ok && walk.next(p, cur)) {
-      const int steps = cur.k1 - cur.k0;
-      const int last_tile = (cur.T - 1) / kTileTok;
+      const int steps = cur.k1 - cur.k0, tokens = cur.T, k0 = cur.k0;
       int where = -1;                            // lane: cache tile of tile 32 * batch + lane of the segment
-      int at[2];                                 // cache tiles of the step that is loaded next
-      uint4 kc[2][2], vc[2][2];
+      unsigned gone = 0;                         // bits: of the loaded tiles, those without a page
+      uint4 code[2][2];
       uint2 sc[2];
-      auto find = [&](int j) {
+      auto load = [&](int j) {
         if ((j & 3) == 0) {
-          const int tl = (cur.k0 + j) * kStepTiles + lane;
+          const int tl = (k0 + j) * kStepTiles + lane;
           where = -1;
-          if (tl <= last_tile && tl < cur.k1 * kStepTiles) {
+          if (tl <= (tokens - 1) / kTileTok && tl < (k0 + steps) * kStepTiles) {
             const int page = kv4_page(p.c, cur.b, tl);
             if (page >= 0) where = static_cast<int>(kv4_tile_index(p.c, page, cur.h, tl));
           }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u) at[u] = __shfl_sync(0xffffffffu, where, (j & 3) * kStepTiles + 2 * w + u);
-      };
-      auto fetch = [&](uint4 (&c)[2][2], int off) {
+        gone = 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t* src =
-              p.c.cache + static_cast<size_t>(static_cast<uint32_t>(max(at[u], 0))) * kTileBytes + off + lane * 16;
-          c[u][0] = c[u][1] = make_uint4(0u, 0u, 0u, 0u);
-          if (at[u] >= 0) {
-            c[u][0] = load_once16(src);
-            c[u][1] = load_once16(src + 512);
+          const int at = __shfl_sync(0xffffffffu, where, (j & 3) * kStepTiles + 2 * w + u);
+          code[u][0] = code[u][1] = make_uint4(0u, 0u, 0u, 0u);
+          sc[u] = make_uint2(0u, 0u);
+          if (at >= 0) {
+            const uint8_t* tile = p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at)) * kTileBytes;
+            const uint8_t* src = tile + (keys ? 0 : kOffV) + lane * 16;
+            code[u][0] = load_once16(src);
+            code[u][1] = load_once16(src + 512);
+            sc[u] = load_once8(tile + kOffScale + lane * 8);
+          } else {
+            gone |= 1u << u;
           }
         }
       };
-      auto fetch_scales = [&]() {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-          sc[u] = at[u] >= 0 ? load_once8(p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at[u])) * kTileBytes +
-                                          kOffScale + lane * 8)
-                             : make_uint2(0u, 0u);
-      };
-      find(0);
-      fetch(kc, 0);
-      fetch(vc, kOffV);
-      fetch_scales();
+      load(0);
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const int i_step = it + j, stage = i_step & 1;
-        const uint32_t parity = ((i_step >> 1) & 1) ^ 1;
-        const int left = cur.T - (cur.k0 + j) * kStepTok;   // tokens from the step's first on
+        const uint4 now[2][2] = {{code[0][0], code[0][1]}, {code[1][0], code[1][1]}};
         const uint2 scale[2] = {sc[0], sc[1]};
-        unsigned bits = (at[0] < 0 ? 1u : 0u) | (at[1] < 0 ? 2u : 0u);
-        bits <<= 2 * w;
-        if (!wait_long_warp(k_empty + stage, parity, p.c.err)) {
+        const unsigned lost = gone;
+        if (j + 1 < steps) load(j + 1);
+        if (!wait_long_warp(empty + stage, ((i_step >> 1) & 1) ^ 1, p.c.err)) {
           ok = false;
           break;
         }
-        // Word i of a row's 16 bytes is dims 32 t + 8 i ..: one 16-byte piece. Lanes with t >= 2 start at word 2:
-        // the eight lanes that store together then meet eight different pieces of the banks.
-        uint8_t* dst = sm + Smem::k + stage * kOperand;
+        if (keys) {
+          // Word i of a row's 16 bytes is dims 32 t + 8 i ..: one 16-byte piece. Lanes with t >= 2 start at word 2:
+          // the eight lanes that store together then meet eight different pieces of the banks.
+          uint8_t* dst = sm + Smem::k + stage * kOperand;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int row = (2 * w + u) * kTileTok + half * 8 + r;
-            const uint32_t cw[4] = {kc[u][half].x, kc[u][half].y, kc[u][half].z, kc[u][half].w};
-            const uint32_t sa = scale_both(scale[u].x, 2 * half), sb = scale_both(scale[u].x, 2 * half + 1);
-            uint8_t* base = dst + (t >> 1) * kHalfOp + row * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t word = t & 2 ? cw[i ^ 2] : cw[i];
-              const uint32_t s1 = ((i & 2) != 0) != ((t & 2) != 0) ? sb : sa;
-              const int piece = (t & 1) * 4 + (i ^ (t & 2));
-              uint32_t x[4];
-              e2m1_to_f16x2(word, x[0], x[1], x[2], x[3]);
-              *reinterpret_cast<uint4*>(base + ((piece ^ (row & 7)) << 4)) =
-                  make_uint4(hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1), hmul2(x[3], s1));
-            }
-          }
-        }
-        // what the softmax has to know of the step
-        unsigned bad = 0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t y = scale[u].y;   // values' scales: bytes 248 and up are not finite
-          bad |= y & (y << 1) & (y << 2) & (y << 3) & (y << 4) & 0x80808080u;
-        }
-        if (__any_sync(0xffffffffu, bad != 0u)) {
-          uint32_t word = 0;               // group r: bit = token of this warp's 32
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (((scale[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
-          word |= __shfl_xor_sync(0xffffffffu, word, 1);
-          word |= __shfl_xor_sync(0xffffffffu, word, 2);
-          if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
-          bits |= 0x100u;
-        } else if (t == 0) {
-          poison_s[(i_step & 3) * 32 + r * 4 + w] = 0u;
-        }
-        if (lane == 0) flags_s[(i_step & 3) * 4 + w] = bits;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(k_full + stage);
-        if (j + 1 < steps) {
-          find(j + 1);
-          fetch(kc, 0);
-          fetch_scales();
-        }
-        if (!wait_long_warp(v_empty + stage, parity, p.c.err)) {
-          ok = false;
-          break;
-        }
-        // The two tokens of a byte part ways; lanes of odd r store the odd token first, against bank conflicts.
-        dst = sm + Smem::v + stage * kOperand + (r >> 2) * kHalfOp;
-        const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
-            uint32_t s2 = scale_pair(scale[u].y, 2 * half);
-            if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;         // not finite, or past the end
-            if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
-            const uint32_t cw[4] = {vc[u][half].x, vc[u][half].y, vc[u][half].z, vc[u][half].w};
-            uint32_t x[16];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              e2m1_to_f16x2(cw[i], x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) x[4 * i + q] = hmul2(x[4 * i + q], s2);
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int row = tok + (e ^ (r & 1));
-              const uint32_t sel = e ? sel1 : sel0;
-#pragma unroll
-              for (int q = 0; q < 2; ++q) {
-                const int piece = (r & 3) * 2 + q;
-                *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ (row & 7)) << 4)) =
-                    make_uint4(__byte_perm(x[8 * q], x[8 * q + 1], sel), __byte_perm(x[8 * q + 2], x[8 * q + 3], sel),
-                               __byte_perm(x[8 * q + 4], x[8 * q + 5], sel), __byte_perm(x[8 * q + 6], x[8 * q + 7], sel));
-              }
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_full + stage);
-        if (j + 1 < steps) fetch(vc, kOffV);
-      }
-      it += steps;
-    }
-  } else {
-    // ================= MMAs: one lane =================
-    const uint32_t q_addr = smem_addr(sm + Smem::q);
-    int it = 0;
-    int made[2] = {0, 0};      // weights waited for, by half
-    bool ok = true;
-    auto qk = [&](int half, int rows_half, int stage) {
-      const uint32_t a = q_addr + rows_half * kOperand, bk = smem_addr(sm + Smem::k) + stage * kOperand;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * kHalfOp + (kk & 3) * 32;
-        mma_ss(tmem + half * 128, desc_k_major(a + off), desc_k_major(bk + off), kk > 0 ? 1u : 0u);
-      }
-      tc_commit(s_full + half);
-    };
-    // weights of a half times the values of step i (of the block), once both are there
-    auto pv = [&](int half, int i, bool fresh) -> bool {
-      if (!wait_long(v_full + (i & 1), (i >> 1) & 1, p.c.err)) return false;
-      if (!wait_long(p_full + half, made[half] & 1, p.c.err)) return false;
-      ++made[half];
-      tc_fence_after();
-      const uint32_t bv = smem_addr(sm + Smem::v) + (i & 1) * kOperand;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, desc_mn_major(bv + kk * 2048),
-               fresh && kk == 0 ? 0u : 1u);
-      return true;
-    };
-#pragma unroll 1
-    for (int segments = 0; walk.next(p, cur); ++segments) {
-      const int steps = cur.k1 - cur.k0;
-      const bool split = cur.rows <= 128;
-      if (lane == 0 && ok) {
-        ok = wait_long(q_full, segments & 1, p.c.err);
-        tc_fence_after();
-        if (split) {      // step j on half j % 2; its values two steps later
-#pragma unroll 1
-          for (int j = 0; ok && j < steps + 2; ++j) {
-            const int i = it + j;
-            if (j < steps && !wait_long(k_full + (i & 1), (i >> 1) & 1, p.c.err)) ok = false;
-            if (ok && j >= 2) {
-              ok = pv(j & 1, i - 2, j < 4);
-              if (ok) tc_commit(v_empty + (i & 1));
-            }
-            if (ok && j < steps) {
-              tc_fence_after();
-              qk(j & 1, 0, i & 1);
-              tc_commit(k_empty + (i & 1));
-            }
-          }
-        } else {          // both halves every step; its values one step later
-#pragma unroll 1
-          for (int j = 0; ok && j <= steps; ++j) {
-            const int i = it + j;
-            if (j < steps && !wait_long(k_full + (i & 1), (i >> 1) & 1, p.c.err)) ok = false;
+          for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if (ok && j > 0) {
-                ok = pv(half, i - 1, j == 1);
-                if (ok && half == 1) tc_commit(v_empty + ((i - 1) & 1));
-              }
-              if (ok && j < steps) {
-                tc_fence_after();
-                qk(half, half, i & 1);
+              const int row = (2 * w + u) * kTileTok + half * 8 + r;
+              const uint32_t cw[4] = {now[u][half].x, now[u][half].y, now[u][half].z, now[u][half].w};
+              const uint32_t sa = scale_both(scale[u].x, 2 * half), sb = scale_both(scale[u].x, 2 * half + 1);
+              uint8_t* base = dst + (t >> 1) * kHalfOp + row * 128;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t word = t & 2 ? cw[i ^ 2] : cw[i];
+                const uint32_t s1 = ((i & 2) != 0) != ((t & 2) != 0) ? sb : sa;
+                const int piece = (t & 1) * 4 + (i ^ (t & 2));
+                uint32_t x[4];
+                e2m1_to_f16x2(word, x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(base + ((piece ^ (row & 7)) << 4)) =
+                    make_uint4(hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1), hmul2(x[3], s1));
               }
             }
-            if (ok && j < steps) tc_commit(k_empty + (i & 1));
+          }
+          // what the softmax has to know of the step
+          unsigned bits = lost << (2 * w), bad = 0;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t y = scale[u].y;   // values' scales: bytes 248 and up are not finite
+            bad |= y & (y << 1) & (y << 2) & (y << 3) & (y << 4) & 0x80808080u;
+          }
+          if (__any_sync(0xffffffffu, bad != 0u)) {
+            uint32_t word = 0;               // group r: bit = token of this warp's 32
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (((scale[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
+            word |= __shfl_xor_sync(0xffffffffu, word, 1);
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+            if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
+            bits |= 0x100u;
+          } else if (t == 0) {
+            poison_s[(i_step & 3) * 32 + r * 4 + w] = 0u;
+          }
+          if (lane == 0) flags_s[(i_step & 3) * 4 + w] = bits;
+        } else {
+          // The two tokens of a byte part ways; lanes of odd r store the odd token first, against bank conflicts.
+          uint8_t* dst = sm + Smem::v + stage * kOperand + (r >> 2) * kHalfOp;
+          const int left = tokens - (k0 + j) * kStepTok;   // tokens from the step's first on
+          const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
+              uint32_t s2 = scale_pair(scale[u].y, 2 * half);
+              if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;         // not finite, or past the end
+              if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
+              const uint32_t cw[4] = {now[u][half].x, now[u][half].y, now[u][half].z, now[u][half].w};
+              uint32_t x[16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                e2m1_to_f16x2(cw[i], x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) x[4 * i + q] = hmul2(x[4 * i + q], s2);
+              }
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int row = tok + (e ^ (r & 1));
+                const uint32_t sel = e ? sel1 : sel0;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const int piece = (r & 3) * 2 + q;
+                  *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ (row & 7)) << 4)) =
+                      make_uint4(__byte_perm(x[8 * q], x[8 * q + 1], sel), __byte_perm(x[8 * q + 2], x[8 * q + 3], sel),
+                                 __byte_perm(x[8 * q + 4], x[8 * q + 5], sel), __byte_perm(x[8 * q + 6], x[8 * q + 7], sel));
+                }
+              }
+            }
           }
         }
-        if (ok) tc_commit(o_full);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full + stage);
       }
-      __syncwarp();
       it += steps;
     }
-    if (lane == 0) {
-      tc_commit(drained);
-      wait_long(drained, 0, p.c.err);   // nothing of ours still writes TMEM
-    }
-    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == 8) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
   }
@@ -917,9 +921,11 @@ __device__ __forceinline__ void write_row(const Kv4AttendParams& p, int r0, int 
                         pack2<T>(x[8 * k + 4], x[8 * k + 5]), pack2<T>(x[8 * k + 6], x[8 * k + 7]));
 }
 
-// Joins the partials of the unit that begins in block blockIdx.x and goes on in the next ones; a warp a row.
+// Joins the partials of the unit that begins in block blockIdx.x and goes on in the next ones: 32 rows x 8 dims a warp.
+constexpr int kMergeWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(256) kv4_prefill_merge_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
+__global__ void __launch_bounds__(kMergeWarps * 32)
+    kv4_prefill_merge_kernel(const __grid_constant__ Kv4AttendParams p, int blocks) {
   pdl_launch_dependents();
   pdl_wait();
   const SlotInfo* info = reinterpret_cast<const SlotInfo*>(p.parts + static_cast<size_t>(2 * kKv4MaxSms) * kSlot);
@@ -933,33 +939,37 @@ __global__ void __launch_bounds__(256) kv4_prefill_merge_kernel(const __grid_con
   if (s0 < 0) return;
   const SlotInfo u = info[s0];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.y * 8 + warp;
-  if (row >= u.rows) return;
+  const int row = blockIdx.y * 32 + lane;
+  if (blockIdx.y * 32 >= u.rows) return;
   int parts = 1;
   while (c + parts < blocks && !info[2 * (c + parts)].ends) ++parts;
   ++parts;   // the one that ends it
-  float m = -1e30f, l = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int d8 = warp; d8 < kD / 8; d8 += kMergeWarps) {
+    float m = -1e30f, l = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll 2
-  for (int i = 0; i < parts; ++i) {
-    const float* slot = p.parts + static_cast<size_t>(i == 0 ? s0 : 2 * (c + i)) * kSlot;
-    const float mi = slot[row], li = slot[kRows + row];
-    const float4 v = *reinterpret_cast<const float4*>(slot + 2 * kRows + row * kD + lane * 4);
-    const float next = fmaxf(m, mi);
-    const float x = fast_exp2(m - next), y = fast_exp2(mi - next);
-    m = next;
-    l = fmaf(l, x, li * y);
-    acc.x = fmaf(acc.x, x, v.x * y);
-    acc.y = fmaf(acc.y, x, v.y * y);
-    acc.z = fmaf(acc.z, x, v.z * y);
-    acc.w = fmaf(acc.w, x, v.w * y);
+    for (int i = 0; i < parts; ++i) {
+      const float* slot = p.parts + static_cast<size_t>(i == 0 ? s0 : 2 * (c + i)) * kSlot;
+      const float mi = slot[row], li = slot[kRows + row];
+      const float4* acc = reinterpret_cast<const float4*>(slot + 2 * kRows) + 2 * d8 * kRows + row;
+      const float4 v = acc[0], w = acc[kRows];
+      const float next = fmaxf(m, mi);
+      const float x = fast_exp2(m - next), y = fast_exp2(mi - next);
+      m = next;
+      l = fmaf(l, x, li * y);
+      a = make_float4(fmaf(a.x, x, v.x * y), fmaf(a.y, x, v.y * y), fmaf(a.z, x, v.z * y), fmaf(a.w, x, v.w * y));
+      b = make_float4(fmaf(b.x, x, w.x * y), fmaf(b.y, x, w.y * y), fmaf(b.z, x, w.z * y), fmaf(b.w, x, w.w * y));
+    }
+    if (row >= u.rows) continue;
+    const float inv = l == 0.f ? 0.f : __frcp_rn(l);
+    const int i = token_of(p, u.row0 + row);
+    const size_t at = (static_cast<size_t>(u.r0) + i) * p.c.Hq + static_cast<size_t>(u.h) * p.G + (u.row0 + row - i * p.G);
+    reinterpret_cast<uint4*>(p.out)[at * (kD / 8) + d8] =
+        make_uint4(pack2<T>(a.x * inv, a.y * inv), pack2<T>(a.z * inv, a.w * inv), pack2<T>(b.x * inv, b.y * inv),
+                   pack2<T>(b.z * inv, b.w * inv));
+    if (p.lse && d8 == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
   }
-  const float inv = l == 0.f ? 0.f : __frcp_rn(l);
-  const int i = token_of(p, u.row0 + row);
-  const size_t at = (static_cast<size_t>(u.r0) + i) * p.c.Hq + static_cast<size_t>(u.h) * p.G + (u.row0 + row - i * p.G);
-  reinterpret_cast<uint2*>(p.out)[at * (kD / 4) + lane] =
-      make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
-  if (p.lse && lane == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
 }
 
 template <typename T>
@@ -979,8 +989,8 @@ cudaError_t launch_prefill_t(const Kv4AttendParams& p, int sms, cudaStream_t str
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kv4_prefill_kernel<T>, p);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3(blocks, kRows / 8);
-  cfg.blockDim = dim3(256);
+  cfg.gridDim = dim3(blocks, kRows / 32);
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, kv4_prefill_merge_kernel<T>, p, blocks);
 }
