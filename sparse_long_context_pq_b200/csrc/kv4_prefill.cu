@@ -21,8 +21,9 @@
 // S overwrites P, and S full means that every earlier P V has been added to O.
 //
 // What bounds it: the tensor cores need 2048 clocks for a step (4 x 128 x 128 x 128 products),
-// ex2 as many (256 x 128 at 16 a clock; a quarter of the weights is therefore a polynomial on the
-// FMA pipes), shared memory about 2000 (operands and dequantised tiles).
+// ex2 as many (256 x 128 at 16 a clock), shared memory about 2000 (operands and dequantised tiles).
+// Measured, a step takes more than twice that: a softmax warp's chain (S, maximum, weights, P) and
+// the issue slots that eight softmax and eight dequantising warps share stand in the way.
 //
 // q, weights and their accuracy are those of kv4_attend.cu for 16-bit calls: q over a power of two
 // in fp16, P in fp16 up to 2^(kHead + kGrow), sums and statistics in fp32. ref moves by whole
@@ -43,7 +44,6 @@ constexpr int kStepTiles = kStepTok / kTileTok;
 constexpr int kThreads = 16 * 32;
 constexpr float kHead = 11.f, kGrow = 4.f;
 constexpr int kPiece = 64;                      // tokens of a step that a softmax thread holds at a time
-constexpr int kPolyPair = 0;                    // of four pairs of weights, the one by poly_exp2
 constexpr uint32_t kOperand = 128 * kD * 2;     // 32 KB: 128 rows of 128 fp16
 constexpr uint32_t kHalfOp = kOperand / 2;      // one 64-element half (128 bytes a row)
 constexpr int kSlot = kRows * (kD + 2);         // floats of a partial: m, l, acc
@@ -146,6 +146,19 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_
   record_error(err, HSA_DEVERR_TIMEOUT);
   return false;
 }
+// The same with pauses, for waits whose end may be noticed late.
+__device__ __forceinline__ bool wait_idle(uint64_t* bar, uint32_t parity, int32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+#pragma unroll 1
+  while (true) {
+    __nanosleep(64);
+    if (mbar_try_wait(bar, parity)) return true;
+    if (global_ns() - t0 > kWaitLimitNs) break;
+  }
+  record_error(err, HSA_DEVERR_TIMEOUT);
+  return false;
+}
 __device__ __forceinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, int32_t* err) {
   bool ok = true;
   if ((threadIdx.x & 31) == 0) ok = wait_long(bar, parity, err);
@@ -180,24 +193,6 @@ __device__ __forceinline__ unsigned long long fmul2_rn(unsigned long long a, uns
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// 2^y of two numbers up to 127 without ex2: y = n + r with n whole and |r| <= 1/2, 2^r by a polynomial of degree
-// four (least relative error on that interval, fitted for this: 2.6e-6, against 2^-12 of the fp16 it is rounded
-// to), n added to its exponent. Numbers below -126 count as -126.
-__device__ __forceinline__ float2 poly_exp2(float2 y) {
-  const unsigned long long v = pair(fmaxf(y.x, -126.f), fmaxf(y.y, -126.f));
-  const unsigned long long t = fadd2_rn(v, pair(12582912.f, 12582912.f));   // the whole part in its last bits
-  const unsigned long long n = fadd2_rn(t, pair(-12582912.f, -12582912.f));
-  const unsigned long long r = ffma2_rn(n, pair(-1.f, -1.f), v);
-  unsigned long long e = ffma2_rn(r, pair(0.009570102207362652f, 0.009570102207362652f),
-                                  pair(0.05591785907745361f, 0.05591785907745361f));
-  e = ffma2_rn(r, e, pair(0.240247443318367f, 0.240247443318367f));
-  e = ffma2_rn(r, e, pair(0.6931217908859253f, 0.6931217908859253f));
-  e = ffma2_rn(r, e, pair(0.9999992847442627f, 0.9999992847442627f));
-  const float2 ee = unpair(e), tt = unpair(t);
-  return make_float2(__int_as_float(__float_as_int(ee.x) + (__float_as_int(tt.x) << 23)),
-                     __int_as_float(__float_as_int(ee.y) + (__float_as_int(tt.y) << 23)));
-}
-
 // Loads that leave L1 alone: the cache's bytes pass once.
 __device__ __forceinline__ uint4 load_once16(const uint8_t* at) {
   uint4 v;
@@ -205,6 +200,9 @@ __device__ __forceinline__ uint4 load_once16(const uint8_t* at) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(at));
   return v;
+}
+__device__ __forceinline__ void store16(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 __device__ __forceinline__ uint2 load_once8(const uint8_t* at) {
   uint2 v;
@@ -378,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint32_t tmem_slot;
+  __shared__ volatile int gave_up[2];
   __shared__ Walk walks[kThreads / 32];
   __shared__ Segment segments_s[kThreads / 32];
   __shared__ float factor[kRows];     // logits from S, in log2 units
@@ -406,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       mbar_init(drained + i, 1);
     }
     fence_mbar_init();
+    gave_up[0] = gave_up[1] = 0;
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
@@ -533,8 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 #pragma unroll 1
       for (int j = first; j < steps; j += by, ++done) {
-        // a wait that gave up: no more work, but the barriers that the four warps share are still passed
-        if (ok) ok = wait_long_warp(s_full + half, done & 1, p.c.err);
+        // One warp polls, the others wait at a barrier, which takes no issue slots from those at work. After a wait
+        // that gave up there is no more work, but the barriers that the four warps share are still passed.
+        if ((warp & 3) == 0 && ok && !wait_long_warp(s_full + half, done & 1, p.c.err) && lane == 0) gave_up[half] = 1;
+        half_barrier(half);
+        ok = ok && gave_up[half] == 0;
         if (!ok) {
           half_barrier(half);
           continue;
@@ -623,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           for (int i = 0; i < kPiece / 2; ++i) {
             // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
             const float2 y = unpair(fadd2_rn(fmul2_rn(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2), ref2));
-            const float2 e = i % 4 == kPolyPair ? poly_exp2(y) : make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             l2[i & 1] = fadd2_rn(l2[i & 1], pair(e.x, e.y));
             x[i] = pack_f16x2(e.x, e.y);
           }
@@ -638,6 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
           if (ok && j + by < steps) ok = qk(j + by);
           else if (ok) tc_commit(o_full + half);
         }
+        if (leader && !ok) gave_up[half] = 1;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
       }
       it += steps;
@@ -764,6 +768,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     const int r = lane >> 2, t = lane & 3;
     uint64_t* full = keys ? k_full : v_full;
     uint64_t* empty = keys ? k_empty : v_empty;
+    // Where this lane stores its four 16-byte pieces of a tile half (stage, tile and half are added):
+    // keys: word i of a row's 16 bytes is dims 32 t + 8 i ..; lanes with t >= 2 take words 2, 3, 0, 1, so that the
+    // eight lanes that store together meet eight different pieces of the banks;
+    // values: [token][piece]; the two tokens of a byte part ways, and lanes of odd r store the odd token first.
+    uint32_t to[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = keys ? r : 2 * t + ((i >> 1) ^ (r & 1));
+      const int piece = keys ? (t & 1) * 4 + (i ^ (t & 2)) : (r & 3) * 2 + (i & 1);
+      to[i] = smem_addr(sm) + (keys ? Smem::k : Smem::v) + (keys ? t >> 1 : r >> 2) * kHalfOp + 2 * w * 2048 + row * 128 +
+              ((piece ^ row) << 4);
+    }
+    const uint8_t* code_base = p.c.cache + (keys ? 0 : kOffV) + lane * 16;
+    const uint8_t* scale_base = p.c.cache + kOffScale + lane * 8;
+    const uint32_t first_group = t & 2 ? 0x2301u : 0x3210u;   // bytes of a scale word, keys: the first word's group first
+    const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
     int it = 0;
     bool ok = true;
 #pragma unroll 1
@@ -786,16 +806,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int at = __shfl_sync(0xffffffffu, where, (j & 3) * kStepTiles + 2 * w + u);
-          code[u][0] = code[u][1] = make_uint4(0u, 0u, 0u, 0u);
-          sc[u] = make_uint2(0u, 0u);
           if (at >= 0) {
-            const uint8_t* tile = p.c.cache + static_cast<size_t>(static_cast<uint32_t>(at)) * kTileBytes;
-            const uint8_t* src = tile + (keys ? 0 : kOffV) + lane * 16;
-            code[u][0] = load_once16(src);
-            code[u][1] = load_once16(src + 512);
-            sc[u] = load_once8(tile + kOffScale + lane * 8);
+            const size_t tile = static_cast<size_t>(static_cast<uint32_t>(at)) * kTileBytes;
+            code[u][0] = load_once16(code_base + tile);
+            code[u][1] = load_once16(code_base + tile + 512);
+            sc[u] = load_once8(scale_base + tile);
           } else {
             gone |= 1u << u;
+            code[u][0] = code[u][1] = make_uint4(0u, 0u, 0u, 0u);
+            sc[u] = make_uint2(0u, 0u);
           }
         }
       };
@@ -803,91 +822,76 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const int i_step = it + j, stage = i_step & 1;
-        const uint4 now[2][2] = {{code[0][0], code[0][1]}, {code[1][0], code[1][1]}};
-        const uint2 scale[2] = {sc[0], sc[1]};
-        const unsigned lost = gone;
-        if (j + 1 < steps) load(j + 1);
-        if (!wait_long_warp(empty + stage, ((i_step >> 1) & 1) ^ 1, p.c.err)) {
-          ok = false;
-          break;
+        if (lane == 0) ok = wait_idle(empty + stage, ((i_step >> 1) & 1) ^ 1, p.c.err);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        const uint32_t at = stage * kOperand;
+        // values' scales that are not finite: bytes 248 and up (a zero byte of ~(y | 7))
+        unsigned bad = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t z = ~(sc[u].y | 0x07070707u);
+          bad |= (z - 0x01010101u) & ~z & 0x80808080u;
         }
+        const bool any_bad = __any_sync(0xffffffffu, bad != 0u);
         if (keys) {
-          // Word i of a row's 16 bytes is dims 32 t + 8 i ..: one 16-byte piece. Lanes with t >= 2 start at word 2:
-          // the eight lanes that store together then meet eight different pieces of the banks.
-          uint8_t* dst = sm + Smem::k + stage * kOperand;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
+            const uint32_t sw = __byte_perm(sc[u].x, 0u, first_group);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const int row = (2 * w + u) * kTileTok + half * 8 + r;
-              const uint32_t cw[4] = {now[u][half].x, now[u][half].y, now[u][half].z, now[u][half].w};
-              const uint32_t sa = scale_both(scale[u].x, 2 * half), sb = scale_both(scale[u].x, 2 * half + 1);
-              uint8_t* base = dst + (t >> 1) * kHalfOp + row * 128;
+              const uint4 c = code[u][half];
+              const uint32_t cw[4] = {t & 2 ? c.z : c.x, t & 2 ? c.w : c.y, t & 2 ? c.x : c.z, t & 2 ? c.y : c.w};
+              const uint32_t sa = scale_both(sw, 2 * half), sb = scale_both(sw, 2 * half + 1);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const uint32_t word = t & 2 ? cw[i ^ 2] : cw[i];
-                const uint32_t s1 = ((i & 2) != 0) != ((t & 2) != 0) ? sb : sa;
-                const int piece = (t & 1) * 4 + (i ^ (t & 2));
                 uint32_t x[4];
-                e2m1_to_f16x2(word, x[0], x[1], x[2], x[3]);
-                *reinterpret_cast<uint4*>(base + ((piece ^ (row & 7)) << 4)) =
-                    make_uint4(hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1), hmul2(x[3], s1));
+                e2m1_to_f16x2(cw[i], x[0], x[1], x[2], x[3]);
+                const uint32_t s1 = i < 2 ? sa : sb;
+                store16(to[i] + at + u * 2048 + half * 1024, hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1),
+                        hmul2(x[3], s1));
               }
             }
           }
           // what the softmax has to know of the step
-          unsigned bits = lost << (2 * w), bad = 0;
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t y = scale[u].y;   // values' scales: bytes 248 and up are not finite
-            bad |= y & (y << 1) & (y << 2) & (y << 3) & (y << 4) & 0x80808080u;
-          }
-          if (__any_sync(0xffffffffu, bad != 0u)) {
-            uint32_t word = 0;               // group r: bit = token of this warp's 32
+          uint32_t word = 0;
+          if (any_bad) {                       // group r: bit = token of this warp's 32
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
-                if (((scale[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
+                if (((sc[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
             word |= __shfl_xor_sync(0xffffffffu, word, 1);
             word |= __shfl_xor_sync(0xffffffffu, word, 2);
-            if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
-            bits |= 0x100u;
-          } else if (t == 0) {
-            poison_s[(i_step & 3) * 32 + r * 4 + w] = 0u;
           }
-          if (lane == 0) flags_s[(i_step & 3) * 4 + w] = bits;
+          if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
+          if (lane == 0) flags_s[(i_step & 3) * 4 + w] = (gone << (2 * w)) | (any_bad ? 0x100u : 0u);
         } else {
-          // The two tokens of a byte part ways; lanes of odd r store the odd token first, against bank conflicts.
-          uint8_t* dst = sm + Smem::v + stage * kOperand + (r >> 2) * kHalfOp;
           const int left = tokens - (k0 + j) * kStepTok;   // tokens from the step's first on
-          const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
+          const bool edge = left < kStepTok || any_bad;
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
-              uint32_t s2 = scale_pair(scale[u].y, 2 * half);
-              if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;         // not finite, or past the end
-              if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
-              const uint32_t cw[4] = {now[u][half].x, now[u][half].y, now[u][half].z, now[u][half].w};
-              uint32_t x[16];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                e2m1_to_f16x2(cw[i], x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) x[4 * i + q] = hmul2(x[4 * i + q], s2);
+              uint32_t s2 = scale_pair(sc[u].y, 2 * half);
+              if (edge) {                      // tokens that are not finite, or past the end, become zeros
+                const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
+                if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;
+                if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
               }
+              const uint32_t cw[4] = {code[u][half].x, code[u][half].y, code[u][half].z, code[u][half].w};
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int row = tok + (e ^ (r & 1));
-                const uint32_t sel = e ? sel1 : sel0;
+              for (int q = 0; q < 2; ++q) {    // eight dims of both tokens
+                uint32_t x[8];
+                e2m1_to_f16x2(cw[2 * q], x[0], x[1], x[2], x[3]);
+                e2m1_to_f16x2(cw[2 * q + 1], x[4], x[5], x[6], x[7]);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const int piece = (r & 3) * 2 + q;
-                  *reinterpret_cast<uint4*>(dst + row * 128 + ((piece ^ (row & 7)) << 4)) =
-                      make_uint4(__byte_perm(x[8 * q], x[8 * q + 1], sel), __byte_perm(x[8 * q + 2], x[8 * q + 3], sel),
-                                 __byte_perm(x[8 * q + 4], x[8 * q + 5], sel), __byte_perm(x[8 * q + 6], x[8 * q + 7], sel));
+                for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], s2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const uint32_t sel = e ? sel1 : sel0;
+                  store16(to[2 * e + q] + at + u * 2048 + half * 1024, __byte_perm(x[0], x[1], sel),
+                          __byte_perm(x[2], x[3], sel), __byte_perm(x[4], x[5], sel), __byte_perm(x[6], x[7], sel));
                 }
               }
             }
@@ -896,6 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full + stage);
+        if (j + 1 < steps) load(j + 1);   // there before the stage after next is free
       }
       it += steps;
     }
