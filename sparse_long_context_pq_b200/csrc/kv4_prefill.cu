@@ -6,14 +6,14 @@
 // every block, one an SM, takes an equal share of it; units that cross blocks leave a partial a
 // block, which the merge kernel joins.
 //
-// A block has 16 warps, each walking through the block's segments for itself:
-//   warps 0-3, 4-7    softmax of rows 0-127 and 128-255, one row a thread: S from TMEM, weights
-//                     2^(S f - ref) as fp16 back into TMEM over S, now and then O scaled down. One lane
-//                     of each four issues their MMAs: S = Q K^T (both operands in shared memory, K-major)
-//                     and O += P V (P in TMEM, V with dims contiguous), M = N = 128, so that one half's
-//                     products run under the other's softmax;
-//   warps 8-11, 12-15 keys and values: codes x scales to fp16 (exact) in 128-byte-swizzled shared
-//                     memory, two stages of 128 tokens each, the next tokens' codes in registers.
+// A block has 14 warps, each walking through the block's segments for itself:
+//   warps 0-3, 4-7  softmax of rows 0-127 and 128-255, one row a thread: S from TMEM, weights
+//                   2^(S f - ref) as fp16 back into TMEM over S, now and then O scaled down;
+//   warps 8-11      keys and values: codes x scales to fp16 (exact) in 128-byte-swizzled shared
+//                   memory, two stages of 128 tokens each, the next tokens' codes in registers;
+//   warps 12, 13    one lane each issues a half's MMAs: S = Q K^T (both operands in shared memory,
+//                   K-major) and O += P V (P in TMEM, V with dims contiguous), M = N = 128, so that one
+//                   half's products run under the other's softmax.
 // A unit of at most 128 rows gives both halves the same rows, one the even steps and one the odd
 // ones; their sums are joined at the end.
 // TMEM: S of both halves (128 columns each; P takes the first 64), O of both (128 each).
@@ -41,7 +41,7 @@ namespace {
 constexpr int kRows = 256;                      // query rows of a unit
 constexpr int kStepTok = 128;
 constexpr int kStepTiles = kStepTok / kTileTok;
-constexpr int kThreads = 16 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr float kHead = 11.f, kGrow = 4.f;
 constexpr int kPiece = 64;                      // tokens of a step that a softmax thread holds at a time
 constexpr uint32_t kOperand = 128 * kD * 2;     // 32 KB: 128 rows of 128 fp16
@@ -164,12 +164,12 @@ __device__ __forceinline__ bool wait_long_warp(uint64_t* bar, uint32_t parity, i
   if ((threadIdx.x & 31) == 0) ok = wait_long(bar, parity, err);
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
-// Barriers of the four warps of a half.
+// Barrier of the four softmax warps of a half and its MMA warp.
 __device__ __forceinline__ void half_barrier(int half) {
   if (half == 0)
-    asm volatile("bar.sync 2, 128;" ::: "memory");
+    asm volatile("bar.sync 2, 160;" ::: "memory");
   else
-    asm volatile("bar.sync 3, 128;" ::: "memory");
+    asm volatile("bar.sync 3, 160;" ::: "memory");
 }
 // Largest of three, NaN if one is.
 __device__ __forceinline__ float max3_nan(float a, float b, float c) {
@@ -376,7 +376,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   extern __shared__ uint8_t raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint32_t tmem_slot;
-  __shared__ volatile int gave_up[2];
   __shared__ Walk walks[kThreads / 32];
   __shared__ Segment segments_s[kThreads / 32];
   __shared__ float factor[kRows];     // logits from S, in log2 units
@@ -405,7 +404,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       mbar_init(drained + i, 1);
     }
     fence_mbar_init();
-    gave_up[0] = gave_up[1] = 0;
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
@@ -482,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         }
       }
       fence_proxy_async_smem();
-      asm volatile("bar.sync 1, 256;" ::: "memory");   // q and its factors
+      asm volatile("bar.sync 4, 320;" ::: "memory");   // q and its factors; the MMA warps wait for them too
 
       const int row = split ? tid & 127 : tid;
       const float f = factor[row];
@@ -495,49 +493,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       unsigned long long l2[2] = {0, 0};
       unsigned poison = 0;          // bits 0-7: dim groups with a value that is not finite, bit 8: the whole row
       const int first = split ? half : 0, by = split ? 2 : 1;
-      // ---- this half's MMAs, by one lane ----
-      auto qk = [&](int j) {        // S of step j; its keys are then free, for this half
-        const int i = it + j;
-        if (!wait_long(k_full + (i & 1), (i >> 1) & 1, p.c.err)) return false;
-        tc_fence_after();
-        const uint32_t a = smem_addr(sm + Smem::q) + (split ? 0 : half) * kOperand;
-        const uint32_t bk = smem_addr(sm + Smem::k) + (i & 1) * kOperand;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = (kk >> 2) * kHalfOp + (kk & 3) * 32;
-          mma_ss(tmem + half * 128, desc_k_major(a + off), desc_k_major(bk + off), kk > 0 ? 1u : 0u);
-        }
-        tc_commit(s_full + half);
-        tc_commit(k_empty + (i & 1));
-        if (split) mbar_arrive(k_empty + (i & 1));   // the other half does not read it
-        return true;
-      };
-      auto pv = [&](int j) {        // weights of step j times its values
-        const int i = it + j;
-        if (!wait_long(v_full + (i & 1), (i >> 1) & 1, p.c.err)) return false;
-        tc_fence_after();
-        const uint32_t bv = smem_addr(sm + Smem::v) + (i & 1) * kOperand;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, desc_mn_major(bv + kk * 2048),
-                 j == first && kk == 0 ? 0u : 1u);
-        tc_commit(v_empty + (i & 1));
-        if (split) mbar_arrive(v_empty + (i & 1));
-        return true;
-      };
-      const bool leader = (warp & 3) == 0 && lane == 0;
-      if (leader && ok) {
-        if (first < steps) ok = qk(first);
-        else tc_commit(o_full + half);
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 #pragma unroll 1
       for (int j = first; j < steps; j += by, ++done) {
-        // One warp polls, the others wait at a barrier, which takes no issue slots from those at work. After a wait
-        // that gave up there is no more work, but the barriers that the four warps share are still passed.
-        if ((warp & 3) == 0 && ok && !wait_long_warp(s_full + half, done & 1, p.c.err) && lane == 0) gave_up[half] = 1;
-        half_barrier(half);
-        ok = ok && gave_up[half] == 0;
+        // After a wait that gave up there is no more work, but the barriers that others share are still passed.
+        if (ok) ok = wait_long_warp(s_full + half, done & 1, p.c.err);
         if (!ok) {
           half_barrier(half);
           continue;
@@ -635,14 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         }
         tmem_wait_st();
         tc_fence_before();
-        half_barrier(half);   // this half's weights are there
-        if (leader) {
-          ok = pv(j);
-          if (ok && j + by < steps) ok = qk(j + by);
-          else if (ok) tc_commit(o_full + half);
-        }
-        if (leader && !ok) gave_up[half] = 1;
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        half_barrier(half);   // this half's weights are there, for its MMA warp
       }
       it += steps;
       ok = ok && wait_long_warp(o_full + half, segments & 1, p.c.err);
@@ -756,31 +708,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       tc_fence_before();
       asm volatile("bar.sync 1, 256;" ::: "memory");   // O, factors and staged sums have been read
     }
-    if ((warp & 3) == 0 && lane == 0) {
-      tc_commit(drained + half);
-      wait_long(drained + half, 0, p.c.err);   // nothing of ours still writes TMEM
-    }
-    __syncwarp();
-  } else {
-    // ================= keys (warps 8-11) and values (12-15) =================
-    const bool keys = warp < 12;
+  } else if (warp < 12) {
+    // ================= keys and values =================
     const int w = warp & 3;                    // tiles 2w, 2w + 1 of a step
     const int r = lane >> 2, t = lane & 3;
-    uint64_t* full = keys ? k_full : v_full;
-    uint64_t* empty = keys ? k_empty : v_empty;
     // Where this lane stores its four 16-byte pieces of a tile half (stage, tile and half are added):
     // keys: word i of a row's 16 bytes is dims 32 t + 8 i ..; lanes with t >= 2 take words 2, 3, 0, 1, so that the
     // eight lanes that store together meet eight different pieces of the banks;
     // values: [token][piece]; the two tokens of a byte part ways, and lanes of odd r store the odd token first.
-    uint32_t to[4];
+    uint32_t to_k[4], to_v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = keys ? r : 2 * t + ((i >> 1) ^ (r & 1));
-      const int piece = keys ? (t & 1) * 4 + (i ^ (t & 2)) : (r & 3) * 2 + (i & 1);
-      to[i] = smem_addr(sm) + (keys ? Smem::k : Smem::v) + (keys ? t >> 1 : r >> 2) * kHalfOp + 2 * w * 2048 + row * 128 +
-              ((piece ^ row) << 4);
+      const int v_row = 2 * t + ((i >> 1) ^ (r & 1));
+      const int k_piece = (t & 1) * 4 + (i ^ (t & 2)), v_piece = (r & 3) * 2 + (i & 1);
+      to_k[i] = smem_addr(sm) + Smem::k + (t >> 1) * kHalfOp + 2 * w * 2048 + r * 128 + ((k_piece ^ r) << 4);
+      to_v[i] = smem_addr(sm) + Smem::v + (r >> 2) * kHalfOp + 2 * w * 2048 + v_row * 128 + ((v_piece ^ v_row) << 4);
     }
-    const uint8_t* code_base = p.c.cache + (keys ? 0 : kOffV) + lane * 16;
+    const uint8_t* code_base = p.c.cache + lane * 16;
     const uint8_t* scale_base = p.c.cache + kOffScale + lane * 8;
     const uint32_t first_group = t & 2 ? 0x2301u : 0x3210u;   // bytes of a scale word, keys: the first word's group first
     const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
@@ -791,9 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       const int steps = cur.k1 - cur.k0, tokens = cur.T, k0 = cur.k0;
       int where = -1;                            // lane: cache tile of tile 32 * batch + lane of the segment
       unsigned gone = 0;                         // bits: of the loaded tiles, those without a page
-      uint4 code[2][2];
+      size_t tile[2];                            // byte offsets of the tiles of the step that is loaded next
+      uint4 kc[2][2], vc[2][2];
       uint2 sc[2];
-      auto load = [&](int j) {
+      auto find = [&](int j) {
         if ((j & 3) == 0) {
           const int tl = (k0 + j) * kStepTiles + lane;
           where = -1;
@@ -806,104 +751,181 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int at = __shfl_sync(0xffffffffu, where, (j & 3) * kStepTiles + 2 * w + u);
-          if (at >= 0) {
-            const size_t tile = static_cast<size_t>(static_cast<uint32_t>(at)) * kTileBytes;
-            code[u][0] = load_once16(code_base + tile);
-            code[u][1] = load_once16(code_base + tile + 512);
-            sc[u] = load_once8(scale_base + tile);
-          } else {
-            gone |= 1u << u;
-            code[u][0] = code[u][1] = make_uint4(0u, 0u, 0u, 0u);
-            sc[u] = make_uint2(0u, 0u);
+          if (at < 0) gone |= 1u << u;
+          tile[u] = static_cast<size_t>(static_cast<uint32_t>(max(at, 0))) * kTileBytes;
+        }
+      };
+      auto fetch = [&](uint4 (&c)[2][2], int off) {   // a tile without a page: zeros
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          c[u][0] = load_once16(code_base + tile[u] + off);
+          c[u][1] = load_once16(code_base + tile[u] + off + 512);
+          if (off == 0) sc[u] = load_once8(scale_base + tile[u]);
+          if (gone >> u & 1u) {
+            c[u][0] = c[u][1] = make_uint4(0u, 0u, 0u, 0u);
+            if (off == 0) sc[u] = make_uint2(0u, 0u);
           }
         }
       };
-      load(0);
+      find(0);
+      fetch(kc, 0);
+      fetch(vc, kOffV);
 #pragma unroll 1
       for (int j = 0; j < steps; ++j) {
         const int i_step = it + j, stage = i_step & 1;
-        if (lane == 0) ok = wait_idle(empty + stage, ((i_step >> 1) & 1) ^ 1, p.c.err);
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        const uint32_t at = stage * kOperand;
+        const uint32_t at = stage * kOperand, parity = ((i_step >> 1) & 1) ^ 1;
+        const uint32_t vs[2] = {sc[0].y, sc[1].y};
         // values' scales that are not finite: bytes 248 and up (a zero byte of ~(y | 7))
         unsigned bad = 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint32_t z = ~(sc[u].y | 0x07070707u);
+          const uint32_t z = ~(vs[u] | 0x07070707u);
           bad |= (z - 0x01010101u) & ~z & 0x80808080u;
         }
         const bool any_bad = __any_sync(0xffffffffu, bad != 0u);
-        if (keys) {
+        if (lane == 0) ok = wait_idle(k_empty + stage, parity, p.c.err);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t sw = __byte_perm(sc[u].x, 0u, first_group);
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t sw = __byte_perm(sc[u].x, 0u, first_group);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint4 c = code[u][half];
-              const uint32_t cw[4] = {t & 2 ? c.z : c.x, t & 2 ? c.w : c.y, t & 2 ? c.x : c.z, t & 2 ? c.y : c.w};
-              const uint32_t sa = scale_both(sw, 2 * half), sb = scale_both(sw, 2 * half + 1);
+          for (int half = 0; half < 2; ++half) {
+            const uint4 c = kc[u][half];
+            const uint32_t cw[4] = {t & 2 ? c.z : c.x, t & 2 ? c.w : c.y, t & 2 ? c.x : c.z, t & 2 ? c.y : c.w};
+            const uint32_t sa = scale_both(sw, 2 * half), sb = scale_both(sw, 2 * half + 1);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t x[4];
-                e2m1_to_f16x2(cw[i], x[0], x[1], x[2], x[3]);
-                const uint32_t s1 = i < 2 ? sa : sb;
-                store16(to[i] + at + u * 2048 + half * 1024, hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1),
-                        hmul2(x[3], s1));
-              }
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[4];
+              e2m1_to_f16x2(cw[i], x[0], x[1], x[2], x[3]);
+              const uint32_t s1 = i < 2 ? sa : sb;
+              store16(to_k[i] + at + u * 2048 + half * 1024, hmul2(x[0], s1), hmul2(x[1], s1), hmul2(x[2], s1),
+                      hmul2(x[3], s1));
             }
           }
-          // what the softmax has to know of the step
-          uint32_t word = 0;
-          if (any_bad) {                       // group r: bit = token of this warp's 32
+        }
+        // what the softmax has to know of the step
+        uint32_t word = 0;
+        if (any_bad) {                       // group r: bit = token of this warp's 32
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+          for (int u = 0; u < 2; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (((sc[u].y >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
-            word |= __shfl_xor_sync(0xffffffffu, word, 1);
-            word |= __shfl_xor_sync(0xffffffffu, word, 2);
-          }
-          if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
-          if (lane == 0) flags_s[(i_step & 3) * 4 + w] = (gone << (2 * w)) | (any_bad ? 0x100u : 0u);
-        } else {
-          const int left = tokens - (k0 + j) * kStepTok;   // tokens from the step's first on
-          const bool edge = left < kStepTok || any_bad;
+            for (int i = 0; i < 4; ++i)
+              if (((vs[u] >> (8 * i)) & 0xffu) >= 248u) word |= 1u << (16 * u + 8 * (i >> 1) + 2 * t + (i & 1));
+          word |= __shfl_xor_sync(0xffffffffu, word, 1);
+          word |= __shfl_xor_sync(0xffffffffu, word, 2);
+        }
+        if (t == 0) poison_s[(i_step & 3) * 32 + r * 4 + w] = word;
+        if (lane == 0) flags_s[(i_step & 3) * 4 + w] = (gone << (2 * w)) | (any_bad ? 0x100u : 0u);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_full + stage);
+        if (j + 1 < steps) {                 // there before the stage after next is free
+          find(j + 1);
+          fetch(kc, 0);
+        }
+        if (lane == 0) ok = wait_idle(v_empty + stage, parity, p.c.err);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        const int left = tokens - (k0 + j) * kStepTok;   // tokens from the step's first on
+        const bool edge = left < kStepTok || any_bad;
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t s2 = scale_pair(sc[u].y, 2 * half);
-              if (edge) {                      // tokens that are not finite, or past the end, become zeros
-                const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
-                if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;
-                if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
-              }
-              const uint32_t cw[4] = {code[u][half].x, code[u][half].y, code[u][half].z, code[u][half].w};
+          for (int half = 0; half < 2; ++half) {
+            uint32_t s2 = scale_pair(vs[u], 2 * half);
+            if (edge) {                      // tokens that are not finite, or past the end, become zeros
+              const int tok = (2 * w + u) * kTileTok + half * 8 + 2 * t;
+              if ((s2 & 0x7c00u) == 0x7c00u || tok >= left) s2 &= 0xffff0000u;
+              if ((s2 & 0x7c000000u) == 0x7c000000u || tok + 1 >= left) s2 &= 0x0000ffffu;
+            }
+            const uint32_t cw[4] = {vc[u][half].x, vc[u][half].y, vc[u][half].z, vc[u][half].w};
 #pragma unroll
-              for (int q = 0; q < 2; ++q) {    // eight dims of both tokens
-                uint32_t x[8];
-                e2m1_to_f16x2(cw[2 * q], x[0], x[1], x[2], x[3]);
-                e2m1_to_f16x2(cw[2 * q + 1], x[4], x[5], x[6], x[7]);
+            for (int q = 0; q < 2; ++q) {    // eight dims of both tokens
+              uint32_t x[8];
+              e2m1_to_f16x2(cw[2 * q], x[0], x[1], x[2], x[3]);
+              e2m1_to_f16x2(cw[2 * q + 1], x[4], x[5], x[6], x[7]);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], s2);
+              for (int k = 0; k < 8; ++k) x[k] = hmul2(x[k], s2);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  const uint32_t sel = e ? sel1 : sel0;
-                  store16(to[2 * e + q] + at + u * 2048 + half * 1024, __byte_perm(x[0], x[1], sel),
-                          __byte_perm(x[2], x[3], sel), __byte_perm(x[4], x[5], sel), __byte_perm(x[6], x[7], sel));
-                }
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t sel = e ? sel1 : sel0;
+                store16(to_v[2 * e + q] + at + u * 2048 + half * 1024, __byte_perm(x[0], x[1], sel),
+                        __byte_perm(x[2], x[3], sel), __byte_perm(x[4], x[5], sel), __byte_perm(x[6], x[7], sel));
               }
             }
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(full + stage);
-        if (j + 1 < steps) load(j + 1);   // there before the stage after next is free
+        if (lane == 0) mbar_arrive(v_full + stage);
+        if (j + 1 < steps) fetch(vc, kOffV);
       }
       it += steps;
     }
+  } else {
+    // ================= a half's MMAs: one lane =================
+    const int half = warp - 12;
+    int it = 0;
+    bool ok = true;
+#pragma unroll 1
+    while (walk.next(p, cur)) {
+      const int steps = cur.k1 - cur.k0;
+      const bool split = cur.rows <= 128;
+      const int first = split ? half : 0, by = split ? 2 : 1;
+      const uint64_t q_desc = desc_k_major(smem_addr(sm + Smem::q) + (split ? 0 : half) * kOperand);
+      const uint64_t k_desc = desc_k_major(smem_addr(sm + Smem::k)), v_desc = desc_mn_major(smem_addr(sm + Smem::v));
+      const uint32_t d_s = tmem + half * 128, d_o = tmem + 256 + half * 128;
+      auto qk = [&](int i) {        // S of the block's step i; its keys are then free, for this half
+        const uint64_t b = k_desc + (i & 1) * (kOperand >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * kHalfOp + (kk & 3) * 32) >> 4;
+          mma_ss(d_s, q_desc + off, b + off, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(s_full + half);
+        tc_commit(k_empty + (i & 1));
+        if (split) mbar_arrive(k_empty + (i & 1));   // the other half does not read it
+      };
+      auto pv = [&](int i, bool fresh) {   // weights of step i times its values
+        const uint64_t b = v_desc + (i & 1) * (kOperand >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_ts(d_o, d_s + kk * 8, b + kk * (2048 >> 4), fresh && kk == 0 ? 0u : 1u);
+        tc_commit(v_empty + (i & 1));
+        if (split) mbar_arrive(v_empty + (i & 1));
+      };
+      asm volatile("bar.sync 4, 320;" ::: "memory");   // q is there
+      if (lane == 0) {
+        tc_fence_after();
+        if (ok && first < steps) ok = wait_long(k_full + ((it + first) & 1), ((it + first) >> 1) & 1, p.c.err);
+        tc_fence_after();
+        if (ok && first < steps) qk(it + first);
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int j = first; j < steps; j += by) {
+        if (lane == 0 && ok) {      // ahead of the weights
+          ok = wait_long(v_full + ((it + j) & 1), ((it + j) >> 1) & 1, p.c.err);
+          if (ok && j + by < steps) ok = wait_long(k_full + ((it + j + by) & 1), ((it + j + by) >> 1) & 1, p.c.err);
+        }
+        __syncwarp();
+        half_barrier(half);
+        if (lane == 0 && ok) {
+          tc_fence_after();
+          pv(it + j, j == first);
+          if (j + by < steps) qk(it + j + by);
+        }
+        __syncwarp();
+      }
+      if (lane == 0 && ok) tc_commit(o_full + half);
+      __syncwarp();
+      it += steps;
+    }
+    if (lane == 0) {
+      tc_commit(drained + half);
+      wait_long(drained + half, 0, p.c.err);   // nothing of ours still writes TMEM
+    }
+    __syncwarp();
   }
 
   tc_fence_before();
