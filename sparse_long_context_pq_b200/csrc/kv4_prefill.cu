@@ -201,6 +201,9 @@ __device__ __forceinline__ uint4 load_once16(const uint8_t* at) {
                : "l"(at));
   return v;
 }
+__device__ __forceinline__ void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void store16(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -738,14 +741,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       size_t tile[2];                            // byte offsets of the tiles of the step that is loaded next
       uint4 kc[2][2], vc[2][2];
       uint2 sc[2];
+      // page numbers of 32 tiles (four steps) ahead; one warp also has their bytes brought into L2
+      auto look_up = [&](int j) -> int {
+        const int tl = (k0 + j) * kStepTiles + lane;
+        if (tl > (tokens - 1) / kTileTok || tl >= (k0 + steps) * kStepTiles) return -1;
+        const int page = kv4_page(p.c, cur.b, tl);
+        if (page < 0) return -1;
+        const uint32_t at = kv4_tile_index(p.c, page, cur.h, tl);
+        if (w == 0) prefetch_l2(p.c.cache + static_cast<size_t>(at) * kTileBytes, kTileBytes);
+        return static_cast<int>(at);
+      };
+      int ahead = look_up(0);
       auto find = [&](int j) {
         if ((j & 3) == 0) {
-          const int tl = (k0 + j) * kStepTiles + lane;
-          where = -1;
-          if (tl <= (tokens - 1) / kTileTok && tl < (k0 + steps) * kStepTiles) {
-            const int page = kv4_page(p.c, cur.b, tl);
-            if (page >= 0) where = static_cast<int>(kv4_tile_index(p.c, page, cur.h, tl));
-          }
+          where = ahead;
+          ahead = look_up(j + 4);
         }
         gone = 0;
 #pragma unroll
@@ -904,16 +914,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       __syncwarp();
 #pragma unroll 1
       for (int j = first; j < steps; j += by) {
-        if (lane == 0 && ok) {      // ahead of the weights
+        // ahead of the weights: the values and the next keys. With split steps these keys are two steps on, and are
+        // made after the values between, whose stage is not free before this step's products.
+        if (lane == 0 && ok) {
           ok = wait_long(v_full + ((it + j) & 1), ((it + j) >> 1) & 1, p.c.err);
-          if (ok && j + by < steps) ok = wait_long(k_full + ((it + j + by) & 1), ((it + j + by) >> 1) & 1, p.c.err);
+          if (ok && !split && j + by < steps) ok = wait_long(k_full + ((it + j + by) & 1), ((it + j + by) >> 1) & 1, p.c.err);
         }
         __syncwarp();
         half_barrier(half);
         if (lane == 0 && ok) {
           tc_fence_after();
           pv(it + j, j == first);
-          if (j + by < steps) qk(it + j + by);
+          if (j + by < steps) {
+            if (split) ok = wait_long(k_full + ((it + j + by) & 1), ((it + j + by) >> 1) & 1, p.c.err);
+            tc_fence_after();
+            if (ok) qk(it + j + by);
+          }
         }
         __syncwarp();
       }
