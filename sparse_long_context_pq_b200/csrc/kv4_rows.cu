@@ -29,15 +29,7 @@ struct Elem<float> {
       x[4 * i + 3] = v.w;
     }
   }
-  // 16 values from fp16 pairs
-  static __device__ __forceinline__ void store16(uint8_t* p, const uint32_t* h) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i]));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[2 * i + 1]));
-      reinterpret_cast<float4*>(p)[i] = make_float4(a.x, a.y, b.x, b.y);
-    }
-  }
+  static __device__ __forceinline__ uint32_t of(uint32_t h) { return h; }   // not used
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -53,16 +45,10 @@ struct Elem<__nv_bfloat16> {
       }
     }
   }
-  static __device__ __forceinline__ void store16(uint8_t* p, const uint32_t* h) {
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);   // exact
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  static __device__ __forceinline__ uint32_t of(uint32_t h) {   // an fp16 pair, exactly
+    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const __nv_bfloat162 b = __floats2bfloat162_rn(a.x, a.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
   }
 };
 template <>
@@ -80,25 +66,32 @@ struct Elem<__half> {
       }
     }
   }
-  static __device__ __forceinline__ void store16(uint8_t* p, const uint32_t* h) {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(h[4], h[5], h[6], h[7]);
-  }
+  static __device__ __forceinline__ uint32_t of(uint32_t h) { return h; }
 };
 
+// Largest of |a|, |b| and m, NaN if one is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return d;
+}
+
 // One block: scale byte and 16 values over scale, not yet rounded to codes.
-// a / 6 and x / scale are correctly rounded divisions: a quotient at a rounding border of the
-// few-bit result is then exact, so ties are ties, and no quotient beside a border reaches it.
+// a / 6 and x / scale are correctly rounded quotients: one at a rounding border of the few-bit
+// result is then exact, so ties are ties, and none beside a border reaches it. x / scale by the
+// reciprocal r = 1 / scale, correctly rounded, and one correction: y = x r, y + r (x - y scale)
+// (Markstein, IBM J. Res. Dev. 34, 1990); two fused steps for two values where a division takes
+// ten (measured: 32768 tokens x 8 heads from bf16 73 us with divisions, see the kernel).
 __device__ __forceinline__ uint32_t quantise16(float* x) {
-  uint32_t top = 0;
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
-  if (top >= 0x7f800000u) {   // a NaN or an infinity
+  for (int i = 0; i < 16; i += 2) top = max_abs(top, x[i], x[i + 1]);
+  if (!(top < INFINITY)) {   // a NaN or an infinity
 #pragma unroll
     for (int i = 0; i < 16; ++i) x[i] = 0.f;
     return 255u;
   }
-  const float y = fminf(__fdiv_rn(__uint_as_float(top), 6.f), 10240.f);
+  const float y = fminf(__fdiv_rn(top, 6.f), 10240.f);
   uint32_t byte;
   float scale;
   if (y >= 6.103515625e-05f) {   // 2^-14, the smallest normal scale: three mantissa bits, nearest even
@@ -111,8 +104,17 @@ __device__ __forceinline__ uint32_t quantise16(float* x) {
     byte = static_cast<uint32_t>(n);
     scale = n * 7.62939453125e-06f;
   }
+  // a zero scale: top is below half of the smallest, and all codes are zero
+  const float r = byte ? __frcp_rn(scale) : 0.f;
+  const unsigned long long r2 = pack_f2(r, r), s2 = pack_f2(-scale, -scale);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = byte ? __fdiv_rn(x[i], scale) : 0.f;
+  for (int i = 0; i < 16; i += 2) {
+    const unsigned long long v = pack_f2(x[i], x[i + 1]);
+    const unsigned long long q = ffma2_rn(v, r2, 0ull);
+    const unsigned long long z = ffma2_rn(ffma2_rn(q, s2, v), r2, q);
+    x[i] = lo_f(z);
+    x[i + 1] = hi_f(z);
+  }
   return byte;
 }
 
@@ -133,7 +135,7 @@ __device__ __forceinline__ void zero16(float* x) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(Kv4RowsParams p) {
+__global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_constant__ Kv4RowsParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const Kv4View& c = p.c;
@@ -209,12 +211,47 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(Kv4RowsParams p
   }
 }
 
+// Byte offset of 16-byte piece c (eight fp16 values) of row `row` in a warp's 16 x 256 byte stage. The swizzle lets the
+// eight lanes that store together, of both layouts, meet eight different pieces of the banks.
+__device__ __forceinline__ uint32_t stage_at(int row, int c) {
+  const int swizzle = ((c >> 3) & 1) ^ (((row >> 1) & 1) | ((row & 1) << 1) | (((row >> 2) & 1) << 2));
+  return row * 256 + ((c ^ swizzle) << 4);
+}
+
+// The stage's rows [from, to) to rows of T, coalesced; `out`: row 0.
 template <typename T>
-__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowsParams p) {
+__device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* out, long long stride, int from, int to) {
+  const int lane = threadIdx.x & 31;
+  if (sizeof(T) == 4) {           // a row an instruction
+#pragma unroll 4
+    for (int row = 0; row < kTileTok; ++row) {
+      const uint2 h = *reinterpret_cast<const uint2*>(stage + stage_at(row, lane >> 1) + (lane & 1) * 8);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h.x));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h.y));
+      if (row >= from && row < to)
+        reinterpret_cast<float4*>(out + row * stride)[lane] = make_float4(a.x, a.y, b.x, b.y);
+    }
+  } else {                        // two
+#pragma unroll 4
+    for (int k = 0; k < kTileTok / 2; ++k) {
+      const int row = 2 * k + (lane >> 4);
+      const uint4 h = *reinterpret_cast<const uint4*>(stage + stage_at(row, lane & 15));
+      if (row >= from && row < to)
+        reinterpret_cast<uint4*>(out + row * stride)[lane & 15] = make_uint4(Elem<T>::of(h.x), Elem<T>::of(h.y), Elem<T>::of(h.z), Elem<T>::of(h.w));
+    }
+  }
+}
+
+// Bound by memory: 144 bytes in and 256 values out a token and head. Values pass through shared memory as fp16
+// (exact), so that rows leave in whole lines.
+template <typename T>
+__global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const __grid_constant__ Kv4RowsParams p) {
+  __shared__ __align__(16) uint8_t stages[kRowsThreads / 32][kTileTok * 256];
   pdl_wait();
   pdl_launch_dependents();
   const Kv4View& c = p.c;
   const int lane = threadIdx.x & 31;
+  uint8_t* stage = stages[threadIdx.x >> 5];
   const int b = blockIdx.y;
   const int r0 = p.cu[b];
   const int p0 = p.start[b];
@@ -238,45 +275,48 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(Kv4RowsParams p)
       sc = __ldg(reinterpret_cast<const uint2*>(tile + kOffScale) + lane);
     }
     const int pos = t * kTileTok;
+    const int from = max(0, p0 - pos), to = min(kTileTok, p1 - pos);
+    const long long row0 = static_cast<long long>(r0) + (pos - p0);
     const int r = lane >> 2, q = lane & 3;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int pk = pos + half * 8 + r;
-      if (pk >= p0 && pk < p1) {
-        uint8_t* row = p.k + (static_cast<long long>(r0) + (pk - p0)) * p.k_tok + h * p.k_head + q * 32 * sizeof(T);
-        const uint32_t w[4] = {code[half].x, code[half].y, code[half].z, code[half].w};
-        uint32_t f[16];
+      const uint32_t w[4] = {code[half].x, code[half].y, code[half].z, code[half].w};
+      const uint32_t sa = scale_both(sc.x, 2 * half), sb = scale_both(sc.x, 2 * half + 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e2m1_to_f16x2(w[i], f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        const uint32_t sa = scale_both(sc.x, 2 * half), sb = scale_both(sc.x, 2 * half + 1);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = hmul2(f[i], i < 8 ? sa : sb);
-        Elem<T>::store16(row, f);
-        Elem<T>::store16(row + 16 * sizeof(T), f + 8);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t f[4];
+        e2m1_to_f16x2(w[i], f[0], f[1], f[2], f[3]);
+        const uint32_t s = i < 2 ? sa : sb;
+        *reinterpret_cast<uint4*>(stage + stage_at(half * 8 + r, q * 4 + i)) =
+            make_uint4(hmul2(f[0], s), hmul2(f[1], s), hmul2(f[2], s), hmul2(f[3], s));
       }
     }
+    __syncwarp();
+    store_rows<T>(stage, p.k + row0 * p.k_tok + h * p.k_head, p.k_tok, from, to);
+    __syncwarp();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int pv = pos + half * 8 + 2 * q;
-      const bool in0 = pv >= p0 && pv < p1, in1 = pv + 1 >= p0 && pv + 1 < p1;
-      if (in0 || in1) {
-        uint8_t* row = p.v + (static_cast<long long>(r0) + (pv - p0)) * p.v_tok + h * p.v_head + r * 16 * sizeof(T);
-        const uint32_t w[4] = {code[2 + half].x, code[2 + half].y, code[2 + half].z, code[2 + half].w};
-        uint32_t f[16], a[8], d[8];
+      const uint32_t w[4] = {code[2 + half].x, code[2 + half].y, code[2 + half].z, code[2 + half].w};
+      const uint32_t s = scale_pair(sc.y, 2 * half);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e2m1_to_f16x2(w[i], f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-        const uint32_t s = scale_pair(sc.y, 2 * half);
+      for (int i = 0; i < 2; ++i) {      // (token, token + 1) pairs to (dim, dim + 1) pairs, eight dims at a time
+        uint32_t f[8];
+        e2m1_to_f16x2(w[2 * i], f[0], f[1], f[2], f[3]);
+        e2m1_to_f16x2(w[2 * i + 1], f[4], f[5], f[6], f[7]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = hmul2(f[i], s);
+        for (int k = 0; k < 8; ++k) f[k] = hmul2(f[k], s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {   // (token, token + 1) pairs to (dim, dim + 1) pairs
-          a[i] = __byte_perm(f[2 * i], f[2 * i + 1], 0x5410);
-          d[i] = __byte_perm(f[2 * i], f[2 * i + 1], 0x7632);
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t sel = e ? 0x7632u : 0x5410u;
+          *reinterpret_cast<uint4*>(stage + stage_at(half * 8 + 2 * q + e, 2 * r + i)) =
+              make_uint4(__byte_perm(f[0], f[1], sel), __byte_perm(f[2], f[3], sel), __byte_perm(f[4], f[5], sel),
+                         __byte_perm(f[6], f[7], sel));
         }
-        if (in0) Elem<T>::store16(row, a);
-        if (in1) Elem<T>::store16(row + p.v_tok, d);
       }
     }
+    __syncwarp();
+    store_rows<T>(stage, p.v + row0 * p.v_tok + h * p.v_head, p.v_tok, from, to);
+    __syncwarp();
   }
 }
 
