@@ -118,15 +118,18 @@ __device__ __forceinline__ uint32_t quantise16(float* x) {
   return byte;
 }
 
-// Two values as one byte of codes (lo in the low nibble), nearest even, at most 6.
-__device__ __forceinline__ uint32_t codes2(float lo, float hi) {
-  uint32_t d;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}"
-      : "=r"(d)
-      : "f"(lo), "f"(hi));
-  return d;
+// Four pairs of values as four bytes of codes (a pair's first value in the low nibble), nearest even, at most 6.
+__device__ __forceinline__ uint32_t codes8(float a0, float a1, float b0, float b1, float c0, float c1, float d0, float d1) {
+  uint32_t w;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1), "f"(d0), "f"(d1));
+  return w;
 }
 
 __device__ __forceinline__ void zero16(float* x) {
@@ -170,11 +173,12 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_co
         Elem<T>::load16(row, x);
         Elem<T>::load16(row + 16 * sizeof(T), y);
         const uint32_t s = quantise16(x) | (quantise16(y) << 8);
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          w[i >> 2] |= codes2(x[2 * i], x[2 * i + 1]) << (8 * (i & 3));
-          w[2 + (i >> 2)] |= codes2(y[2 * i], y[2 * i + 1]) << (8 * (i & 3));
+        for (int i = 0; i < 2; ++i) {
+          const float *a = x + 8 * i, *e = y + 8 * i;
+          w[i] = codes8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
+          w[2 + i] = codes8(e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]);
         }
         reinterpret_cast<uint4*>(tile + half * 512)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
         scales.x = (scales.x & ~(0xffffu << (16 * half))) | (s << (16 * half));
@@ -191,9 +195,10 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_co
         if (in0) Elem<T>::load16(row, x); else zero16(x);
         if (in1) Elem<T>::load16(row + p.v_tok, y); else zero16(y);
         const uint32_t s0 = quantise16(x), s1 = quantise16(y);
-        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i >> 2] |= codes2(x[i], y[i]) << (8 * (i & 3));
+        for (int i = 0; i < 4; ++i)
+          w[i] = codes8(x[4 * i], y[4 * i], x[4 * i + 1], y[4 * i + 1], x[4 * i + 2], y[4 * i + 2], x[4 * i + 3], y[4 * i + 3]);
         uint32_t keep = (in0 ? 0u : 0x0f0f0f0fu) | (in1 ? 0u : 0xf0f0f0f0u);
         if (keep) {
           const uint4 old = *at;
