@@ -677,7 +677,9 @@ def _kv4_call(kv: KV4Cache, name: str, args, workspace_buf, stream) -> None:
         with torch.cuda.device(kv._index):
             return _kv4_call(kv, name, args, workspace_buf, stream)
     ws = _kv4_workspace(kv, workspace_buf, stream)
-    st = getattr(load_library(), name)(kv._ref, *args, ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream))
+    # the current stream as a handle: building the Stream object takes longer than the rest of a short call
+    raw = torch._C._cuda_getCurrentRawStream(kv._index) if stream is None else _stream(stream)
+    st = getattr(load_library(), name)(kv._ref, *args, ws.data_ptr(), ws.numel() * ws.element_size(), raw)
     if st != 0:
         raise HSAError(name, st)
 
@@ -696,7 +698,7 @@ def _kv4_cu(kv: KV4Cache, cu: torch.Tensor, cu_host: torch.Tensor, name: str) ->
             or cu_host.device.type != "cpu"):
         raise ValueError(f"{name}: expected contiguous int32 tensors [{kv.B + 1}] on the device and on the host")
     _kv4_on(kv, cu)
-    return int(cu_host[-1])
+    return ctypes.c_int32.from_address(cu_host.data_ptr() + 4 * kv.B).value
 
 
 def _kv4_type(*ts: torch.Tensor) -> int:

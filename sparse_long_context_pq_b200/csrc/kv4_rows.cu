@@ -15,29 +15,39 @@ namespace {
 
 constexpr int kRowsThreads = 256;
 
+// 16 values of T as they lie in memory.
+template <typename T>
+struct Raw {
+  uint4 v[sizeof(T)];
+  // zeros where not `in`: no branch, so that many loads are in flight
+  __device__ __forceinline__ void load(const uint8_t* p, bool in) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+      v[i] = in ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+};
+
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
-  static __device__ __forceinline__ void load16(const uint8_t* p, float* x) {
+  static __device__ __forceinline__ void widen(const Raw<float>& r, float* x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = reinterpret_cast<const float4*>(p)[i];
-      x[4 * i] = v.x;
-      x[4 * i + 1] = v.y;
-      x[4 * i + 2] = v.z;
-      x[4 * i + 3] = v.w;
+      x[4 * i] = __uint_as_float(r.v[i].x);
+      x[4 * i + 1] = __uint_as_float(r.v[i].y);
+      x[4 * i + 2] = __uint_as_float(r.v[i].z);
+      x[4 * i + 3] = __uint_as_float(r.v[i].w);
     }
   }
   static __device__ __forceinline__ uint32_t of(uint32_t h) { return h; }   // not used
 };
 template <>
 struct Elem<__nv_bfloat16> {
-  static __device__ __forceinline__ void load16(const uint8_t* p, float* x) {
+  static __device__ __forceinline__ void widen(const Raw<__nv_bfloat16>& r, float* x) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         x[8 * i + 2 * j] = bf16lo(w[j]);
@@ -53,11 +63,10 @@ struct Elem<__nv_bfloat16> {
 };
 template <>
 struct Elem<__half> {
-  static __device__ __forceinline__ void load16(const uint8_t* p, float* x) {
+  static __device__ __forceinline__ void widen(const Raw<__half>& r, float* x) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
@@ -80,8 +89,8 @@ __device__ __forceinline__ float max_abs(float m, float a, float b) {
 // a / 6 and x / scale are correctly rounded quotients: one at a rounding border of the few-bit
 // result is then exact, so ties are ties, and none beside a border reaches it. x / scale by the
 // reciprocal r = 1 / scale, correctly rounded, and one correction: y = x r, y + r (x - y scale)
-// (Markstein, IBM J. Res. Dev. 34, 1990); two fused steps for two values where a division takes
-// ten (measured: 32768 tokens x 8 heads from bf16 73 us with divisions, see the kernel).
+// (Markstein, IBM J. Res. Dev. 34, 1990), three instructions for two values (32768 tokens x 8 heads
+// from bf16 took 73 us with divisions, 47 with this).
 __device__ __forceinline__ uint32_t quantise16(float* x) {
   float top = 0.f;
 #pragma unroll
@@ -132,11 +141,8 @@ __device__ __forceinline__ uint32_t codes8(float a0, float a1, float b0, float b
   return w;
 }
 
-__device__ __forceinline__ void zero16(float* x) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = 0.f;
-}
-
+// Bound by memory (256 values in and 144 bytes out a token and head): the loads of a tile are all in flight before the
+// first is used (32768 tokens x 8 heads from bf16 47 -> 40 us, 4.3 TB/s; 131072 tokens 144 us, 4.8 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_constant__ Kv4RowsParams p) {
   pdl_wait();
@@ -162,44 +168,68 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_co
     const int pos = t * kTileTok;
     uint2* sw = reinterpret_cast<uint2*>(tile + kOffScale) + lane;
     const bool whole = pos >= p0 && pos + kTileTok <= p1;
-    uint2 scales = whole ? make_uint2(0u, 0u) : *sw;   // tokens that stay keep their bytes
     const int r = lane >> 2, q = lane & 3;
+    Raw<T> kr[2][2], vr[2][2];
+    auto load_k = [&]() {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int pk = pos + half * 8 + r;
+        const bool in = pk >= p0 && pk < p1;
+        const uint8_t* row = p.k + (static_cast<long long>(first) + pk) * p.k_tok + h * p.k_head + q * 32 * sizeof(T);
+        kr[half][0].load(row, in);
+        kr[half][1].load(row + 16 * sizeof(T), in);
+      }
+    };
+    auto load_v = [&]() {
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int pv = pos + half * 8 + 2 * q + e;
+          vr[half][e].load(p.v + (static_cast<long long>(first) + pv) * p.v_tok + h * p.v_head + r * 16 * sizeof(T),
+                           pv >= p0 && pv < p1);
+        }
+    };
+    load_k();
+    if (sizeof(T) == 2) load_v();                      // 64 registers in flight for either width
+    uint2 scales = whole ? make_uint2(0u, 0u) : *sw;   // tokens that stay keep their bytes
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+      if (pos + half * 8 >= p1 || pos + half * 8 + 8 <= p0) continue;   // no token of this half (a decode step has one)
       const int pk = pos + half * 8 + r;
-      if (pk >= p0 && pk < p1) {
-        const uint8_t* row = p.k + (static_cast<long long>(first) + pk) * p.k_tok + h * p.k_head + q * 32 * sizeof(T);
-        float x[16], y[16];
-        Elem<T>::load16(row, x);
-        Elem<T>::load16(row + 16 * sizeof(T), y);
-        const uint32_t s = quantise16(x) | (quantise16(y) << 8);
-        uint32_t w[4];
+      float x[16], y[16];
+      Elem<T>::widen(kr[half][0], x);
+      Elem<T>::widen(kr[half][1], y);
+      const uint32_t s = quantise16(x) | (quantise16(y) << 8);
+      uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float *a = x + 8 * i, *e = y + 8 * i;
-          w[i] = codes8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
-          w[2 + i] = codes8(e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const float *a = x + 8 * i, *e = y + 8 * i;
+        w[i] = codes8(a[0], a[1], a[2], a[3], a[4], a[5], a[6], a[7]);
+        w[2 + i] = codes8(e[0], e[1], e[2], e[3], e[4], e[5], e[6], e[7]);
+      }
+      if (pk >= p0 && pk < p1) {
         reinterpret_cast<uint4*>(tile + half * 512)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
         scales.x = (scales.x & ~(0xffffu << (16 * half))) | (s << (16 * half));
       }
     }
+    if (sizeof(T) == 4) load_v();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
+      if (pos + half * 8 >= p1 || pos + half * 8 + 8 <= p0) continue;
       const int pv = pos + half * 8 + 2 * q;
       const bool in0 = pv >= p0 && pv < p1, in1 = pv + 1 >= p0 && pv + 1 < p1;
-      if (in0 || in1) {
-        const uint8_t* row = p.v + (static_cast<long long>(first) + pv) * p.v_tok + h * p.v_head + r * 16 * sizeof(T);
-        float x[16], y[16];
-        uint4* at = reinterpret_cast<uint4*>(tile + kOffV + half * 512) + lane;
-        if (in0) Elem<T>::load16(row, x); else zero16(x);
-        if (in1) Elem<T>::load16(row + p.v_tok, y); else zero16(y);
-        const uint32_t s0 = quantise16(x), s1 = quantise16(y);
-        uint32_t w[4];
+      float x[16], y[16];
+      Elem<T>::widen(vr[half][0], x);
+      Elem<T>::widen(vr[half][1], y);
+      const uint32_t s0 = quantise16(x), s1 = quantise16(y);
+      uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = codes8(x[4 * i], y[4 * i], x[4 * i + 1], y[4 * i + 1], x[4 * i + 2], y[4 * i + 2], x[4 * i + 3], y[4 * i + 3]);
-        uint32_t keep = (in0 ? 0u : 0x0f0f0f0fu) | (in1 ? 0u : 0xf0f0f0f0u);
+      for (int i = 0; i < 4; ++i)
+        w[i] = codes8(x[4 * i], y[4 * i], x[4 * i + 1], y[4 * i + 1], x[4 * i + 2], y[4 * i + 2], x[4 * i + 3], y[4 * i + 3]);
+      if (in0 || in1) {
+        uint4* at = reinterpret_cast<uint4*>(tile + kOffV + half * 512) + lane;
+        const uint32_t keep = (in0 ? 0u : 0x0f0f0f0fu) | (in1 ? 0u : 0xf0f0f0f0u);
         if (keep) {
           const uint4 old = *at;
           w[0] = (w[0] & ~keep) | (old.x & keep);
@@ -248,7 +278,7 @@ __device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* out, l
 }
 
 // Bound by memory: 144 bytes in and 256 values out a token and head. Values pass through shared memory as fp16
-// (exact), so that rows leave in whole lines.
+// (exact), so that rows leave in whole lines (131072 tokens x 8 heads to bf16 148 -> 108 us, 6.35 TB/s).
 template <typename T>
 __global__ void __launch_bounds__(kRowsThreads) kv4_read_kernel(const __grid_constant__ Kv4RowsParams p) {
   __shared__ __align__(16) uint8_t stages[kRowsThreads / 32][kTileTok * 256];
