@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_co
     uint2 scales = whole ? make_uint2(0u, 0u) : *sw;   // tokens that stay keep their bytes
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (pos + half * 8 >= p1 || pos + half * 8 + 8 <= p0) continue;   // no token of this half (a decode step has one)
       const int pk = pos + half * 8 + r;
       float x[16], y[16];
       Elem<T>::widen(kr[half][0], x);
@@ -216,7 +215,6 @@ __global__ void __launch_bounds__(kRowsThreads) kv4_write_kernel(const __grid_co
     if (sizeof(T) == 4) load_v();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      if (pos + half * 8 >= p1 || pos + half * 8 + 8 <= p0) continue;
       const int pv = pos + half * 8 + 2 * q;
       const bool in0 = pv >= p0 && pv < p1, in1 = pv + 1 >= p0 && pv + 1 < p1;
       float x[16], y[16];
