@@ -615,6 +615,9 @@ class KV4Cache:
         object.__setattr__(self, "_struct", s)
         object.__setattr__(self, "_ref", ctypes.byref(s))
         object.__setattr__(self, "_index", c.device.index)
+        object.__setattr__(self, "_row_shape", (c.shape[1], HEAD_DIM))
+        object.__setattr__(self, "_per_seq", (B,))
+        object.__setattr__(self, "_offsets", (B + 1,))
 
     @staticmethod
     def empty(num_pages: int, Hkv: int, page_size: int, device) -> torch.Tensor:
@@ -685,25 +688,28 @@ def _kv4_call(kv: KV4Cache, name: str, args, workspace_buf, stream) -> None:
 
 
 def _kv4_rows(kv: KV4Cache, t: torch.Tensor, name: str, n: int) -> _KV4Rows:
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != kv.Hkv or t.shape[2] != HEAD_DIM or t.stride(2) != 1:
+    strides = t.stride()
+    if t.shape != (n,) + kv._row_shape or strides[2] != 1:
         raise ValueError(f"{name}: expected [{n}, {kv.Hkv}, {HEAD_DIM}] with contiguous rows")
-    return _KV4Rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return _KV4Rows(t.data_ptr(), strides[0], strides[1])
+
+
+def _kv4_ints(kv: KV4Cache, t: torch.Tensor, host: torch.Tensor, shape, name: str) -> None:
+    if (t.dtype != torch.int32 or host.dtype != torch.int32 or t.shape != shape or host.shape != shape
+            or not t.is_contiguous() or not host.is_contiguous() or host.is_cuda):
+        raise ValueError(f"{name}: expected contiguous int32 tensors {list(shape)} on the device and on the host")
+    _kv4_on(kv, t)
 
 
 def _kv4_cu(kv: KV4Cache, cu: torch.Tensor, cu_host: torch.Tensor, name: str) -> int:
     """Checks the row offsets of the sequences; returns the rows of the call."""
-    want = (kv.B + 1,)
-    if (cu.dtype != torch.int32 or cu_host.dtype != torch.int32 or tuple(cu.shape) != want
-            or tuple(cu_host.shape) != want or not cu.is_contiguous() or not cu_host.is_contiguous()
-            or cu_host.device.type != "cpu"):
-        raise ValueError(f"{name}: expected contiguous int32 tensors [{kv.B + 1}] on the device and on the host")
-    _kv4_on(kv, cu)
-    return ctypes.c_int32.from_address(cu_host.data_ptr() + 4 * kv.B).value
+    _kv4_ints(kv, cu, cu_host, kv._offsets, name)
+    return ctypes.c_int32.from_address(cu_host.data_ptr() + 4 * (kv._offsets[0] - 1)).value
 
 
-def _kv4_type(*ts: torch.Tensor) -> int:
-    code = _KV4_TYPES.get(ts[0].dtype)
-    if code is None or any(t.dtype != ts[0].dtype for t in ts):
+def _kv4_type(a: torch.Tensor, b: torch.Tensor) -> int:
+    code = _KV4_TYPES.get(a.dtype)
+    if code is None or b.dtype != a.dtype:
         raise ValueError("expected tensors of one type: float32, bfloat16 or float16")
     return code
 
@@ -730,16 +736,13 @@ def hsa_kv4_read(kv: KV4Cache, start: torch.Tensor, start_host: torch.Tensor, cu
     """Read positions [start[b], start[b] + n_b) of every sequence back (see hsa_kv4_read in include/pqhsa.h) as
     rows [cu[b], cu[b + 1]) of two tensors [rows, Hkv, 128], new ones of `dtype` or the given ones."""
     n = _kv4_cu(kv, cu, cu_host, "cu")
-    if (start.dtype != torch.int32 or start_host.dtype != torch.int32 or tuple(start.shape) != (kv.B,)
-            or tuple(start_host.shape) != (kv.B,) or not start.is_contiguous() or not start_host.is_contiguous()
-            or start_host.device.type != "cpu"):
-        raise ValueError(f"start: expected contiguous int32 tensors [{kv.B}] on the device and on the host")
+    _kv4_ints(kv, start, start_host, kv._per_seq, "start")
     new = lambda: torch.empty(n, kv.Hkv, HEAD_DIM, dtype=dtype, device=kv.cache.device)  # noqa: E731
     if k_out is None:
         k_out = _kv4_new(kv, stream, new)
     if v_out is None:
         v_out = _kv4_new(kv, stream, new)
-    _kv4_on(kv, start, k_out, v_out)
+    _kv4_on(kv, k_out, v_out)
     code = _kv4_type(k_out, v_out)
     if n == 0:
         return k_out, v_out
