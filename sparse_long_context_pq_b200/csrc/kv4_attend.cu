@@ -39,6 +39,7 @@ constexpr int kStep = 2;            // tiles a step
 constexpr int kStepTok = kStep * kTileTok;
 constexpr int kStepBytes = kStep * kTileBytes;
 constexpr float kHead = 11.f, kGrow = 4.f;
+constexpr float kWhole = 8388608.f;   // 2^23: larger logits are whole numbers, up to far more than kHead apart
 constexpr int kSoloSteps = 16;
 constexpr int kMergeThreads = 256;
 constexpr int kMergeWarps = kMergeThreads / 32;
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
               mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float next = fmaxf(ref[c], mx - kHead);
+              const float next = fmaxf(ref[c], fabsf(mx) < kWhole ? mx - kHead : mx);   // mx - 11 may round to mx - 16
               const float shrink = fast_exp2(ref[c] - next);
               ref[c] = next;
               l[c] *= shrink;

@@ -380,7 +380,180 @@ def test_prefill(cuda_device, kind, lens, news, Hkv, G, page, causal, window):
     assert case.error() == 0
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("lens,news,Hkv,G,units", [
+    ([9000], [30], 1, 4, None),                           # 120 rows, one unit over many blocks, steps on both halves
+    ([5000, 130], [70, 130], 2, 4, {(0, 1), (1, 0)}),     # 280 rows: a full unit and a rest of 24
+    ([128], [100], 1, 1, None),                           # a single step
+    ([257], [65], 1, 1, None),                            # three steps on two halves
+    ([40, 300], [90, 80], 1, 2, None),                    # rows before the first token, in units and beside them
+    ([12, 33], [200, 260], 1, 1, None),                   # units whose rows all see nothing
+])
+def test_prefill_units_of_many_rows(cuda_device, kind, lens, news, Hkv, G, units):
+    case = Case(lens, Hkv, G, 32, seed=sum(lens) + 1, filler=None if max(lens) > 2000 else 255)
+    case.device()
+    q = rows(case.rng, (sum(news), Hkv * G, D), kind)
+    out, lse = prefill(case, q, news, 0.11)
+    check(out, lse, q, case, news, 0.11, kind, units=units)
+    again, _ = prefill(case, q, news, 0.11)
+    assert torch.equal(out, again)
+    assert case.error() == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_prefill_large_logits_and_growing_maximum(cuda_device, kind):
+    """Logits of several hundred that grow from step to step and within a step, rows of zeros, negative scales."""
+    T, n = 420, 70
+    case = Case([T], 1, 2, 16, seed=6)
+    kv = case.device()
+    k = torch.randn(T, 1, D) * 0.3
+    k[:, 0, 0] = torch.linspace(0.1, 30.0, T)
+    cu = cu_of([T])
+    P.hsa_kv4_write(kv, k.to(cuda_device), torch.randn(T, 1, D).to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    q = rows(case.rng, (n, 2, D), kind)
+    q[:, 0, 0] = 25.0
+    q[3] = 0
+    q[5] *= 2.0 ** -12
+    for scale in (0.5, -0.5, 0.0):
+        out, lse = prefill(case, q, [n], scale)
+        check(out, lse, q, case, [n], scale, kind)
+
+
+@pytest.mark.parametrize("n", [9, 100])
+@pytest.mark.parametrize("kind,factor", [(k, f) for k in ("f32", "bf16", "f16") for f in (1e5, 1e6, 3e6, 1e7, 3e7, 1e9)
+                                         if (k, f) != ("f16", 1e9)])      # q of that size is not finite in fp16
+def test_huge_logits_stay_finite(cuda_device, kind, factor, n):
+    """Logits up to 10^10: nearly all weight is on the largest, and nothing overflows."""
+    if kind == "f16":
+        factor /= 65536.0
+    T = 300
+    case = Case([T], 1, 1, 16, seed=16)
+    case.device()
+    q = rows(case.rng, (n, 1, D), kind) * factor
+    scale = 65536.0 if kind == "f16" else 1.0
+    out, lse = prefill(case, q, [n], scale)
+    k, v = case.held(0, 0)
+    best = (q[:, 0].double().numpy() @ k.T) * scale
+    best[np.arange(T)[None] > (T - n + np.arange(n))[:, None]] = -np.inf
+    at = best.argmax(1)
+    got = out[:, 0].double().cpu().numpy()
+    assert np.isfinite(got).all() and torch.isfinite(lse).all()
+    gap = np.sort(best, 1)[:, -1] - np.sort(best, 1)[:, -2]
+    clear = gap > 1e-5 * np.abs(best.max(1)) + 100       # far more than the rounding of a logit
+    assert clear.any()
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind]
+    ref = v[at]
+    assert (np.abs(got - ref)[clear] <= (2 * half + 2.0 ** -11) * np.abs(ref)[clear] + 1e-30).all()
+
+
+@pytest.mark.parametrize("rows_of", ["few", "many"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_many_sequences(cuda_device, kind, rows_of):
+    """More sequences than lanes of a warp, many of them empty or without queries."""
+    rng = np.random.default_rng(40)
+    B = 70
+    lens = [int(x) for x in rng.integers(0, 90, B)]
+    lens[0], lens[50] = 700, 1500
+    news = [int(rng.integers(0, 4)) for _ in range(B)]
+    if rows_of == "many":
+        news[0], news[50] = 90, 33
+    case = Case(lens, 1, 4, 16, seed=41)
+    case.device()
+    q = rows(case.rng, (sum(news), 4, D), kind)
+    out, lse = prefill(case, q, news, 0.1)
+    check(out, lse, q, case, news, 0.1, kind)
+    q1 = rows(case.rng, (B, 4, D), kind)
+    out, lse = decode(case, q1, 0.1)
+    check(out, lse, q1, case, [1] * B, 0.1, kind)
+    assert case.error() == 0
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_units_of_all_row_counts(cuda_device, kind):
+    """1 to 130 query rows a KV head: every row tile of the streaming kernel, the border to the other, its two shapes."""
+    case = Case([333], 1, 1, 16, seed=50)
+    case.device()
+    for n in (1, 4, 5, 8, 9, 16, 17, 24, 25, 32, 33, 40, 63, 64, 65, 127, 128, 129, 130):
+        q = rows(case.rng, (n, 1, D), kind)
+        out, lse = prefill(case, q, [n], 0.1)
+        check(out, lse, q, case, [n], 0.1, kind)
+
+
 # ---- what the calls promise ------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("n", [60, 200])
+def test_masked_nan_does_not_spread_in_long_chunks(cuda_device, n):
+    """The same in units of 128 and of 256 rows, bad tokens in several steps."""
+    T = 400
+    case = Case([T], 1, 2, 16, seed=18)
+    kv = case.device()
+    k, v = torch.randn(T, 1, D), torch.randn(T, 1, D)
+    v[T - 40, 0, 37] = float("nan")
+    v[T - 3, 0, 100] = float("inf")
+    k[T - 20, 0, 5] = float("nan")
+    cu = cu_of([T])
+    P.hsa_kv4_write(kv, k.to(cuda_device), v.to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    q = rows(case.rng, (n, 2, D), "bf16")
+    for window in (0, 10):
+        out, lse = prefill(case, q, [n], 0.1, window=window)
+        bad = torch.isnan(out).cpu()
+        assert not bad[:n - 40].any() and bad[n - 40, :, 32:48].all() and not bad[n - 40, :, :32].any()
+        assert bad[n - 20].all()
+        check(out, lse, q, case, [n], 0.1, "bf16", window=window)
+
+
+def test_bad_pages_in_long_chunks(cuda_device):
+    """Tokens of a page that the block table does not name take no part, and are flagged."""
+    T, n = 500, 90
+    case = Case([T], 1, 2, 32, seed=19)
+    kv = case.device()
+    kv.block_table[0, 3] = -1
+    kv.block_table[0, 9] = 1 << 20
+    q = rows(case.rng, (n, 2, D), "bf16")
+    out, lse = prefill(case, q, [n], 0.1)
+    assert case.error() == P.HSA_DEVERR_PAGE
+    k, v = case.held(0, 0)
+    j = np.arange(T)
+    seen = j[None] <= (T - n + np.arange(n))[:, None]
+    seen &= ~((j // 32 == 3) | (j // 32 == 9))[None]
+    for g in range(2):
+        ref, ref_lse = O4.attend(q[:, g].double().numpy(), k, v, 0.1, seen)
+        assert np.abs(out[:, g].double().cpu().numpy() - ref).max() <= (2.0 ** -8 + 2.0 ** -10) * np.abs(v).max()
+        assert np.abs(lse[:, g].double().cpu().numpy() - ref_lse).max() <= 1e-4
+
+
+def test_prefill_captured_and_replayed(cuda_device):
+    """A captured chunk (write, attend) replayed with other data and lengths."""
+    case = Case([900, 500], 2, 4, 16, seed=60)
+    kv = case.device()
+    n = [70, 40]
+    cu = cu_of(n)
+    cud = cu.to(cuda_device)
+    k, v = torch.randn(110, 2, D, device=cuda_device).half(), torch.randn(110, 2, D, device=cuda_device).half()
+    q = torch.randn(110, 8, D, device=cuda_device).half()
+    out = torch.empty_like(q)
+
+    def step(w):
+        P.hsa_kv4_write(kv, k, v, cud, cu, workspace_buf=w)
+        P.dense_prefill_kv4(kv, q, cud, cu, out, scale=0.1, workspace_buf=w)
+
+    step(case.ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(case.ws)
+    for lens in ([900, 500], [330, 41], [70, 300]):
+        kv.seq_lens.copy_(i32(lens))
+        for x in (k, v, q):
+            x.normal_()
+        graph.replay()
+        got = out.clone()
+        kv.seq_lens_host.copy_(i32(lens))
+        step(P.workspace(P.hsa_kv4_workspace_bytes(kv), cuda_device))
+        assert torch.equal(got, out)
+    assert case.error() == 0
 
 
 def test_bad_pages_are_flagged_and_skipped(cuda_device):
