@@ -354,8 +354,15 @@ hsa_status hsa_train_index(const hsa_kv_cache* kv, hsa_index* index, int32_t n_t
  * page block_table[b * max_pages + t / page_size]. The kernels go by the device arrays; the
  * *_host copies serve validation and planning, so a captured call may be replayed with other
  * lengths as long as they fit the block table and, where a call takes rows, the row counts do
- * not grow. Every call takes the same workspace (hsa_kv4_workspace_bytes; error word first,
- * see hsa_read_error); calls that overlap on the GPU need one each.
+ * not grow. (How many blocks share the work is planned for the lengths of the call that is
+ * captured: capture with long ones.) Every call takes the same workspace
+ * (hsa_kv4_workspace_bytes; error word first, see hsa_read_error); calls that overlap on the GPU
+ * need one each, so do captured graphs whose replays may overlap.
+ *
+ * Limits (HSA_ERR_UNSUPPORTED beyond): 65535 sequences, 2^30 positions a block table row, 2^31
+ * tiles in the cache, 2^25 query rows a KV head, and in attention of few rows 2^30 steps of 32
+ * tokens over all sequences, KV heads and row tiles. Logits are held in fp32 (times log2(e), so
+ * below 2.3e38); q and out do not overlap.
  */
 #define HSA_KV4_TILE_TOKENS 16
 #define HSA_KV4_TILE_BYTES 2304

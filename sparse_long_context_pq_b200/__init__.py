@@ -696,7 +696,7 @@ def _kv4_rows(kv: KV4Cache, t: torch.Tensor, name: str, n: int) -> _KV4Rows:
 
 def _kv4_ints(kv: KV4Cache, t: torch.Tensor, host: torch.Tensor, shape, name: str) -> None:
     if (t.dtype != torch.int32 or host.dtype != torch.int32 or t.shape != shape or host.shape != shape
-            or not t.is_contiguous() or not host.is_contiguous() or host.is_cuda):
+            or not t.is_contiguous() or not host.is_contiguous() or not host.is_cpu):
         raise ValueError(f"{name}: expected contiguous int32 tensors {list(shape)} on the device and on the host")
     _kv4_on(kv, t)
 
@@ -752,6 +752,11 @@ def hsa_kv4_read(kv: KV4Cache, start: torch.Tensor, start_host: torch.Tensor, cu
     return k_out, v_out
 
 
+def _kv4_window(window: int) -> int:
+    """As an int32: more than any sequence has is all the same."""
+    return max(-1, min(window, (1 << 31) - 1))
+
+
 def _kv4_out(kv: KV4Cache, q: torch.Tensor, out: Optional[torch.Tensor], lse: Optional[torch.Tensor], stream):
     shape = q.shape
     if out is None:
@@ -772,7 +777,8 @@ def dense_decode_kv4(kv: KV4Cache, q: torch.Tensor, out: Optional[torch.Tensor] 
     if tuple(q.shape) != (kv.B, kv.Hq, HEAD_DIM) or not q.is_contiguous():
         raise ValueError(f"q: expected a contiguous tensor [{kv.B}, {kv.Hq}, {HEAD_DIM}]")
     out = _kv4_out(kv, q, out, lse, stream)
-    _kv4_call(kv, "dense_decode_kv4", (q.data_ptr(), out.data_ptr(), _ptr(lse), _kv4_type(q, out), scale, window),
+    _kv4_call(kv, "dense_decode_kv4", (q.data_ptr(), out.data_ptr(), _ptr(lse), _kv4_type(q, out), scale,
+                                       _kv4_window(window)),
               workspace_buf, stream)
     return out
 
@@ -791,7 +797,8 @@ def dense_prefill_kv4(kv: KV4Cache, q: torch.Tensor, cu_q: torch.Tensor, cu_q_ho
     code = _kv4_type(q, out)
     if n == 0:
         return out
-    _kv4_call(kv, "dense_prefill_kv4", (q.data_ptr(), q.stride(0), out.data_ptr(), _ptr(lse), code, cu_q.data_ptr(),
-                                        cu_q_host.data_ptr(), scale, 1 if causal else 0, window),
+    stride = q.stride(0) if n > 1 else kv.Hq * HEAD_DIM    # of a single row: anything
+    _kv4_call(kv, "dense_prefill_kv4", (q.data_ptr(), stride, out.data_ptr(), _ptr(lse), code, cu_q.data_ptr(),
+                                        cu_q_host.data_ptr(), scale, 1 if causal else 0, _kv4_window(window)),
               workspace_buf, stream)
     return out

@@ -35,7 +35,7 @@ hsa_status check_kv4(const hsa_kv4_cache* kv) {
     return HSA_ERR_UNSUPPORTED;
   if (!aligned(kv->cache, 256) || !aligned(kv->block_table, 4) || !aligned(kv->seq_lens, 4)) return HSA_ERR_ALIGNMENT;
   const long long tmax = static_cast<long long>(kv->max_pages) * kv->page_size;
-  if (tmax >= (1LL << 31)) return HSA_ERR_UNSUPPORTED;   // positions are 32-bit
+  if (tmax >= (1LL << 30)) return HSA_ERR_UNSUPPORTED;   // differences of positions, rows and windows are 32-bit
   if (static_cast<long long>(kv->num_pages) * kv->Hkv * (kv->page_size / kTileTok) >= (1LL << 31))
     return HSA_ERR_UNSUPPORTED;                          // tile numbers are 32-bit
   for (int b = 0; b < kv->B; ++b)
@@ -123,6 +123,7 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   st = check_workspace(ws, ws_bytes);
   if (st != HSA_OK) return st;
   if (n_rows == 0) return HSA_OK;
+  if (q == out) return HSA_ERR_INVALID_ARG;   // blocks read q while others write
   const int sms = device_sms();
   if (!sms) return HSA_ERR_CUDA;
   Kv4AttendParams p = {};
@@ -135,7 +136,7 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   p.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
   p.n_rows = n_rows;
   p.causal = causal;
-  p.window = window;
+  p.window = window < static_cast<long long>(kv->max_pages) * kv->page_size ? window : 0;   // else it leaves nothing out
   p.G = kv->Hq / kv->Hkv;
   p.inv_G = static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G);   // not used for G = 1
   p.scale = scale;

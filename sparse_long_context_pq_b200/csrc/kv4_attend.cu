@@ -117,7 +117,7 @@ __device__ __forceinline__ Seq sequence(const Kv4AttendParams& p, int b, int RT)
   s.n = p.cu ? p.cu[b + 1] - s.r0 : 1;
   s.n = max(0, min(s.n, p.n_rows - s.r0));
   if (s.r0 < 0) s.n = 0;
-  const int first = s.T - s.n - p.window + 1;   // leftmost position of a window (all below 2^31)
+  const int first = s.T - s.n - p.window + 1;   // leftmost position of a window (T and the window are below 2^30)
   s.lo = p.window > 0 && first > 0 ? first / kStepTok : 0;
   const int hi = (s.T + kStepTok - 1) / kStepTok;
   s.nt = s.n > 0 ? hi - s.lo : 0;
@@ -942,7 +942,7 @@ int kv4_attend_rows(int dtype, int max_rows) {
   return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 24 ? 24 : 32;
 }
 
-// Two slots a block and one a warp: 18 of 8 rows, 14 of 16, 12 of 24, 10 of 32.
+// Two slots a block and one a warp: 18 of 8 rows or 10 of 16, 24 or 32.
 size_t kv4_attend_part_bytes() {
   return static_cast<size_t>(2 + 8) * kKv4MaxSms * 32 * (kD + 2) * sizeof(float);
 }

@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   if (blockIdx.y * 32 >= u.rows) return;
   int parts = 1;
   while (c + parts < blocks && !info[2 * (c + parts)].ends) ++parts;
-  ++parts;   // the one that ends it
+  parts = min(parts + 1, blocks - c);   // with the one that ends it
 #pragma unroll 1
   for (int d8 = warp; d8 < kD / 8; d8 += kMergeWarps) {
     float m = -1e30f, l = 0.f;

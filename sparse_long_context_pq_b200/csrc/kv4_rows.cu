@@ -40,7 +40,6 @@ struct Elem<float> {
       x[4 * i + 3] = __uint_as_float(r.v[i].w);
     }
   }
-  static __device__ __forceinline__ uint32_t of(uint32_t h) { return h; }   // not used
 };
 template <>
 struct Elem<__nv_bfloat16> {
@@ -255,7 +254,7 @@ __device__ __forceinline__ uint32_t stage_at(int row, int c) {
 template <typename T>
 __device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* out, long long stride, int from, int to) {
   const int lane = threadIdx.x & 31;
-  if (sizeof(T) == 4) {           // a row an instruction
+  if constexpr (sizeof(T) == 4) { // a row an instruction
 #pragma unroll 4
     for (int row = 0; row < kTileTok; ++row) {
       const uint2 h = *reinterpret_cast<const uint2*>(stage + stage_at(row, lane >> 1) + (lane & 1) * 8);
@@ -270,7 +269,8 @@ __device__ __forceinline__ void store_rows(const uint8_t* stage, uint8_t* out, l
       const int row = 2 * k + (lane >> 4);
       const uint4 h = *reinterpret_cast<const uint4*>(stage + stage_at(row, lane & 15));
       if (row >= from && row < to)
-        reinterpret_cast<uint4*>(out + row * stride)[lane & 15] = make_uint4(Elem<T>::of(h.x), Elem<T>::of(h.y), Elem<T>::of(h.z), Elem<T>::of(h.w));
+        reinterpret_cast<uint4*>(out + row * stride)[lane & 15] =
+            make_uint4(Elem<T>::of(h.x), Elem<T>::of(h.y), Elem<T>::of(h.z), Elem<T>::of(h.w));
     }
   }
 }

@@ -694,6 +694,83 @@ def test_refusals_with_device_tensors(cuda_device):
         P.dense_prefill_kv4(kv, torch.zeros(2, 4, 2 * D, device=cuda_device)[..., :D].transpose(0, 1), cud, cu, scale=0.1)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_windows_larger_than_any_sequence(cuda_device, kind):
+    """A window that leaves nothing out, up to the largest int and past it, with rows before the first token."""
+    case = Case([50, 3], 1, 2, 16, seed=80)
+    case.device()
+    for news in ([10, 20], [90, 1]):
+        q = rows(case.rng, (sum(news), 2, D), kind)
+        want, want_lse = prefill(case, q, news, 0.1)
+        for window in (64, (1 << 31) - 1, (1 << 32) + 5):
+            out, lse = prefill(case, q, news, 0.1, window=window)
+            assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_sequences_that_share_pages(cuda_device, kind):
+    """The same pages at the front of every sequence, and twice in one."""
+    case = Case([64, 80, 100], 2, 2, 16, seed=81)
+    case.table[1, :3] = case.table[0, :3]
+    case.table[2, :3] = case.table[0, :3]
+    case.table[2, 4] = case.table[0, 1]
+    case.device()
+    for news in ([1, 1, 1], [40, 50, 60]):
+        q = rows(case.rng, (sum(news), 4, D), kind)
+        out, lse = prefill(case, q, news, 0.1)
+        check(out, lse, q, case, news, 0.1, kind)
+
+
+@pytest.mark.parametrize("n", [3, 40])
+def test_rows_apart_and_behind_stay(cuda_device, n):
+    """q as a view of a fused projection; a tensor behind out and lse keeps its bytes; a single row of any stride."""
+    case = Case([200], 2, 4, 16, seed=82)
+    kv = case.device()
+    fused = torch.randn(n, 8 + 2 + 2, D, device=cuda_device).bfloat16()
+    big = torch.full((n + 4, 8, D), 7.0, device=cuda_device, dtype=torch.bfloat16)
+    lse = torch.full((n + 4, 8), 7.0, device=cuda_device)
+    cu = cu_of([n])
+    q = fused[:, :8]
+    P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, big[:n], scale=0.1, lse=lse[:n])
+    check(big[:n], lse[:n], q.cpu(), case, [n], 0.1, "bf16")
+    assert (big[n:] == 7).all() and (lse[n:] == 7).all()
+    one = torch.randn(8, D, device=cuda_device).bfloat16().as_strided((1, 8, D), (3, D, 1))
+    cu = cu_of([1])
+    out = P.dense_prefill_kv4(kv, one, cu.to(cuda_device), cu, scale=0.1)
+    assert torch.equal(out, P.dense_decode_kv4(kv, one.contiguous().view(1, 8, D), scale=0.1))
+
+
+def test_chunks_on_two_streams(cuda_device):
+    """Writes and chunks of two caches on two streams at once, each with its workspace, against one after the other."""
+    cases = [Case([3000], 2, 4, 16, seed=90 + i) for i in range(2)]
+    work = []
+    for c in cases:
+        kv = c.device()
+        n = 150
+        cu = cu_of([n])
+        k, v = (torch.randn(n, 2, D, device=cuda_device).half() for _ in range(2))
+        q = torch.randn(n, 8, D, device=cuda_device).half()
+        work.append((kv, k, v, q, cu.to(cuda_device), cu, P.workspace(P.hsa_kv4_workspace_bytes(kv), cuda_device)))
+
+    def run(w, stream=None):
+        kv, k, v, q, cud, cu, ws = w
+        outs = []
+        for _ in range(4):
+            P.hsa_kv4_write(kv, k, v, cud, cu, workspace_buf=ws, stream=stream)
+            outs.append(P.dense_prefill_kv4(kv, q, cud, cu, scale=0.1, workspace_buf=ws, stream=stream))
+        return outs
+
+    want = [run(w) for w in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in work]
+    got = [run(w, s) for w, s in zip(work, streams)]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+    assert all(P.hsa_read_error(w[-1]) == 0 for w in work)
+
+
 # ---- together --------------------------------------------------------------------------------------------------
 
 

@@ -146,6 +146,23 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         P.KV4Cache.empty(4, 2, 24, "cpu")
 
 
+def test_limits(lib):
+    kv, host = _kv(B_=1, max_pages=(1 << 30) // 16)                    # positions up to 2^30
+    assert lib.hsa_kv4_workspace_bytes(ctypes.byref(kv)) == 0
+    kv, host = _kv(Hkv=8, num_pages=1 << 28)                           # 2^31 tiles
+    assert _decode(lib, kv, n=1 << 30) == 2
+    kv, host = _kv(B_=65536)
+    assert _decode(lib, kv, n=1 << 30) == 2
+    kv, host = _kv(Hq=256, Hkv=2)
+    assert _prefill(lib, kv, _cu(1 << 18, 0), out=2 * FAKE) == 2       # 2^25 query rows a head
+
+
+def test_attention_refuses_to_write_over_its_queries(lib):
+    kv, host = _kv()
+    assert _decode(lib, kv) == 1
+    assert _prefill(lib, kv, _cu(1, 1)) == 1
+
+
 # ---- the oracle's format, from its definition ----
 
 def test_scales_are_shifted_halves():
