@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint32_t tmem_slot;
   __shared__ Walk walks[kThreads / 32];
-  __shared__ Segment segments_s[kThreads / 32];
+  __shared__ Segment segments_s[kThreads / 32 + 8];   // the softmax warps have two
   __shared__ float factor[kRows];     // logits from S, in log2 units
   __shared__ float2 other[128];       // ref and l of the odd steps' half
   __shared__ unsigned other_poison[128];
@@ -457,47 +457,53 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
 
   // in shared memory, a copy a warp: the registers are wanted elsewhere
   Walk& walk = walks[warp];
-  Segment& cur = segments_s[warp];
   walk.start(p);
   if (warp < 8) {
     // ================= q, and softmax: one row a thread =================
     const int half = warp >> 2;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
+    bool more = walk.next(p, segments_s[warp]);
     int done = 0;         // this half's steps so far: phase of its barriers
     int it = 0;           // the block's steps so far: place of their flags
     bool ok = true;       // a wait gave up: from there on only the barriers, which all eight warps pass
 #pragma unroll 1
-    for (int segments = 0; walk.next(p, cur); ++segments) {
+    for (int segments = 0; more; ++segments) {
+      const Segment& cur = segments_s[warp + (segments & 1 ? kThreads / 32 : 0)];
       const int first_step = cur.k0, steps = cur.k1 - first_step;
       const bool split = cur.rows <= 128;
       // ---- q: rows over a power of two (with the scale's sign), fp16, K-major swizzled ----
+      // two rows an instruction, eight values a lane, all of a warp's rows in flight
       const int mine = split ? 16 : 32;       // rows of this warp
-#pragma unroll 1
-      for (int base = 0; base < mine; base += 16) {
-        uint2 x8[16];
+      {
+        uint4 x8[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int row = min(warp * mine + base + k, cur.rows - 1);
+          const int row = min(warp * mine + min(2 * k, mine - 2) + (lane >> 4), cur.rows - 1);
           const int i = token_of(p, cur.row0 + row);
-          x8[k] = __ldg(reinterpret_cast<const uint2*>(
+          x8[k] = __ldg(reinterpret_cast<const uint4*>(
               p.q + (static_cast<long long>(cur.r0) + i) * p.q_tok +
-              (static_cast<size_t>(cur.h) * p.G + (cur.row0 + row - i * p.G)) * kD * sizeof(T) + lane * 4 * sizeof(T)));
+              (static_cast<size_t>(cur.h) * p.G + (cur.row0 + row - i * p.G)) * kD * sizeof(T)) + (lane & 15));
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-          const int row = warp * mine + base + k;
-          const float4 x = q4_of<T>(x8[k]);
-          const float top = warp_max_f32(fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+          if (2 * k >= mine) break;
+          const int row = warp * mine + 2 * k + (lane >> 4);
+          const float4 a = q4_of<T>(make_uint2(x8[k].x, x8[k].y)), b = q4_of<T>(make_uint2(x8[k].z, x8[k].w));
+          float top = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                            fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
           e = e > 126 ? 0 : max(e, -126);
           const float down = copysignf(__int_as_float((127 - e) << 23), p.scale);
-          const int r = row & 127, chunk = (lane & 15) >> 1;
-          *reinterpret_cast<uint2*>(sm + Smem::q + (row >> 7) * kOperand + (lane >> 4) * kHalfOp + r * 128 +
-                                    ((chunk ^ (r & 7)) << 4) + (lane & 1) * 8) =
-              make_uint2(pack_f16x2(x.x * down, x.y * down), pack_f16x2(x.z * down, x.w * down));
+          const int r = row & 127;
+          store16(smem_addr(sm) + Smem::q + (row >> 7) * kOperand + ((lane >> 3) & 1) * kHalfOp + r * 128 +
+                      (((lane & 7) ^ (r & 7)) << 4),
+                  pack_f16x2(a.x * down, a.y * down), pack_f16x2(a.z * down, a.w * down),
+                  pack_f16x2(b.x * down, b.y * down), pack_f16x2(b.z * down, b.w * down));
           // never so small that a masked logit, -inf times f, is NaN
-          if (lane == 0) factor[row] = fmaxf(fabsf(p.scale * kLog2e * __int_as_float((e + 127) << 23)), 1e-36f);
+          if ((lane & 15) == 0) factor[row] = fmaxf(fabsf(p.scale * kLog2e * __int_as_float((e + 127) << 23)), 1e-36f);
         }
       }
       fence_proxy_async_smem();
@@ -627,6 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         half_barrier(half);   // this half's weights are there, for its MMA warp
       }
       it += steps;
+      more = walk.next(p, segments_s[warp + (segments & 1 ? 0 : kThreads / 32)]);   // while the last products run
       ok = ok && wait_long_warp(o_full + half, segments & 1, p.c.err);
       tc_fence_after();
       // ---- the result, or a partial ----
@@ -760,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     const uint32_t sel0 = r & 1 ? 0x7632u : 0x5410u, sel1 = r & 1 ? 0x5410u : 0x7632u;
     int it = 0;
     bool ok = true;
+    Segment& cur = segments_s[warp];
 #pragma unroll 1
     while (ok && walk.next(p, cur)) {
       const int steps = cur.k1 - cur.k0, tokens = cur.T, k0 = cur.k0;
@@ -905,6 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     const int half = warp - 12;
     int it = 0;
     bool ok = true;
+    Segment& cur = segments_s[warp];
 #pragma unroll 1
     while (walk.next(p, cur)) {
       const int steps = cur.k1 - cur.k0;
