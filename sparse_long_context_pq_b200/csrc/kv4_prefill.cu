@@ -22,8 +22,10 @@
 //
 // What bounds it: the tensor cores need 2048 clocks for a step (4 x 128 x 128 x 128 products),
 // ex2 as many (256 x 128 at 16 a clock), shared memory about 2000 (operands and dequantised tiles).
-// Measured, a step takes more than twice that: a softmax warp's chain (S, maximum, weights, P) and
-// the issue slots that eight softmax and eight dequantising warps share stand in the way.
+// Measured, a step takes about 5400 (2048 tokens over 32768, 32 heads on 8: 1.38 ms, 770 TFLOP/s): a
+// half's chain is S full, maximum, weights, P, P V, the next S, with its softmax (about 2400 for 128 rows
+// x 128 tokens) beside the other half's on the same schedulers, and TMEM has no room for a second S.
+// Between two segments there are about 12000 clocks of output and q (4 sequences of 2048: 0.34 ms).
 //
 // q, weights and their accuracy are those of kv4_attend.cu for 16-bit calls: q over a power of two
 // in fp16, P in fp16 up to 2^(kHead + kGrow), sums and statistics in fp32. ref moves by whole
