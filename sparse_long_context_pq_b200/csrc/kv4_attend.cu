@@ -31,7 +31,7 @@
 // for the chain lengths -> block table -> tiles, the join and the merge kernel (8 heads of 131072
 // tokens 39.0 us with fp32 q, 37.7 us with bf16 q; 1000 tokens 8.9 us). Many rows a tile: the
 // tensor instructions of the older kind and the work of making fragments (20 rows on 16 x 8
-// heads of 5000 tokens 47 us).
+// heads of 5000 tokens each 47 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -49,6 +49,7 @@ constexpr float kHead = 11.f, kGrow = 4.f;
 constexpr float kWhole = 8388608.f;   // 2^23: larger logits are whole numbers, up to far more than kHead apart
 constexpr int kSoloSteps = 16;
 constexpr int kMergeThreads = 256;
+constexpr int kTeamParts = 4;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kPitch = kD + 4;      // floats a row of a warp's partial in shared memory
 constexpr int kQPitch = 2 * kD + 16; // bytes a row of q in shared memory
@@ -793,8 +794,8 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
   }
 }
 
-// One block a query row of a unit: joins the partials of a unit that several blocks shared.
-template <typename T>
+// Joins the partials of units that several blocks shared, kTeam warps a query row.
+template <typename T, int kTeam>
 __global__ void __launch_bounds__(kMergeThreads)
     kv4_merge_kernel(const __grid_constant__ Kv4AttendParams p, int RT, int blocks) {
   __shared__ float4 acc_s[kMergeWarps][32];
@@ -805,7 +806,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int b = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Seq s = sequence(p, b, RT);
   const int rows_all = s.n * p.G;                       // query rows of a head
-  const int h = blockIdx.x % p.c.Hkv;
+  const int team = warp / kTeam, member = warp % kTeam;
   int before = 0, W = 0;
 #pragma unroll 1
   for (int i = lane; i - lane < p.c.B; i += 32) {
@@ -816,7 +817,9 @@ __global__ void __launch_bounds__(kMergeThreads)
   const Line line(W, blocks);
   pdl_wait();
 #pragma unroll 1
-  for (int qrow = blockIdx.x / p.c.Hkv; qrow < rows_all && s.nt > 0; qrow += gridDim.x / p.c.Hkv) {
+  for (unsigned item = blockIdx.x * (kMergeWarps / kTeam) + team; s.nt > 0; item += gridDim.x * (kMergeWarps / kTeam)) {
+    const int qrow = item / p.c.Hkv, h = item % p.c.Hkv;
+    if (qrow >= rows_all) break;
     const int rt = qrow / RT, row = qrow % RT;
     const int u0 = before + (h * s.nrt + rt) * s.nt;
     const int c0 = line.block_of(u0), c1 = line.block_of(u0 + s.nt - 1);
@@ -825,16 +828,16 @@ __global__ void __launch_bounds__(kMergeThreads)
     const float* slots = p.parts + static_cast<size_t>(2 * c0) * RT * (kD + 2);
     const int parts = c1 - c0 + 1;
     auto slot_of = [&](int i) { return slots + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * RT * (kD + 2); };
-    // a warp takes every eighth part, four in flight
+    // a warp takes every kTeam-th part, four in flight
     float m = -1e30f, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-    for (int i0 = warp; i0 < parts; i0 += 4 * kMergeWarps) {
+    for (int i0 = member; i0 < parts; i0 += 4 * kTeam) {
       float mi[4], li[4];
       float4 v[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int i = i0 + k * kMergeWarps;
+        const int i = i0 + k * kTeam;
         const float* slot = slot_of(min(i, parts - 1));
         mi[k] = slot[row];
         li[k] = slot[RT + row];
@@ -851,7 +854,7 @@ __global__ void __launch_bounds__(kMergeThreads)
       acc.w *= old;
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (i0 + k * kMergeWarps >= parts) break;
+        if (i0 + k * kTeam >= parts) break;
         const float y = fast_exp2(mi[k] - m);
         l = fmaf(li[k], y, l);
         acc.x = fmaf(v[k].x, y, acc.x);
@@ -859,6 +862,10 @@ __global__ void __launch_bounds__(kMergeThreads)
         acc.z = fmaf(v[k].z, y, acc.z);
         acc.w = fmaf(v[k].w, y, acc.w);
       }
+    }
+    if constexpr (kTeam == 1) {
+      finish<T>(p, head_row(p, s.r0, h, qrow), lane, m, l, acc);
+      continue;
     }
     acc_s[warp][lane] = acc;
     if (lane == 0) {
@@ -909,11 +916,12 @@ cudaError_t launch_attend_t(Kv4AttendParams p, const Kv4Load& load, int sms, cud
   if (e != cudaSuccess) return e;
   const long long most = std::min(sms, kKv4MaxSms);
   // Solo: blocks take whole units. Their longest share is then longer than the mean by what is compared here,
-  // and the joint work is spared, which takes as long as about kSoloSteps steps of a block for eight rows. Measured,
-  // solo and shared (us): 32 sequences x 8 heads of 500 tokens 11.8 and 17.6, 64 x 8 of 200 13.5 and 22.0, 13 x 8 of
-  // 1500 14.2 and 16.5, 20 rows on 16 x 8 of 5000 47 and 59; but 8 units of 1000 12.0 and 8.9, of 512 9.9 and 9.4.
+  // and the joint work is spared, which takes as long as kSoloSteps steps of a block for eight rows and half of that
+  // for each eight more. Measured, solo and shared (us): 32 sequences x 8 heads of 500 tokens 12.0 and 15.5, 64 x 8 of
+  // 200 13.7 and 15.6, 13 x 8 of 1500 14.2 and 17.3, 20 rows on 16 x 8 of 5000 47 and 50; but 8 units of 1000 11.8 and
+  // 9.0, two times 32 rows on 10 x 8 of 2000 62 and 52.
   const long long rounds = (load.units + most - 1) / most;
-  p.solo = rounds * load.longest - load.steps / most <= kSoloSteps * NR ? 1 : 0;
+  p.solo = rounds * load.longest - load.steps / most <= kSoloSteps * (NR + 1) / 2 ? 1 : 0;
   // Steps are spread over the SMs before they are over the warps of one (a block's warps share its issue slots),
   // and there are no more warps than steps.
   const long long per_block = p.solo ? rounds * load.longest : (load.steps + most - 1) / most;
@@ -924,8 +932,15 @@ cudaError_t launch_attend_t(Kv4AttendParams p, const Kv4Load& load, int sms, cud
   cudaLaunchConfig_t cfg = launch_config(dim3(blocks), warps * 32, warps * S::of_warp, stream, attr, pdl);
   e = cudaLaunchKernelEx(&cfg, kv4_attend_kernel<T, NR, M>, p);
   if (e != cudaSuccess || p.solo) return e;
-  cfg = launch_config(dim3(p.c.Hkv * std::max(1, load.max_rows), p.c.B), kMergeThreads, 0, stream, attr, pdl);
-  return cudaLaunchKernelEx(&cfg, kv4_merge_kernel<T>, p, static_cast<int>(S::RT), blocks);
+  // A unit's partials, about: a few are joined by a warp a row, many by a block a row (us, warp and block: 20 rows on
+  // 16 x 8 heads of about 5000 tokens 50.6 and 57.8; 8 heads of 131072 tokens, one row, 42.9 and 39.4).
+  const long long parts = load.longest * blocks / std::max(1ll, load.steps) + 2;
+  const long long rows = static_cast<long long>(p.c.Hkv) * load.max_rows;
+  const bool few = parts <= kTeamParts;
+  cfg = launch_config(dim3(static_cast<unsigned>(few ? (rows + kMergeWarps - 1) / kMergeWarps : rows), p.c.B),
+                      kMergeThreads, 0, stream, attr, pdl);
+  return few ? cudaLaunchKernelEx(&cfg, kv4_merge_kernel<T, 1>, p, static_cast<int>(S::RT), blocks)
+             : cudaLaunchKernelEx(&cfg, kv4_merge_kernel<T, kMergeWarps>, p, static_cast<int>(S::RT), blocks);
 }
 
 template <typename T>
