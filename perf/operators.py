@@ -356,7 +356,8 @@ def run(s):
             return P.hsa_kv4_read(kv, s["start"], s["start_host"], s["cu"], s["cu_host"], k_out=s["k_out"], v_out=s["v_out"], workspace_buf=s["work"])
         if op == "decode":
             return P.dense_decode_kv4(kv, s["q"], s["out"], scale=s["scale"], window=s["case"]["window"], lse=s["lse"], workspace_buf=s["work"]), s["lse"]
-        return P.dense_prefill_kv4(kv, s["q"], s["cu"], s["cu_host"], s["out"], scale=s["scale"], causal=s["case"]["causal"], window=s["case"]["window"],
+        causal = s["case"]["causal"]  # a window is one of a causal mask
+        return P.dense_prefill_kv4(kv, s["q"], s["cu"], s["cu_host"], s["out"], scale=s["scale"], causal=causal, window=s["case"]["window"] if causal else 0,
                                    lse=s["lse"], workspace_buf=s["work"]), s["lse"]
     if op == "write":
         put(s)
