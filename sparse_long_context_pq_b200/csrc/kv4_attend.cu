@@ -658,11 +658,18 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
               for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt) {
-                  mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
-                                ph[nt][1]);
-                  if (M == kHiLo)
-                    mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0],
-                                  pl[nt][1]);
+                  if (M == kHiLo) {
+                    // The tensor cores cut off what does not fit a sum, a bias that grows with the tiles of a segment:
+                    // a tile's products are summed by themselves, lo before hi, and added with rounding.
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16_16816(sum, x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0], pl[nt][1]);
+                    mma_f16_16816(sum, x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0], ph[nt][1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[nt][2 * w + kk][j] += sum[j];
+                  } else {
+                    mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
+                                  ph[nt][1]);
+                  }
                 }
               }
             }

@@ -447,6 +447,25 @@ def test_huge_logits_stay_finite(cuda_device, kind, factor, n):
     assert (np.abs(got - ref)[clear] <= (2 * half + 2.0 ** -11) * np.abs(ref)[clear] + 1e-30).all()
 
 
+@pytest.mark.parametrize("n", [1, 2, 4, 12])
+def test_sums_of_32_bit_calls_have_no_bias(cuda_device, n):
+    """Equal values come back as themselves on the mean. The tensor cores cut sums off: at most two cuts of less than
+    2^-23 to a tile of 16 tokens (one hi and one lo product), or to a sum over tiles where there is no lo product of its
+    own (n = 1: four rows); all else rounds to nearest. A bias that adds up over the tiles of a segment is far larger."""
+    B, T = 148, 600
+    cache = P.KV4Cache.empty(B * 5, 1, 128, cuda_device)
+    table = torch.arange(B * 5, dtype=torch.int32).view(B, 5)
+    kv = P.KV4Cache(cache, table.to(cuda_device), i32([T] * B).to(cuda_device), i32([T] * B), 4)
+    gen = torch.Generator(device=cuda_device).manual_seed(5)
+    cu = cu_of([T] * B)
+    k = torch.randn(B * T, 1, D, generator=gen, device=cuda_device)
+    P.hsa_kv4_write(kv, k, torch.full_like(k, 6.0), cu.to(cuda_device), cu)
+    cu = cu_of([n] * B)
+    q = torch.randn(B * n, 4, D, generator=gen, device=cuda_device)
+    out = P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, scale=0.1)
+    assert abs((out.double() / 6 - 1).mean().item()) <= 2 * 2.0 ** -23 + 2.0 ** -24
+
+
 @pytest.mark.parametrize("rows_of", ["few", "many"])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_many_sequences(cuda_device, kind, rows_of):
