@@ -660,7 +660,8 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
                 for (int nt = 0; nt < NR; ++nt) {
                   if (M == kHiLo) {
                     // The tensor cores cut off what does not fit a sum, a bias that grows with the tiles of a segment:
-                    // a tile's products are summed by themselves, lo before hi, and added with rounding.
+                    // a tile's products are summed by themselves, lo before hi, and added with rounding (500 tokens a
+                    // warp -8e-7 -> -4e-8 of the result; 20 rows on 16 x 8 heads of 5000 tokens 79 -> 87 us).
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
                     mma_f16_16816(sum, x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0], pl[nt][1]);
                     mma_f16_16816(sum, x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0], ph[nt][1]);
