@@ -598,6 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
             l2[0] = fmul2_rn(l2[0], pair(shrink, shrink));
             l2[1] = fmul2_rn(l2[1], pair(shrink, shrink));
             uint32_t y[16];
+            tmem_wait_st();   // weights and O of this step that are stored already are read back below
             if (j > first) {
 #pragma unroll 1
               for (int k = 0; k < 8; ++k) {

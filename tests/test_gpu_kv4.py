@@ -865,3 +865,29 @@ def test_a_sequence_from_prompt_to_decoded_tokens(cuda_device):
     sparse = P.hsa_decode(bf, ix, q, scale=scale, budget=1.0)    # every token selected: dense attention
     assert (sparse - out).abs().max() <= 5 * 4 * 2.0 ** -15 * 10
     assert case.error() == 0
+
+
+# ---- sums, ranges and limits -----------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("stairs", ["inside", "everywhere"])
+@pytest.mark.parametrize("n", [60, 200])
+def test_maximum_that_jumps_inside_a_step(cuda_device, n, stairs):
+    """The maximum of a third of the rows grows by more than the weights' head room (15 in log2 units) between the two
+    halves of a 128-token step, so that weights already stored are scaled: from the first half to the second only, or
+    from every half to the next. Other rows keep theirs or have it at the front."""
+    T = 640
+    case = Case([T], 1, 2, 16, seed=61)
+    kv = case.device()
+    gen = torch.Generator().manual_seed(62)
+    k = torch.randn(T, 1, D, generator=gen) * 0.05
+    half = torch.arange(T) // 64
+    k[:, 0, 0] = ((half + 1) // 2 if stairs == "inside" else half).float()
+    cu = cu_of([T])
+    P.hsa_kv4_write(kv, k.to(cuda_device), torch.randn(T, 1, D, generator=gen).to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    for kind in ("bf16", "f16"):
+        q = rows(case.rng, (n, 2, D), kind)
+        q[0::3, :, 0], q[1::3, :, 0], q[2::3, :, 0] = 48.0, 0.125, -48.0      # 24 natural units a stair, 34 in log2
+        out, lse = prefill(case, q, [n], 0.5)
+        check(out, lse, q, case, [n], 0.5, kind)
