@@ -360,8 +360,10 @@ hsa_status hsa_train_index(const hsa_kv_cache* kv, hsa_index* index, int32_t n_t
  * need one each, so do captured graphs whose replays may overlap.
  *
  * Limits (HSA_ERR_UNSUPPORTED beyond): 65535 sequences, 2^30 positions a block table row, 2^31
- * tiles in the cache, 2^25 query rows a KV head, and in attention of few rows 2^30 steps of 32
- * tokens over all sequences, KV heads and row tiles. Logits are held in fp32 (times log2(e), so
+ * tiles in the cache, 2^25 query rows a KV head, and of attention's work 2^30 steps of 32 tokens
+ * over all sequences, KV heads and tiles of 4 to 32 query rows (fp32 calls, and up to 64 query
+ * rows a KV head) or 2^31 steps of 128 tokens and 256 query rows. A replayed call whose device
+ * lengths pass that leaves its outputs unwritten and flags HSA_DEVERR_LIMIT. Logits are held in fp32 (times log2(e), so
  * below 2.3e38); q and out do not overlap.
  */
 #define HSA_KV4_TILE_TOKENS 16
@@ -451,6 +453,7 @@ hsa_status hsa_read_error(void* workspace, int32_t* error_host, cudaStream_t str
 #define HSA_DEVERR_TIMEOUT 4       /* a bounded wait gave up */
 #define HSA_DEVERR_SELECT 8        /* top-k bookkeeping inconsistent */
 #define HSA_DEVERR_SLOT 16         /* a training slot outside [0, n_train) */
+#define HSA_DEVERR_LIMIT 32        /* kv4 attention: device lengths past the limits of its work */
 
 /* ABI self-description: sizeof of the public structs, for bindings to check. */
 void hsa_abi_sizes(int64_t* kv_cache, int64_t* index, int64_t* decode_params, int64_t* debug);

@@ -24,11 +24,12 @@ __all__ = [
     "dense_decode_workspace_bytes", "hsa_index_workspace_bytes", "hsa_read_error", "hsa_strerror",
     "selected_counts", "DecodeStep", "HSA_DEVERR_PAGE", "HSA_DEVERR_CLUSTER", "HSA_DEVERR_TIMEOUT",
     "HSA_DEVERR_SELECT",
-    "KV4Cache", "KV4_TILE_BYTES", "hsa_kv4_workspace_bytes", "hsa_kv4_write", "hsa_kv4_read", "dense_decode_kv4",
+    "HSA_DEVERR_LIMIT", "KV4Cache", "KV4_TILE_BYTES", "hsa_kv4_workspace_bytes", "hsa_kv4_write", "hsa_kv4_read", "dense_decode_kv4",
     "dense_prefill_kv4",
 ]
 
 HSA_DEVERR_PAGE, HSA_DEVERR_CLUSTER, HSA_DEVERR_TIMEOUT, HSA_DEVERR_SELECT = 1, 2, 4, 8
+HSA_DEVERR_LIMIT = 32
 M_SUB, DSUB, NCODE, HEAD_DIM = 16, 8, 256, 128
 KV4_TILE_TOKENS, KV4_TILE_BYTES = 16, 2304
 

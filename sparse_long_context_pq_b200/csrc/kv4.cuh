@@ -16,6 +16,10 @@ constexpr int kTileBytes = HSA_KV4_TILE_BYTES;
 constexpr int kOffV = 1024;                        // value codes within a tile
 constexpr int kOffScale = 2048;                    // scale words within a tile
 constexpr int kKv4MaxSms = 160;                    // blocks that the workspace has slots for, by SMs
+// Places on the lines of steps are 32-bit. The host refuses longer lines; a kernel that finds one, by device lengths that
+// have grown since, does no work and flags it.
+constexpr long long kKv4MaxSteps = 1ll << 30;      // kv4_attend.cu
+constexpr long long kKv4MaxWideSteps = 1ll << 31;  // kv4_prefill.cu
 
 // What every kv4 kernel knows of the cache.
 struct Kv4View {
@@ -119,6 +123,7 @@ cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, con
                               cudaStream_t stream, bool pdl);
 
 // Many query rows a KV head, 16-bit types (kv4_prefill.cu); p.cu is not null.
+double kv4_prefill_steps(long long T, long long n, int G, bool causal, long long window, bool exact);   // of one head
 size_t kv4_prefill_part_bytes();
 cudaError_t launch_kv4_prefill(int dtype, const Kv4AttendParams& p, int sms, cudaStream_t stream, bool pdl);
 

@@ -124,8 +124,6 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   if (st != HSA_OK) return st;
   if (n_rows == 0) return HSA_OK;
   if (q == out) return HSA_ERR_INVALID_ARG;   // blocks read q while others write
-  const int sms = device_sms();
-  if (!sms) return HSA_ERR_CUDA;
   Kv4AttendParams p = {};
   p.c = view(kv, ws);
   p.q = static_cast<const uint8_t*>(q);
@@ -140,8 +138,19 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
   p.G = kv->Hq / kv->Hkv;
   p.inv_G = static_cast<uint32_t>(((1ull << 32) + p.G - 1) / p.G);   // not used for G = 1
   p.scale = scale;
-  if (cu && dtype != HSA_F32 && most * p.G > kFewRows)
+  if (cu && dtype != HSA_F32 && most * p.G > kFewRows) {
+    double steps = 0;
+    for (int exact = 0; exact < 2; ++exact) {   // counted out only where rows times tokens are too many
+      steps = 0;
+      for (int b = 0; b < kv->B; ++b)
+        steps += kv->Hkv * kv4_prefill_steps(kv->seq_lens_host[b], cu_host[b + 1] - cu_host[b], p.G, causal, p.window, exact);
+      if (steps < kKv4MaxWideSteps) break;
+    }
+    if (steps >= kKv4MaxWideSteps) return HSA_ERR_UNSUPPORTED;
+    const int sms = device_sms();
+    if (!sms) return HSA_ERR_CUDA;
     return launch_kv4_prefill(dtype, p, sms, stream, pdl_enabled()) == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
+  }
   const int rows = kv4_attend_rows(dtype, most * p.G);
   Kv4Load load = {0, 0, 0, most * p.G};
   const int step = kv4_attend_step_tokens();
@@ -150,11 +159,14 @@ hsa_status attend(const hsa_kv4_cache* kv, const void* q, int64_t q_stride, void
     if (n == 0 || T == 0) continue;
     const long long lo = window > 0 ? std::max(0ll, T - n - window + 1) / step : 0;
     const long long of_unit = (T + step - 1) / step - lo, units = (n * p.G + rows - 1) / rows * kv->Hkv;
+    if (units >= kKv4MaxSteps) return HSA_ERR_UNSUPPORTED;
     load.steps += of_unit * units;
+    if (load.steps >= kKv4MaxSteps) return HSA_ERR_UNSUPPORTED;
     load.units += units;
     load.longest = std::max(load.longest, of_unit);
   }
-  if (load.steps >= (1LL << 30)) return HSA_ERR_UNSUPPORTED;
+  const int sms = device_sms();
+  if (!sms) return HSA_ERR_CUDA;
   const cudaError_t err = launch_kv4_attend(dtype, rows, p, load, sms, stream, pdl_enabled());
   return err == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;
 }

@@ -130,7 +130,7 @@ __device__ __forceinline__ Seq sequence(const Kv4AttendParams& p, int b, int RT)
   const int hi = (s.T + kStepTok - 1) / kStepTok;
   s.nt = s.n > 0 ? hi - s.lo : 0;
   s.nrt = (s.n * p.G + RT - 1) / RT;
-  s.count = s.nt * s.nrt * p.c.Hkv;
+  s.count = static_cast<int>(static_cast<unsigned>(s.nt) * static_cast<unsigned>(s.nrt) * static_cast<unsigned>(p.c.Hkv));
   return s;
 }
 
@@ -143,8 +143,8 @@ __device__ __forceinline__ size_t head_row(const Kv4AttendParams& p, int r0, int
   return (static_cast<size_t>(r0) + i) * p.c.Hq + static_cast<size_t>(h) * p.G + (qrow - i * p.G);
 }
 
-// The line of all steps (fewer than 2^30, as the host checks) and its equal shares: the first
-// `rest` blocks take one step more.
+// The line of all steps (fewer than kKv4MaxSteps) and its equal shares: the first `rest`
+// blocks take one step more.
 struct Line {
   int W, N, each, rest;
   __device__ __forceinline__ Line(int w, int blocks) : W(w) {
@@ -170,19 +170,37 @@ __device__ __forceinline__ int lane_sums(int x) {
   return x;
 }
 
+// Whether the line is too long: its steps counted in 256s beside the exact count, at most 2^24 too few (of 65535
+// sequences), and no further than 2^28.
+struct Length {
+  unsigned of256 = 0;
+  // The next 32 sequences, one a lane.
+  __device__ __forceinline__ void add(const Kv4AttendParams& p, const Seq& s) {
+    const long long count = static_cast<long long>(s.nt) * s.nrt * p.c.Hkv;
+    of256 = min(of256 + __reduce_add_sync(0xffffffffu, static_cast<unsigned>(min(count >> 8, 1ll << 22))), 1u << 28);
+  }
+  __device__ __forceinline__ bool too_long() const { return of256 >= kKv4MaxSteps >> 8; }
+};
+
 // A place on the line, by a whole warp: a sequence with the steps and units before it.
 struct Spot {
   int b, steps, units;
 };
-// Totals of all sequences (b = B).
+// Totals of all sequences (b = B); none of a line that is too long.
 __device__ __forceinline__ Spot line_totals(const Kv4AttendParams& p, int RT) {
   Spot t = {p.c.B, 0, 0};
+  Length length;
 #pragma unroll 1
   for (int b = threadIdx.x & 31; b - (threadIdx.x & 31) < p.c.B; b += 32) {
     Seq s = {};
     if (b < p.c.B) s = sequence(p, b, RT);
+    length.add(p, s);
     t.steps += __reduce_add_sync(0xffffffffu, s.count);
     t.units += __reduce_add_sync(0xffffffffu, s.count ? s.nrt * p.c.Hkv : 0);
+  }
+  if (length.too_long()) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) record_error(p.c.err, HSA_DEVERR_LIMIT);
+    t.steps = t.units = 0;
   }
   return t;
 }
@@ -816,14 +834,18 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int rows_all = s.n * p.G;                       // query rows of a head
   const int team = warp / kTeam, member = warp % kTeam;
   int before = 0, W = 0;
+  Length length;
 #pragma unroll 1
   for (int i = lane; i - lane < p.c.B; i += 32) {
-    const int n = i < p.c.B ? sequence(p, i, RT).count : 0;
-    W += __reduce_add_sync(0xffffffffu, n);
-    before += __reduce_add_sync(0xffffffffu, i < b ? n : 0);
+    Seq e = {};
+    if (i < p.c.B) e = sequence(p, i, RT);
+    length.add(p, e);
+    W += __reduce_add_sync(0xffffffffu, e.count);
+    before += __reduce_add_sync(0xffffffffu, i < b ? e.count : 0);
   }
   const Line line(W, blocks);
   pdl_wait();
+  if (length.too_long()) return;
 #pragma unroll 1
   for (unsigned item = blockIdx.x * (kMergeWarps / kTeam) + team; s.nt > 0; item += gridDim.x * (kMergeWarps / kTeam)) {
     const int qrow = item / p.c.Hkv, h = item % p.c.Hkv;

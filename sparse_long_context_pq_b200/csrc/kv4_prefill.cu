@@ -276,8 +276,8 @@ __device__ __forceinline__ int2 unit_steps(const Kv4AttendParams& p, const Seq& 
   return make_int2(lo, max(lo, hi));
 }
 // Steps of one head of a sequence, by a whole warp.
-__device__ __forceinline__ int head_steps(const Kv4AttendParams& p, const Seq& s) {
-  int sum = 0;
+__device__ __forceinline__ long long head_steps(const Kv4AttendParams& p, const Seq& s) {
+  long long sum = 0;
 #pragma unroll 1
   for (int rt = threadIdx.x & 31; rt - static_cast<int>(threadIdx.x & 31) < s.nrt; rt += 32) {
     const int2 u = rt < s.nrt ? unit_steps(p, s, rt) : make_int2(0, 0);
@@ -307,9 +307,12 @@ struct Walk {
     __syncwarp();
   }
   __device__ __forceinline__ void find(const Kv4AttendParams& p) {
-    int W = 0;
+    long long all = 0;
 #pragma unroll 1
-    for (int i = 0; i < p.c.B; ++i) W += head_steps(p, sequence(p, i)) * p.c.Hkv;
+    for (int i = 0; i < p.c.B; ++i) all += head_steps(p, sequence(p, i)) * p.c.Hkv;
+    const bool past = all >= kKv4MaxWideSteps;   // by lengths that the host did not see
+    if (past && blockIdx.x == 0 && threadIdx.x == 0) record_error(p.c.err, HSA_DEVERR_LIMIT);
+    const int W = past ? 0 : static_cast<int>(all);
     const int N = min(static_cast<int>(gridDim.x), W), c = blockIdx.x;
     if (c >= N) {
       g = end = 0;
@@ -322,7 +325,7 @@ struct Walk {
 #pragma unroll 1
     for (;; ++b) {
       s = sequence(p, b);
-      const int of_head = head_steps(p, s);
+      const int of_head = static_cast<int>(head_steps(p, s));
       if (left < of_head * p.c.Hkv) {
         h = left / of_head;
         left -= h * of_head;
@@ -1078,6 +1081,19 @@ cudaError_t launch_prefill_t(const Kv4AttendParams& p, int sms, cudaStream_t str
 }
 
 }  // namespace
+
+// As unit_steps, on the host and over all row tiles; not exact: those of a mask that leaves everything.
+double kv4_prefill_steps(long long T, long long n, int G, bool causal, long long window, bool exact) {
+  const long long every = (T + kStepTok - 1) / kStepTok, tiles = (n * G + kRows - 1) / kRows;
+  if (!causal || !exact) return static_cast<double>(every) * static_cast<double>(tiles);
+  double sum = 0;
+  for (long long t = 0; t < tiles; ++t) {
+    const long long first = T - n + t * kRows / G, last = T - n + (std::min((t + 1) * kRows, n * G) - 1) / G;
+    const long long lo = window > 0 ? std::max(0ll, first - window + 1) / kStepTok : 0;
+    sum += static_cast<double>(std::max(0ll, (last < 0 ? 0 : last / kStepTok + 1) - lo));
+  }
+  return sum;
+}
 
 size_t kv4_prefill_part_bytes() {
   return static_cast<size_t>(2 * kKv4MaxSms) * (kSlot * sizeof(float) + sizeof(SlotInfo));

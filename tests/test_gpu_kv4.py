@@ -891,3 +891,20 @@ def test_maximum_that_jumps_inside_a_step(cuda_device, n, stairs):
         q[0::3, :, 0], q[1::3, :, 0], q[2::3, :, 0] = 48.0, 0.125, -48.0      # 24 natural units a stair, 34 in log2
         out, lse = prefill(case, q, [n], 0.5)
         check(out, lse, q, case, [n], 0.5, kind)
+
+
+@pytest.mark.parametrize("kind,n", [("f32", 16), ("bf16", 1056)])
+def test_device_lengths_past_the_limits_are_flagged(cuda_device, kind, n):
+    """A replay's lengths (here: the device's alone) that make more steps than a call may have: 2^31 of 32 tokens with
+    8 tiles of 16 rows, 33 x 2^26 of 128 tokens with 8448 rows. Nothing is written, no step is taken."""
+    Hkv, G, T = 8, 8, (1 << 30) - 128
+    cache = P.KV4Cache.empty(1, Hkv, 128, cuda_device)
+    table = torch.zeros(1, T // 128, dtype=torch.int32, device=cuda_device)
+    kv = P.KV4Cache(cache, table, i32([T]).to(cuda_device), i32([n]), Hkv * G)
+    ws = P.workspace(P.hsa_kv4_workspace_bytes(kv), cuda_device)
+    q = torch.zeros(n, Hkv * G, D, dtype=TYPES[kind], device=cuda_device)
+    out = torch.full_like(q, 7.0)
+    cu = cu_of([n])
+    P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, out, scale=0.1, causal=False, workspace_buf=ws)
+    assert P.hsa_read_error(ws) == P.HSA_DEVERR_LIMIT
+    assert (out == 7).all()

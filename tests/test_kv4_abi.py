@@ -157,6 +157,22 @@ def test_limits(lib):
     assert _prefill(lib, kv, _cu(1 << 18, 0), out=2 * FAKE) == 2       # 2^25 query rows a head
 
 
+@pytest.mark.parametrize("steps,kw", [
+    ((1 << 20, 0), dict(causal=0)),                                    # 2^15 row tiles x 2^13 steps x 8 heads
+    ((1 << 20, 1 << 20), {}),                                          # causal: half of that, twice
+    ((1 << 20, 0), dict(causal=0, dtype=0)),                           # the kernel of few rows
+])
+def test_attention_refuses_more_steps_than_it_counts(lib, steps, kw):
+    kv, host = _kv(Hq=64, Hkv=8, max_pages=1 << 16, seq=1 << 20)
+    assert _prefill(lib, kv, _cu(*steps), stride=64 * 128, out=2 * FAKE, **kw) == 2
+
+
+def test_a_window_keeps_long_chunks_within_the_limit(lib):
+    """2^20 tokens of 64 query heads under a window of 1000: their number times the tokens is too large, their steps are not."""
+    kv, host = _kv(Hq=64, Hkv=8, max_pages=1 << 16, seq=1 << 20)
+    assert _prefill(lib, kv, _cu(1 << 20, 0), stride=64 * 128, out=2 * FAKE, window=1000) == 6   # no device here
+
+
 def test_attention_refuses_to_write_over_its_queries(lib):
     kv, host = _kv()
     assert _decode(lib, kv) == 1
