@@ -27,9 +27,9 @@
 // largest is lost.
 //
 // What bounds it. Long batches: the cache's bytes (32 sequences x 8 heads of 32768 tokens with
-// bf16 q 205 us, 5.9 TB/s; with fp32 q 216 us). One long sequence: about 14 us beside the bytes
+// bf16 q 202 us, 6.0 TB/s; with fp32 q 221 us). One long sequence: about 14 us beside the bytes
 // for the chain lengths -> block table -> tiles, the join and the merge kernel (8 heads of 131072
-// tokens 39.0 us with fp32 q, 37.7 us with bf16 q; 1000 tokens 8.9 us). Many rows a tile: the
+// tokens 40.9 us with fp32 q, 37.7 us with bf16 q; 1000 tokens 9.4 us). Many rows a tile: the
 // tensor instructions of the older kind and the work of making fragments (20 rows on 16 x 8
 // heads of 5000 tokens each 47 us).
 #include <cuda_runtime.h>
@@ -65,6 +65,10 @@ struct Shape {
   static constexpr int max_warps = NR == 1 ? 16 : 8;
   static constexpr int stages = NR == 2 ? 2 : NR == 4 ? 4 : 3;
   static constexpr int U = 2;                                    // tiles worked on at once
+  // The tensor cores cut off what does not fit a sum, a bias that grows with the tiles of a segment (values of
+  // one sign: -9e-7 of the result after 64 tiles, -6e-6 after 256). In 32-bit calls the products of U tiles are summed by
+  // themselves and added with rounding (-4e-8 at any length; 32 x 8 heads of 32768 tokens 214 -> 221 us).
+  static constexpr int sum_tiles = M == kHi ? 1 : U;
   static constexpr size_t ring = static_cast<size_t>(stages) * kStepBytes;      // a warp's
   static constexpr size_t part = static_cast<size_t>(RT) * (kPitch + 2) * sizeof(float);
   static_assert(part <= ring, "a warp's last partial lies over its ring");
@@ -635,59 +639,68 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
           }
           // ---- O^T += V^T P ----
 #pragma unroll
-          for (int u = 0; u < S::U; ++u) {
-            uint32_t ph[NR][2], pl[NR][2];
+          for (int ub = 0; ub < S::U; ub += S::sum_tiles) {
+            uint32_t ph[S::sum_tiles][NR][2], pl[S::sum_tiles][NR][2];
+            uint4 v0[S::sum_tiles], v1[S::sum_tiles];
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt) {
-              float pr[4];
+            for (int u = 0; u < S::sum_tiles; ++u) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int c = 2 * nt + (j & 1);
-                pr[j] = fast_exp2(y[u][nt][j]);
-                l[c] += pr[j];
-              }
+              for (int nt = 0; nt < NR; ++nt) {
+                float pr[4];
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
-                if (M != kHi) {
-                  const float2 back = unpack_f16x2(hi2);
-                  const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
-                  if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
-                  else pl[nt][half] = transpose8x8(lo2);
+                for (int j = 0; j < 4; ++j) {
+                  const int c = 2 * nt + (j & 1);
+                  pr[j] = fast_exp2(y[ub + u][nt][j]);
+                  l[c] += pr[j];
                 }
-                ph[nt][half] = transpose8x8(hi2);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
+                  if (M != kHi) {
+                    const float2 back = unpack_f16x2(hi2);
+                    const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
+                    if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
+                    else pl[u][nt][half] = transpose8x8(lo2);
+                  }
+                  ph[u][nt][half] = transpose8x8(hi2);
+                }
               }
+              const uint8_t* tile = stage + (ub + u) * kTileBytes + kOffV;
+              v0[u] = reinterpret_cast<const uint4*>(tile)[lane];
+              v1[u] = reinterpret_cast<const uint4*>(tile + 512)[lane];
             }
-            const uint8_t* tile = stage + u * kTileBytes + kOffV;
-            const uint4 v0 = reinterpret_cast<const uint4*>(tile)[lane];
-            const uint4 v1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
-            const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              uint32_t x[4], y[4];
-              e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
-              e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
+              uint32_t x[S::sum_tiles][4], z[S::sum_tiles][4];
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[j] = hmul2(x[j], vs[u][0]);
-                y[j] = hmul2(y[j], vs[u][1]);
+              for (int u = 0; u < S::sum_tiles; ++u) {
+                const uint32_t w0[4] = {v0[u].x, v0[u].y, v0[u].z, v0[u].w}, w1[4] = {v1[u].x, v1[u].y, v1[u].z, v1[u].w};
+                e2m1_to_f16x2(w0[w], x[u][0], x[u][1], x[u][2], x[u][3]);
+                e2m1_to_f16x2(w1[w], z[u][0], z[u][1], z[u][2], z[u][3]);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  x[u][j] = hmul2(x[u][j], vs[ub + u][0]);
+                  z[u][j] = hmul2(z[u][j], vs[ub + u][1]);
+                }
               }
 #pragma unroll
               for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt) {
-                  if (M == kHiLo) {
-                    // The tensor cores cut off what does not fit a sum, a bias that grows with the tiles of a segment:
-                    // a tile's products are summed by themselves, lo before hi, and added with rounding (500 tokens a
-                    // warp -8e-7 -> -4e-8 of the result; 20 rows on 16 x 8 heads of 5000 tokens 79 -> 87 us).
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16_16816(sum, x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], pl[nt][0], pl[nt][1]);
-                    mma_f16_16816(sum, x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0], ph[nt][1]);
+                  float* to = o[nt][2 * w + kk];
+                  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                  float* d = M == kHi ? to : sum;
+                  if (M == kHiLo) {      // the small ones first
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) o[nt][2 * w + kk][j] += sum[j];
-                  } else {
-                    mma_f16_16816(o[nt][2 * w + kk], x[2 * kk], x[2 * kk + 1], y[2 * kk], y[2 * kk + 1], ph[nt][0],
-                                  ph[nt][1]);
+                    for (int u = 0; u < S::sum_tiles; ++u)
+                      mma_f16_16816(d, x[u][2 * kk], x[u][2 * kk + 1], z[u][2 * kk], z[u][2 * kk + 1], pl[u][nt][0], pl[u][nt][1]);
+                  }
+#pragma unroll
+                  for (int u = 0; u < S::sum_tiles; ++u)
+                    mma_f16_16816(d, x[u][2 * kk], x[u][2 * kk + 1], z[u][2 * kk], z[u][2 * kk + 1], ph[u][nt][0], ph[u][nt][1]);
+                  if (M != kHi) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) to[j] += sum[j];
                   }
                 }
               }

@@ -908,3 +908,24 @@ def test_device_lengths_past_the_limits_are_flagged(cuda_device, kind, n):
     P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, out, scale=0.1, causal=False, workspace_buf=ws)
     assert P.hsa_read_error(ws) == P.HSA_DEVERR_LIMIT
     assert (out == 7).all()
+
+
+@pytest.mark.parametrize("n", [1, 2, 4, 12])
+def test_sums_of_32_bit_calls_have_no_bias_over_long_segments(cuda_device, n):
+    """Equal values come back as themselves on the mean, however long the segments: 148 sequences of 32768 tokens, one a
+    block, are 128 tiles and more a warp (n = 1, 2: 16 warps; n = 4, 12: 8). A step's products are cut off at most once for
+    each of its at most four matrix instructions, less than 2^-23 of the step's own sum, half of that on the mean, and the
+    partial sums that they cut are half of that sum on the mean: 2^-23 together. The rest rounds to nearest."""
+    B, T = 148, 32768
+    pages = T // 128
+    cache = P.KV4Cache.empty(B * pages, 1, 128, cuda_device)
+    table = torch.arange(B * pages, dtype=torch.int32).view(B, pages)
+    kv = P.KV4Cache(cache, table.to(cuda_device), i32([T] * B).to(cuda_device), i32([T] * B), 4)
+    gen = torch.Generator(device=cuda_device).manual_seed(5)
+    cu = cu_of([T] * B)
+    k = torch.randn(B * T, 1, D, generator=gen, device=cuda_device, dtype=torch.bfloat16)
+    P.hsa_kv4_write(kv, k, torch.full_like(k, 6.0), cu.to(cuda_device), cu)
+    cu = cu_of([n] * B)
+    q = torch.randn(B * n, 4, D, generator=gen, device=cuda_device)
+    out = P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, scale=0.1)
+    assert abs((out.double() / 6 - 1).mean().item()) <= 2.0 ** -23 + 2.0 ** -24
