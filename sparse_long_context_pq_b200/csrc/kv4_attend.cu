@@ -27,11 +27,11 @@
 // largest is lost.
 //
 // What bounds it. Long batches: the cache's bytes (32 sequences x 8 heads of 32768 tokens with
-// bf16 q 202 us, 6.0 TB/s; with fp32 q 221 us). One long sequence: about 14 us beside the bytes
+// bf16 q 204 us, 5.9 TB/s; with fp32 q 221 us). One long sequence: about 14 us beside the bytes
 // for the chain lengths -> block table -> tiles, the join and the merge kernel (8 heads of 131072
 // tokens 40.9 us with fp32 q, 37.7 us with bf16 q; 1000 tokens 9.4 us). Many rows a tile: the
 // tensor instructions of the older kind and the work of making fragments (20 rows on 16 x 8
-// heads of 5000 tokens each 47 us).
+// heads of 5000 tokens each 48 us).
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -48,6 +48,7 @@ constexpr int kStepBytes = kStep * kTileBytes;
 constexpr float kHead = 11.f, kGrow = 4.f;
 constexpr float kWhole = 8388608.f;   // 2^23: larger logits are whole numbers, up to far more than kHead apart
 constexpr int kSoloSteps = 16;
+constexpr int kRun = 256;
 constexpr int kMergeThreads = 256;
 constexpr int kTeamParts = 4;
 constexpr int kMergeWarps = kMergeThreads / 32;
@@ -69,6 +70,10 @@ struct Shape {
   // one sign: -9e-7 of the result after 64 tiles, -6e-6 after 256). In 32-bit calls the products of U tiles are summed by
   // themselves and added with rounding (-4e-8 at any length; 32 x 8 heads of 32768 tokens 214 -> 221 us).
   static constexpr int sum_tiles = M == kHi ? 1 : U;
+  // 16-bit calls sum up to kRun steps in the tensor cores (-2e-5, a thirtieth of fp16's rounding) and then add to sums in
+  // the workspace, a lane's own beside their ref: 65536 tokens a warp came out 7e-4 too small, 131072 came out 1.6e-3.
+  // It costs 1 to 2% (32 x 8 heads of 32768 tokens 202 -> 204 us), rounded additions as above 4 to 8%.
+  static constexpr int run_floats = 32 * (32 * NR + 2 * NR);   // a warp's
   static constexpr size_t ring = static_cast<size_t>(stages) * kStepBytes;      // a warp's
   static constexpr size_t part = static_cast<size_t>(RT) * (kPitch + 2) * sizeof(float);
   static_assert(part <= ring, "a warp's last partial lies over its ring");
@@ -477,6 +482,35 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
       float o[NR][8][4];
       float ref[2 * NR], l[2 * NR];
       unsigned poison = 0;          // bit c: column c saw a value of this lane's dims that is not finite
+      // Sums so far, into the workspace (store) or, with what is there, into o.
+      auto run_sums = [&](bool store, bool add) {
+        float4* sums = reinterpret_cast<float4*>(p.parts + static_cast<size_t>(2 + warps) * gridDim.x * kSlot +
+                                                 static_cast<size_t>(blockIdx.x * warps + warp) * S::run_floats) + lane;
+        float* refs = reinterpret_cast<float*>(sums - lane + 8 * NR * 32) + lane;
+        float shrink[2 * NR];
+#pragma unroll
+        for (int c = 0; c < 2 * NR; ++c) {
+          shrink[c] = add ? fast_exp2(refs[32 * c] - ref[c]) : 0.f;
+          if (store) refs[32 * c] = ref[c];
+        }
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+          for (int i8 = 0; i8 < 8; ++i8) {
+            float* v = o[nt][i8];
+            if (add) {
+              const float4 w = sums[32 * (8 * nt + i8)];
+              v[0] = fmaf(w.x, shrink[2 * nt], v[0]);
+              v[1] = fmaf(w.y, shrink[2 * nt + 1], v[1]);
+              v[2] = fmaf(w.z, shrink[2 * nt], v[2]);
+              v[3] = fmaf(w.w, shrink[2 * nt + 1], v[3]);
+            }
+            if (store) {
+              sums[32 * (8 * nt + i8)] = make_float4(v[0], v[1], v[2], v[3]);
+              v[0] = v[1] = v[2] = v[3] = 0.f;
+            }
+          }
+      };
 #pragma unroll
       for (int j = 0; j < 2 * NR; ++j) {
         ref[j] = -1e30f;
@@ -490,217 +524,222 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
           for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
 
 #pragma unroll 1
-      for (int i = 0; i < len; ++i) {
-        cp_async_wait<S::stages - 2>();
-        __syncwarp();
-        const int st = i % S::stages;
-        const unsigned missing_now = (missing >> (2 * st)) & 3u;
-        issue(i + S::stages - 1);
+      for (int run = 0; run < len; run += M == kHi ? kRun : len) {
+        if (run > 0) run_sums(true, run > kRun);
+        const int run_end = M == kHi ? min(len, run + kRun) : len;
 #pragma unroll 1
-        for (int u0 = 0; u0 < kStep; u0 += S::U) {
-          const uint8_t* stage = ring + st * kStepBytes + u0 * kTileBytes;
-          const int pos = (tile0 + i * kStep + u0) * kTileTok;
-          const unsigned absent = (missing_now >> u0) & ((1u << S::U) - 1u);
-          // ---- S^T = K q^T ----
-          float sacc[S::U][NR][4];
-          uint2 sc[S::U];
+        for (int i = run; i < run_end; ++i) {
+          cp_async_wait<S::stages - 2>();
+          __syncwarp();
+          const int st = i % S::stages;
+          const unsigned missing_now = (missing >> (2 * st)) & 3u;
+          issue(i + S::stages - 1);
+#pragma unroll 1
+          for (int u0 = 0; u0 < kStep; u0 += S::U) {
+            const uint8_t* stage = ring + st * kStepBytes + u0 * kTileBytes;
+            const int pos = (tile0 + i * kStep + u0) * kTileTok;
+            const unsigned absent = (missing_now >> u0) & ((1u << S::U) - 1u);
+            // ---- S^T = K q^T ----
+            float sacc[S::U][NR][4];
+            uint2 sc[S::U];
 #pragma unroll
-          for (int u = 0; u < S::U; ++u) {
-            const uint8_t* tile = stage + u * kTileBytes;
-            const uint4 k0 = reinterpret_cast<const uint4*>(tile)[lane];
-            const uint4 k1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
-            sc[u] = reinterpret_cast<const uint2*>(tile + kOffScale)[lane];
-            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+            for (int u = 0; u < S::U; ++u) {
+              const uint8_t* tile = stage + u * kTileBytes;
+              const uint4 k0 = reinterpret_cast<const uint4*>(tile)[lane];
+              const uint4 k1 = reinterpret_cast<const uint4*>(tile + 512)[lane];
+              sc[u] = reinterpret_cast<const uint2*>(tile + kOffScale)[lane];
+              const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
+              for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-              for (int j = 0; j < 4; ++j) sacc[u][nt][j] = 0.f;
+                for (int j = 0; j < 4; ++j) sacc[u][nt][j] = 0.f;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t x[4], y[4];
-              e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
-              e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
-              const uint32_t s0 = scale_both(sc[u].x, w >> 1), s1 = scale_both(sc[u].x, 2 + (w >> 1));
+              for (int w = 0; w < 4; ++w) {
+                uint32_t x[4], y[4];
+                e2m1_to_f16x2(w0[w], x[0], x[1], x[2], x[3]);
+                e2m1_to_f16x2(w1[w], y[0], y[1], y[2], y[3]);
+                const uint32_t s0 = scale_both(sc[u].x, w >> 1), s1 = scale_both(sc[u].x, 2 + (w >> 1));
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                x[j] = hmul2(x[j], s0);
-                y[j] = hmul2(y[j], s1);
+                for (int j = 0; j < 4; ++j) {
+                  x[j] = hmul2(x[j], s0);
+                  y[j] = hmul2(y[j], s1);
+                }
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                  for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+                    for (int part_q = 0; part_q < (M == kHiLo ? 2 : 1); ++part_q) {
+                      const int fr = M == kHiLo ? 2 * nt + part_q : nt;
+                      const uint4 bq = S::q_smem ? *reinterpret_cast<const uint4*>(qs + (fr * 8 + r) * kQPitch + t * 64 + w * 16)
+                                                 : qf[S::q_smem ? 0 : fr][w];
+                      mma_f16_16816(sacc[u][nt], x[2 * kk], y[2 * kk], x[2 * kk + 1], y[2 * kk + 1], kk ? bq.z : bq.x,
+                                    kk ? bq.w : bq.y);
+                    }
+                  }
+                }
+              }
+              if (M == kPack) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) sacc[u][0][j] += __shfl_xor_sync(0xffffffffu, sacc[u][0][j], 2);
+              }
+            }
+            // ---- masks ----
+            uint32_t vs[S::U][2];
+#pragma unroll
+            for (int u = 0; u < S::U; ++u) {
+              vs[u][0] = scale_pair(sc[u].y, 0);
+              vs[u][1] = scale_pair(sc[u].y, 2);
+            }
+            const bool whole = absent == 0u && pos + S::U * kTileTok - 1 <= all_hi && pos >= all_lo;
+            if (!whole) {
+              int hi[2 * NR], lo[2 * NR];
+#pragma unroll
+              for (int c = 0; c < 2 * NR; ++c) {
+                hi[c] = last_seen(c);
+                lo[c] = first_seen(c);
               }
 #pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
+              for (int u = 0; u < S::U; ++u) {
+                const int pu = pos + u * kTileTok;
+                const bool present = !((absent >> u) & 1u);
 #pragma unroll
-                for (int nt = 0; nt < NR; ++nt) {
+                for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                  for (int part_q = 0; part_q < (M == kHiLo ? 2 : 1); ++part_q) {
-                    const int fr = M == kHiLo ? 2 * nt + part_q : nt;
-                    const uint4 bq = S::q_smem ? *reinterpret_cast<const uint4*>(qs + (fr * 8 + r) * kQPitch + t * 64 + w * 16)
-                                               : qf[S::q_smem ? 0 : fr][w];
-                    mma_f16_16816(sacc[u][nt], x[2 * kk], y[2 * kk], x[2 * kk + 1], y[2 * kk + 1], kk ? bq.z : bq.x,
-                                  kk ? bq.w : bq.y);
+                  for (int j = 0; j < 4; ++j) {
+                    const int tp = pu + r + 8 * (j >> 1), c = 2 * nt + (j & 1);
+                    // times f it is -inf, whatever f's sign
+                    if (tp > hi[c] || tp < lo[c] || !present) sacc[u][nt][j] = f[c] < 0.f ? INFINITY : -INFINITY;
+                  }
+                // A zero weight must not meet a NaN or an infinity: tokens past the end hold anything.
+                const int left = present ? s.T - (pu + 2 * t) : 0;   // tokens from this lane's first on
+                vs[u][0] &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
+                vs[u][1] &= (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
+                // Values that are not finite count for the rows that see their token, and for no other:
+                // taken out of the product, and the block's dims of those rows become NaN in the end.
+                const unsigned bad = ((vs[u][0] & 0x7c00u) == 0x7c00u ? 1u : 0u) |
+                                     ((vs[u][0] & 0x7c000000u) == 0x7c000000u ? 2u : 0u) |
+                                     ((vs[u][1] & 0x7c00u) == 0x7c00u ? 256u : 0u) |
+                                     ((vs[u][1] & 0x7c000000u) == 0x7c000000u ? 512u : 0u);
+                if (__any_sync(0xffffffffu, bad != 0u)) {
+                  vs[u][0] &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
+                  vs[u][1] &= (bad & 256u ? 0u : 0xffffu) | (bad & 512u ? 0u : 0xffff0000u);
+                  unsigned all = bad << (2 * t);                       // bit: token of the tile
+                  all |= __shfl_xor_sync(0xffffffffu, all, 1);
+                  all |= __shfl_xor_sync(0xffffffffu, all, 2);
+#pragma unroll
+                  for (int c = 0; c < 2 * NR; ++c) {
+                    const int from = max(0, lo[c] - pu), to = min(kTileTok - 1, hi[c] - pu);
+                    if (from <= to && (all & ((2u << to) - (1u << from))) != 0u) poison |= 1u << c;
                   }
                 }
               }
             }
-            if (M == kPack) {
+            // ---- online softmax: weights 2^(s f - ref) ----
+            float y[S::U][NR][4], top = -INFINITY;
 #pragma unroll
-              for (int j = 0; j < 4; ++j) sacc[u][0][j] += __shfl_xor_sync(0xffffffffu, sacc[u][0][j], 2);
-            }
-          }
-          // ---- masks ----
-          uint32_t vs[S::U][2];
-#pragma unroll
-          for (int u = 0; u < S::U; ++u) {
-            vs[u][0] = scale_pair(sc[u].y, 0);
-            vs[u][1] = scale_pair(sc[u].y, 2);
-          }
-          const bool whole = absent == 0u && pos + S::U * kTileTok - 1 <= all_hi && pos >= all_lo;
-          if (!whole) {
-            int hi[2 * NR], lo[2 * NR];
-#pragma unroll
-            for (int c = 0; c < 2 * NR; ++c) {
-              hi[c] = last_seen(c);
-              lo[c] = first_seen(c);
-            }
-#pragma unroll
-            for (int u = 0; u < S::U; ++u) {
-              const int pu = pos + u * kTileTok;
-              const bool present = !((absent >> u) & 1u);
+            for (int u = 0; u < S::U; ++u)
 #pragma unroll
               for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                  const int tp = pu + r + 8 * (j >> 1), c = 2 * nt + (j & 1);
-                  // times f it is -inf, whatever f's sign
-                  if (tp > hi[c] || tp < lo[c] || !present) sacc[u][nt][j] = f[c] < 0.f ? INFINITY : -INFINITY;
+                  // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
+                  sacc[u][nt][j] = __fmul_rn(sacc[u][nt][j], f[2 * nt + (j & 1)]);
+                  y[u][nt][j] = __fsub_rn(sacc[u][nt][j], ref[2 * nt + (j & 1)]);
+                  top = fmaxf(top, y[u][nt][j]);
                 }
-              // A zero weight must not meet a NaN or an infinity: tokens past the end hold anything.
-              const int left = present ? s.T - (pu + 2 * t) : 0;   // tokens from this lane's first on
-              vs[u][0] &= (left > 0 ? 0xffffu : 0u) | (left > 1 ? 0xffff0000u : 0u);
-              vs[u][1] &= (left > 8 ? 0xffffu : 0u) | (left > 9 ? 0xffff0000u : 0u);
-              // Values that are not finite count for the rows that see their token, and for no other:
-              // taken out of the product, and the block's dims of those rows become NaN in the end.
-              const unsigned bad = ((vs[u][0] & 0x7c00u) == 0x7c00u ? 1u : 0u) |
-                                   ((vs[u][0] & 0x7c000000u) == 0x7c000000u ? 2u : 0u) |
-                                   ((vs[u][1] & 0x7c00u) == 0x7c00u ? 256u : 0u) |
-                                   ((vs[u][1] & 0x7c000000u) == 0x7c000000u ? 512u : 0u);
-              if (__any_sync(0xffffffffu, bad != 0u)) {
-                vs[u][0] &= (bad & 1u ? 0u : 0xffffu) | (bad & 2u ? 0u : 0xffff0000u);
-                vs[u][1] &= (bad & 256u ? 0u : 0xffffu) | (bad & 512u ? 0u : 0xffff0000u);
-                unsigned all = bad << (2 * t);                       // bit: token of the tile
-                all |= __shfl_xor_sync(0xffffffffu, all, 1);
-                all |= __shfl_xor_sync(0xffffffffu, all, 2);
+            if (__any_sync(0xffffffffu, top > kHead + kGrow)) {
 #pragma unroll
-                for (int c = 0; c < 2 * NR; ++c) {
-                  const int from = max(0, lo[c] - pu), to = min(kTileTok - 1, hi[c] - pu);
-                  if (from <= to && (all & ((2u << to) - (1u << from))) != 0u) poison |= 1u << c;
+              for (int c = 0; c < 2 * NR; ++c) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < S::U; ++u)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j) mx = fmaxf(mx, sacc[u][c >> 1][(c & 1) + 2 * j]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                const float next = fmaxf(ref[c], fabsf(mx) < kWhole ? mx - kHead : mx);   // mx - 11 may round to mx - 16
+                const float shrink = fast_exp2(ref[c] - next);
+                ref[c] = next;
+                l[c] *= shrink;
+#pragma unroll
+                for (int i8 = 0; i8 < 8; ++i8) {
+                  o[c >> 1][i8][c & 1] *= shrink;
+                  o[c >> 1][i8][(c & 1) + 2] *= shrink;
                 }
+#pragma unroll
+                for (int u = 0; u < S::U; ++u)
+#pragma unroll
+                  for (int j = 0; j < 2; ++j)
+                    y[u][c >> 1][(c & 1) + 2 * j] = __fsub_rn(sacc[u][c >> 1][(c & 1) + 2 * j], next);
               }
             }
-          }
-          // ---- online softmax: weights 2^(s f - ref) ----
-          float y[S::U][NR][4], top = -INFINITY;
+            // ---- O^T += V^T P ----
 #pragma unroll
-          for (int u = 0; u < S::U; ++u)
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                // rounded before ref is taken off: ref is made of rounded logits, and large ones must meet it
-                sacc[u][nt][j] = __fmul_rn(sacc[u][nt][j], f[2 * nt + (j & 1)]);
-                y[u][nt][j] = __fsub_rn(sacc[u][nt][j], ref[2 * nt + (j & 1)]);
-                top = fmaxf(top, y[u][nt][j]);
-              }
-          if (__any_sync(0xffffffffu, top > kHead + kGrow)) {
-#pragma unroll
-            for (int c = 0; c < 2 * NR; ++c) {
-              float mx = -INFINITY;
-#pragma unroll
-              for (int u = 0; u < S::U; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j) mx = fmaxf(mx, sacc[u][c >> 1][(c & 1) + 2 * j]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float next = fmaxf(ref[c], fabsf(mx) < kWhole ? mx - kHead : mx);   // mx - 11 may round to mx - 16
-              const float shrink = fast_exp2(ref[c] - next);
-              ref[c] = next;
-              l[c] *= shrink;
-#pragma unroll
-              for (int i8 = 0; i8 < 8; ++i8) {
-                o[c >> 1][i8][c & 1] *= shrink;
-                o[c >> 1][i8][(c & 1) + 2] *= shrink;
-              }
-#pragma unroll
-              for (int u = 0; u < S::U; ++u)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                  y[u][c >> 1][(c & 1) + 2 * j] = __fsub_rn(sacc[u][c >> 1][(c & 1) + 2 * j], next);
-            }
-          }
-          // ---- O^T += V^T P ----
-#pragma unroll
-          for (int ub = 0; ub < S::U; ub += S::sum_tiles) {
-            uint32_t ph[S::sum_tiles][NR][2], pl[S::sum_tiles][NR][2];
-            uint4 v0[S::sum_tiles], v1[S::sum_tiles];
-#pragma unroll
-            for (int u = 0; u < S::sum_tiles; ++u) {
-#pragma unroll
-              for (int nt = 0; nt < NR; ++nt) {
-                float pr[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const int c = 2 * nt + (j & 1);
-                  pr[j] = fast_exp2(y[ub + u][nt][j]);
-                  l[c] += pr[j];
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
-                  if (M != kHi) {
-                    const float2 back = unpack_f16x2(hi2);
-                    const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
-                    if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
-                    else pl[u][nt][half] = transpose8x8(lo2);
-                  }
-                  ph[u][nt][half] = transpose8x8(hi2);
-                }
-              }
-              const uint8_t* tile = stage + (ub + u) * kTileBytes + kOffV;
-              v0[u] = reinterpret_cast<const uint4*>(tile)[lane];
-              v1[u] = reinterpret_cast<const uint4*>(tile + 512)[lane];
-            }
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              uint32_t x[S::sum_tiles][4], z[S::sum_tiles][4];
+            for (int ub = 0; ub < S::U; ub += S::sum_tiles) {
+              uint32_t ph[S::sum_tiles][NR][2], pl[S::sum_tiles][NR][2];
+              uint4 v0[S::sum_tiles], v1[S::sum_tiles];
 #pragma unroll
               for (int u = 0; u < S::sum_tiles; ++u) {
-                const uint32_t w0[4] = {v0[u].x, v0[u].y, v0[u].z, v0[u].w}, w1[4] = {v1[u].x, v1[u].y, v1[u].z, v1[u].w};
-                e2m1_to_f16x2(w0[w], x[u][0], x[u][1], x[u][2], x[u][3]);
-                e2m1_to_f16x2(w1[w], z[u][0], z[u][1], z[u][2], z[u][3]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  x[u][j] = hmul2(x[u][j], vs[ub + u][0]);
-                  z[u][j] = hmul2(z[u][j], vs[ub + u][1]);
-                }
-              }
-#pragma unroll
-              for (int kk = 0; kk < 2; ++kk) {
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt) {
-                  float* to = o[nt][2 * w + kk];
-                  float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                  float* d = M == kHi ? to : sum;
-                  if (M == kHiLo) {      // the small ones first
+                  float pr[4];
 #pragma unroll
-                    for (int u = 0; u < S::sum_tiles; ++u)
-                      mma_f16_16816(d, x[u][2 * kk], x[u][2 * kk + 1], z[u][2 * kk], z[u][2 * kk + 1], pl[u][nt][0], pl[u][nt][1]);
+                  for (int j = 0; j < 4; ++j) {
+                    const int c = 2 * nt + (j & 1);
+                    pr[j] = fast_exp2(y[ub + u][nt][j]);
+                    l[c] += pr[j];
                   }
 #pragma unroll
-                  for (int u = 0; u < S::sum_tiles; ++u)
-                    mma_f16_16816(d, x[u][2 * kk], x[u][2 * kk + 1], z[u][2 * kk], z[u][2 * kk + 1], ph[u][nt][0], ph[u][nt][1]);
-                  if (M != kHi) {
+                  for (int half = 0; half < 2; ++half) {
+                    uint32_t hi2 = pack_f16x2(pr[2 * half], pr[2 * half + 1]);
+                    if (M != kHi) {
+                      const float2 back = unpack_f16x2(hi2);
+                      const uint32_t lo2 = pack_f16x2(pr[2 * half] - back.x, pr[2 * half + 1] - back.y);
+                      if (M == kPack) hi2 = t >= 2 ? lo2 : hi2;
+                      else pl[u][nt][half] = transpose8x8(lo2);
+                    }
+                    ph[u][nt][half] = transpose8x8(hi2);
+                  }
+                }
+                const uint8_t* tile = stage + (ub + u) * kTileBytes + kOffV;
+                v0[u] = reinterpret_cast<const uint4*>(tile)[lane];
+                v1[u] = reinterpret_cast<const uint4*>(tile + 512)[lane];
+              }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) to[j] += sum[j];
+              for (int w = 0; w < 4; ++w) {
+                uint32_t x[S::sum_tiles][4], z[S::sum_tiles][4];
+#pragma unroll
+                for (int u = 0; u < S::sum_tiles; ++u) {
+                  const uint32_t w0[4] = {v0[u].x, v0[u].y, v0[u].z, v0[u].w}, w1[4] = {v1[u].x, v1[u].y, v1[u].z, v1[u].w};
+                  e2m1_to_f16x2(w0[w], x[u][0], x[u][1], x[u][2], x[u][3]);
+                  e2m1_to_f16x2(w1[w], z[u][0], z[u][1], z[u][2], z[u][3]);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    x[u][j] = hmul2(x[u][j], vs[ub + u][0]);
+                    z[u][j] = hmul2(z[u][j], vs[ub + u][1]);
+                  }
+                }
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+#pragma unroll
+                  for (int nt = 0; nt < NR; ++nt) {
+                    float* to = o[nt][2 * w + kk];
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    float* d = M == kHi ? to : sum;
+                    if (M == kHiLo) {      // the small ones first
+#pragma unroll
+                      for (int u = 0; u < S::sum_tiles; ++u)
+                        mma_f16_16816(d, x[u][2 * kk], x[u][2 * kk + 1], z[u][2 * kk], z[u][2 * kk + 1], pl[u][nt][0], pl[u][nt][1]);
+                    }
+#pragma unroll
+                    for (int u = 0; u < S::sum_tiles; ++u)
+                      mma_f16_16816(d, x[u][2 * kk], x[u][2 * kk + 1], z[u][2 * kk], z[u][2 * kk + 1], ph[u][nt][0], ph[u][nt][1]);
+                    if (M != kHi) {
+#pragma unroll
+                      for (int j = 0; j < 4; ++j) to[j] += sum[j];
+                    }
                   }
                 }
               }
@@ -709,6 +748,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
         }
       }
       cp_async_wait<0>();
+      if (M == kHi && len > kRun) run_sums(false, true);
 
       // ---- end of a segment: through shared memory, into the result or a partial to be joined ----
       __syncwarp();   // the ring has been read
@@ -1007,9 +1047,9 @@ int kv4_attend_rows(int dtype, int max_rows) {
   return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 24 ? 24 : 32;
 }
 
-// Two slots a block and one a warp: 18 of 8 rows or 10 of 16, 24 or 32.
+// Two slots a block and one a warp, and a warp's sums of earlier runs: 18 of 8 rows or 10 of 16, 24 or 32, and 16 or 8.
 size_t kv4_attend_part_bytes() {
-  return static_cast<size_t>(2 + 8) * kKv4MaxSms * 32 * (kD + 2) * sizeof(float);
+  return static_cast<size_t>(kKv4MaxSms) * (10 * 32 * (kD + 2) + 8 * Shape<4, kHi>::run_floats) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attend(int dtype, int rows, const Kv4AttendParams& p, const Kv4Load& load, int sms,

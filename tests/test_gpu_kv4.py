@@ -929,3 +929,37 @@ def test_sums_of_32_bit_calls_have_no_bias_over_long_segments(cuda_device, n):
     q = torch.randn(B * n, 4, D, generator=gen, device=cuda_device)
     out = P.dense_prefill_kv4(kv, q, cu.to(cuda_device), cu, scale=0.1)
     assert abs((out.double() / 6 - 1).mean().item()) <= 2.0 ** -23 + 2.0 ** -24
+
+
+def long_bias(n, kind, device, Hkv=2, G=4, T=1 << 20, B=148):
+    """Mean relative error of values of one sign over a million tokens, B sequences of the same pages so that a unit's
+    tokens are shared by few warps or blocks; the last rows of one sequence against 64 bits."""
+    gen = torch.Generator(device=device).manual_seed(9)
+    cache = P.KV4Cache.empty(T // 128, Hkv, 128, device)
+    table = torch.arange(T // 128, dtype=torch.int32, device=device).view(1, -1)
+    one = P.KV4Cache(cache, table, i32([T]).to(device), i32([T]), Hkv * G)
+    k = torch.randn(T, Hkv, D, generator=gen, device=device, dtype=torch.bfloat16)
+    v = torch.rand(T, Hkv, D, generator=gen, device=device, dtype=torch.bfloat16) + 0.5
+    cu, st = cu_of([T]), i32([0])
+    P.hsa_kv4_write(one, k, v, cu.to(device), cu)
+    k, v = P.hsa_kv4_read(one, st.to(device), st, cu.to(device), cu)
+    kv = P.KV4Cache(cache, table.expand(B, -1).contiguous(), i32([T] * B).to(device), i32([T] * B), Hkv * G)
+    q = torch.randn(n, Hkv * G, D, generator=gen, device=device).to(TYPES[kind])
+    cu = cu_of([n] * B)
+    out = P.dense_prefill_kv4(kv, q.repeat(B, 1, 1), cu.to(device), cu, scale=0.1).view(B, n, Hkv, G, D)
+    m = min(n, 4)
+    errors = []
+    for h in range(Hkv):
+        x = 0.1 * (q.view(n, Hkv, G, D)[n - m:, h].reshape(-1, D).double() @ k[:, h].double().T)
+        seen = torch.arange(T, device=device)[None] <= torch.arange(T - m, T, device=device).repeat_interleave(G)[:, None]
+        ref = torch.softmax(x.masked_fill_(~seen, -math.inf), -1) @ v[:, h].double()
+        errors.append((out[B // 2, n - m:, h].reshape(-1, D).double() / ref - 1).mean().item())
+    return float(np.mean(errors))
+
+
+@pytest.mark.parametrize("n", [2, 4, 8])
+def test_sums_of_16_bit_calls_over_long_segments(cuda_device, n):
+    """65536 to 131072 tokens a warp. Sums of at most 512 tiles are cut off by less than 2^-23 each; the results of 256
+    dims round apart from one another by at most 2^-11 of a value, evenly spread (of all rows alike, as rows see nearly
+    the same mean): four standard deviations of their mean."""
+    assert abs(long_bias(n, "f16", cuda_device)) <= 512 * 2.0 ** -23 + 4 * 2.0 ** -11 / math.sqrt(3 * 256)
