@@ -22,7 +22,7 @@
 //
 // What bounds it: the tensor cores need 2048 clocks for a step (4 x 128 x 128 x 128 products),
 // ex2 as many (256 x 128 at 16 a clock), shared memory about 2000 (operands and dequantised tiles).
-// Measured, a step takes about 5400 (2048 tokens over 32768, 32 heads on 8: 1.38 ms, 770 TFLOP/s): a
+// Measured, a step takes about 5400 (2048 tokens over 32768, 32 heads on 8: 1.40 ms, 762 TFLOP/s): a
 // half's chain is S full, maximum, weights, P, P V, the next S, with its softmax (about 2400 for 128 rows
 // x 128 tokens) beside the other half's on the same schedulers, and TMEM has no room for a second S.
 // Between two segments there are about 12000 clocks of output and q (4 sequences of 2048: 0.34 ms).
@@ -49,6 +49,7 @@ constexpr int kStepTiles = kStepTok / kTileTok;
 constexpr int kThreads = 14 * 32;
 constexpr float kHead = 11.f, kGrow = 4.f;
 constexpr float kWhole = 8388608.f;             // 2^23: larger logits are whole numbers, up to far more than kHead apart
+constexpr int kRun = 128;                       // steps of a half that the tensor cores sum without rounding
 constexpr int kPiece = 64;                      // tokens of a step that a softmax thread holds at a time
 constexpr uint32_t kOperand = 128 * kD * 2;     // 32 KB: 128 rows of 128 fp16
 constexpr uint32_t kHalfOp = kOperand / 2;      // one 64-element half (128 bytes a row)
@@ -187,6 +188,41 @@ __device__ __noinline__ void scale_tmem(uint32_t at, int n, float f) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__fmul_rn(__uint_as_float(y[i]), f));
     tmem_st16(at + c, y);
+  }
+  tmem_wait_st();
+}
+// The tensor cores cut off what does not fit a sum, a bias that grows with its tokens (a million of them came out 6e-3
+// too small). So O holds kRun steps at most (16384 tokens, -5e-5): then each thread adds its row, with rounding, to its
+// sums in a slot of the workspace, which holds their ref too, and in the end those to O (2048 tokens over 32768
+// 1367 -> 1398 us).
+enum Fold { kFoldFirst, kFoldMore, kFoldBack };
+__device__ __noinline__ void fold(uint32_t o, float* slot, float ref, Fold how) {
+  const float w = how == kFoldFirst ? 0.f : fast_exp2(slot[threadIdx.x] - ref);
+  if (how != kFoldBack) slot[threadIdx.x] = ref;
+  float4* sums = reinterpret_cast<float4*>(slot + 2 * kRows) + threadIdx.x;
+#pragma unroll 1
+  for (int c = 0; c < kD; c += 32) {
+    float4 s[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = how == kFoldFirst ? make_float4(0.f, 0.f, 0.f, 0.f) : sums[(c / 4 + i) * kRows];
+    uint32_t y[32];
+    tmem_ld32(o + c, y);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float4 v = make_float4(
+          fmaf(s[i].x, w, __uint_as_float(y[4 * i])), fmaf(s[i].y, w, __uint_as_float(y[4 * i + 1])),
+          fmaf(s[i].z, w, __uint_as_float(y[4 * i + 2])), fmaf(s[i].w, w, __uint_as_float(y[4 * i + 3])));
+      if (how != kFoldBack) sums[(c / 4 + i) * kRows] = v;
+      y[4 * i] = __float_as_uint(v.x);
+      y[4 * i + 1] = __float_as_uint(v.y);
+      y[4 * i + 2] = __float_as_uint(v.z);
+      y[4 * i + 3] = __float_as_uint(v.w);
+    }
+    if (how == kFoldBack) {
+      tmem_st16(o + c, y);
+      tmem_st16(o + c + 16, y + 16);
+    }
   }
   tmem_wait_st();
 }
@@ -415,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
   uint64_t* v_full = bars + 4;        // [2] four warps
   uint64_t* v_empty = bars + 6;       // [2] as k_empty
   uint64_t* s_full = bars + 8;        // [2 halves] commit
-  uint64_t* o_full = bars + 10;       // [2 halves] commit, once a segment
+  uint64_t* o_full = bars + 10;       // [2 halves] commit, once a run
   uint64_t* drained = bars + 12;      // [2 halves] commit, at the end
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -470,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
     const uint32_t ts = tmem + lanes + half * 128, to = tmem + lanes + 256 + half * 128;
     bool more = walk.next(p, segments_s[warp]);
     int done = 0;         // this half's steps so far: phase of its barriers
+    int runs = 0;         // and runs: phase of o_full
     int it = 0;           // the block's steps so far: place of their flags
     bool ok = true;       // a wait gave up: from there on only the barriers, which all eight warps pass
 #pragma unroll 1
@@ -525,123 +562,138 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       unsigned long long l2[2] = {0, 0};
       unsigned poison = 0;          // bits 0-7: dim groups with a value that is not finite, bit 8: the whole row
       const int first = split ? half : 0, by = split ? 2 : 1;
+      // slot of the sums of earlier runs: that of the partial; of a whole unit the second, which the last segment gets
+      auto sums = [&]() { return p.parts + static_cast<size_t>(cur.open == 3 ? 2 * blockIdx.x + 1 : cur.slot) * kSlot; };
 #pragma unroll 1
-      for (int j = first; j < steps; j += by, ++done) {
-        // After a wait that gave up there is no more work, but the barriers that others share are still passed.
-        if (ok) ok = wait_long_warp(s_full + half, done & 1, p.c.err);
-        if (!ok) {
-          half_barrier(half);
-          continue;
+      for (int run = first; run < steps; run += kRun * by) {
+        if (run > first) {
+          ok = ok && wait_long_warp(o_full + half, runs++ & 1, p.c.err);
+          tc_fence_after();
+          if (ok) fold(to, sums(), ref, run == first + kRun * by ? kFoldFirst : kFoldMore);
+          tc_fence_before();
         }
-        tc_fence_after();
-        const int k0 = (first_step + j) * kStepTok;
-        const uint4 fl = *reinterpret_cast<const uint4*>(flags_s + ((it + j) & 3) * 4);
-        const unsigned flags = fl.x | fl.y | fl.z | fl.w;     // bits 0-7: tiles without a page, bit 8: poison
-        const int from = max(0, lo - k0), upto = min(kStepTok - 1, hi - k0);   // tokens of the step that the row sees
-        const bool masked = __any_sync(0xffffffffu, from > 0 || upto < kStepTok - 1 || (flags & 0xffu));
-        auto seen32 = [&](int c0) -> uint32_t {   // those among [c0, c0 + 32)
-          const int a = max(from - c0, 0), z = min(upto - c0, 31);
-          uint32_t m = a <= z ? (0xffffffffu >> (31 - z)) & (0xffffffffu << a) : 0u;
-          const unsigned gone = (flags >> (c0 / kTileTok)) & 3u;
-          if (gone & 1u) m &= 0xffff0000u;
-          if (gone & 2u) m &= 0x0000ffffu;
-          return m;
-        };
-        if (flags & 0x100u) {   // values that are not finite, in blocks of 16 dims
-          const uint32_t* words = poison_s + ((it + j) & 3) * 32;
+        const int run_end = min(steps, run + kRun * by);
 #pragma unroll 1
-          for (int gr = 0; gr < 8; ++gr) {
-            uint32_t seen = 0;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) seen |= words[gr * 4 + q] & seen32(q * 32);
-            if (seen) poison |= 1u << gr;
+        for (int j = run; j < run_end; j += by, ++done) {
+          // After a wait that gave up there is no more work, but the barriers that others share are still passed.
+          if (ok) ok = wait_long_warp(s_full + half, done & 1, p.c.err);
+          if (!ok) {
+            half_barrier(half);
+            continue;
           }
-        }
-        if (scaled) scale_tmem(ts, kStepTok, factor[row]);
-        // in pieces of kPiece tokens: more at a time spill, and local memory is slow beside 200 KB of shared memory
+          tc_fence_after();
+          const int k0 = (first_step + j) * kStepTok;
+          const uint4 fl = *reinterpret_cast<const uint4*>(flags_s + ((it + j) & 3) * 4);
+          const unsigned flags = fl.x | fl.y | fl.z | fl.w;     // bits 0-7: tiles without a page, bit 8: poison
+          const int from = max(0, lo - k0), upto = min(kStepTok - 1, hi - k0);   // tokens of the step that the row sees
+          const bool masked = __any_sync(0xffffffffu, from > 0 || upto < kStepTok - 1 || (flags & 0xffu));
+          auto seen32 = [&](int c0) -> uint32_t {   // those among [c0, c0 + 32)
+            const int a = max(from - c0, 0), z = min(upto - c0, 31);
+            uint32_t m = a <= z ? (0xffffffffu >> (31 - z)) & (0xffffffffu << a) : 0u;
+            const unsigned gone = (flags >> (c0 / kTileTok)) & 3u;
+            if (gone & 1u) m &= 0xffff0000u;
+            if (gone & 2u) m &= 0x0000ffffu;
+            return m;
+          };
+          if (flags & 0x100u) {   // values that are not finite, in blocks of 16 dims
+            const uint32_t* words = poison_s + ((it + j) & 3) * 32;
 #pragma unroll 1
-        for (int q = 0; q < kStepTok / kPiece; ++q) {
-          uint32_t x[kPiece];
-#pragma unroll
-          for (int k = 0; k < kPiece; k += 32) tmem_ld32(ts + q * kPiece + k, x + k);
-          tmem_wait_ld();
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < kPiece; k += 32) {
-              const uint32_t m = seen32(q * kPiece + k);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[k + i] = (m >> i) & 1u ? x[k + i] : 0xff800000u;
+            for (int gr = 0; gr < 8; ++gr) {
+              uint32_t seen = 0;
+#pragma unroll 1
+              for (int q = 0; q < 4; ++q) seen |= words[gr * 4 + q] & seen32(q * 32);
+              if (seen) poison |= 1u << gr;
             }
           }
-          float tops[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tops[k] = max3_nan(__uint_as_float(x[k]), __uint_as_float(x[k + 4]), __uint_as_float(x[k + 8]));
-#pragma unroll
-          for (int i = 12; i + 8 <= kPiece; i += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k) tops[k] = max3_nan(tops[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + 4 + k]));
-#pragma unroll
-          for (int k = 0; k < 4; ++k) tops[k] = max3_nan(tops[k], __uint_as_float(x[kPiece - 4 + k]), tops[k]);
-          const float top = __fmul_rn(max3_nan(max3_nan(tops[0], tops[1], tops[2]), tops[3], tops[3]), f);
-          if (__any_sync(0xffffffffu, !(__fsub_rn(top, ref) <= kHead + kGrow))) {
-            // a logit of 2^23 or more: S of this piece and the rest times f, and the piece once more
-            if (!scaled && __any_sync(0xffffffffu, fabsf(top) >= kWhole && top != -INFINITY)) {
-              scaled = true;
-              scale_tmem(ts + q * kPiece, kStepTok - q * kPiece, f);
-              f = 1.f;
-              --q;
-              continue;
-            }
-            if (isnan(top)) poison |= 0x100u;
-            const bool grow = __fsub_rn(top, ref) > kHead + kGrow;
-            const float next = !grow ? ref : fabsf(top) < kWhole ? ceilf(top) - kHead : top;
-            const float down = fmaxf(ref - next, -127.f);              // a whole number
-            const float shrink = __int_as_float((static_cast<int>(down) + 127) << 23);   // 0 for 2^-127 and less
-            ref = next;
-            l2[0] = fmul2_rn(l2[0], pair(shrink, shrink));
-            l2[1] = fmul2_rn(l2[1], pair(shrink, shrink));
-            uint32_t y[16];
-            tmem_wait_st();   // weights and O of this step that are stored already are read back below
-            if (j > first) {
+          if (scaled) scale_tmem(ts, kStepTok, factor[row]);
+          // in pieces of kPiece tokens: more at a time spill, and local memory is slow beside 200 KB of shared memory
 #pragma unroll 1
-              for (int k = 0; k < 8; ++k) {
-                tmem_ld16(to + k * 16, y);
-                tmem_wait_ld();
+          for (int q = 0; q < kStepTok / kPiece; ++q) {
+            uint32_t x[kPiece];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * shrink);
-                tmem_st16(to + k * 16, y);
+            for (int k = 0; k < kPiece; k += 32) tmem_ld32(ts + q * kPiece + k, x + k);
+            tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int k = 0; k < kPiece; k += 32) {
+                const uint32_t m = seen32(q * kPiece + k);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[k + i] = (m >> i) & 1u ? x[k + i] : 0xff800000u;
               }
             }
-            const uint32_t s2 = pack_f16x2(shrink, shrink);
+            float tops[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              tops[k] = max3_nan(__uint_as_float(x[k]), __uint_as_float(x[k + 4]), __uint_as_float(x[k + 8]));
+#pragma unroll
+            for (int i = 12; i + 8 <= kPiece; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                tops[k] = max3_nan(tops[k], __uint_as_float(x[i + k]), __uint_as_float(x[i + 4 + k]));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) tops[k] = max3_nan(tops[k], __uint_as_float(x[kPiece - 4 + k]), tops[k]);
+            const float top = __fmul_rn(max3_nan(max3_nan(tops[0], tops[1], tops[2]), tops[3], tops[3]), f);
+            if (__any_sync(0xffffffffu, !(__fsub_rn(top, ref) <= kHead + kGrow))) {
+              // a logit of 2^23 or more: S of this piece and the rest times f, and the piece once more
+              if (!scaled && __any_sync(0xffffffffu, fabsf(top) >= kWhole && top != -INFINITY)) {
+                scaled = true;
+                scale_tmem(ts + q * kPiece, kStepTok - q * kPiece, f);
+                f = 1.f;
+                --q;
+                continue;
+              }
+              if (isnan(top)) poison |= 0x100u;
+              const bool grow = __fsub_rn(top, ref) > kHead + kGrow;
+              const float next = !grow ? ref : fabsf(top) < kWhole ? ceilf(top) - kHead : top;
+              const float down = fmaxf(ref - next, -127.f);              // a whole number
+              const float shrink = __int_as_float((static_cast<int>(down) + 127) << 23);   // 0 for 2^-127 and less
+              ref = next;
+              l2[0] = fmul2_rn(l2[0], pair(shrink, shrink));
+              l2[1] = fmul2_rn(l2[1], pair(shrink, shrink));
+              uint32_t y[16];
+              tmem_wait_st();   // weights and O of this step that are stored already are read back below
+              if (j > run) {
 #pragma unroll 1
-            for (int k = 0; k < q * (kPiece / 32); ++k) {     // weights of this step that are written already
-              tmem_ld16(ts + k * 16, y);
-              tmem_wait_ld();
+                for (int k = 0; k < 8; ++k) {
+                  tmem_ld16(to + k * 16, y);
+                  tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) y[i] = hmul2(y[i], s2);
-              tmem_st16(ts + k * 16, y);
+                  for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * shrink);
+                  tmem_st16(to + k * 16, y);
+                }
+              }
+              const uint32_t s2 = pack_f16x2(shrink, shrink);
+#pragma unroll 1
+              for (int k = 0; k < q * (kPiece / 32); ++k) {     // weights of this step that are written already
+                tmem_ld16(ts + k * 16, y);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) y[i] = hmul2(y[i], s2);
+                tmem_st16(ts + k * 16, y);
+              }
             }
-          }
-          const unsigned long long ref2 = pair(-ref, -ref);
-          const unsigned long long f2 = pair(f, f);
+            const unsigned long long ref2 = pair(-ref, -ref);
+            const unsigned long long f2 = pair(f, f);
 #pragma unroll
-          for (int i = 0; i < kPiece / 2; ++i) {
-            const float2 y = unpair(ffma2_rn(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2, ref2));
-            const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            l2[i & 1] = fadd2_rn(l2[i & 1], pair(e.x, e.y));
-            x[i] = pack_f16x2(e.x, e.y);
-          }
+            for (int i = 0; i < kPiece / 2; ++i) {
+              const float2 y = unpair(ffma2_rn(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), f2, ref2));
+              const float2 e = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+              l2[i & 1] = fadd2_rn(l2[i & 1], pair(e.x, e.y));
+              x[i] = pack_f16x2(e.x, e.y);
+            }
 #pragma unroll
-          for (int k = 0; k < kPiece / 32; ++k) tmem_st16(ts + (q * kPiece / 32 + k) * 16, x + 16 * k);
+            for (int k = 0; k < kPiece / 32; ++k) tmem_st16(ts + (q * kPiece / 32 + k) * 16, x + 16 * k);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          half_barrier(half);   // this half's weights are there, for its MMA warp
         }
-        tmem_wait_st();
-        tc_fence_before();
-        half_barrier(half);   // this half's weights are there, for its MMA warp
       }
       it += steps;
       more = walk.next(p, segments_s[warp + (segments & 1 ? 0 : kThreads / 32)]);   // while the last products run
-      ok = ok && wait_long_warp(o_full + half, segments & 1, p.c.err);
+      ok = ok && wait_long_warp(o_full + half, runs++ & 1, p.c.err);
       tc_fence_after();
+      if (ok && steps > first + kRun * by) fold(to, sums(), ref, kFoldBack);
       // ---- the result, or a partial ----
       const float2 l01 = unpair(fadd2_rn(l2[0], l2[1]));
       float l = l01.x + l01.y;
@@ -954,6 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         if (ok && first < steps) qk(it + first);
       }
       __syncwarp();
+      int nth = 0;                  // of the run
 #pragma unroll 1
       for (int j = first; j < steps; j += by) {
         // ahead of the weights: the values and the next keys. With split steps these keys are two steps on, and are
@@ -966,7 +1019,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
         half_barrier(half);
         if (lane == 0 && ok) {
           tc_fence_after();
-          pv(it + j, j == first);
+          pv(it + j, nth == 0);
+          nth = (nth + 1) % kRun;
+          if (nth == 0 && j + by < steps) tc_commit(o_full + half);
           if (j + by < steps) {
             if (split) ok = wait_long(k_full + ((it + j + by) & 1), ((it + j + by) >> 1) & 1, p.c.err);
             tc_fence_after();

@@ -963,3 +963,63 @@ def test_sums_of_16_bit_calls_over_long_segments(cuda_device, n):
     dims round apart from one another by at most 2^-11 of a value, evenly spread (of all rows alike, as rows see nearly
     the same mean): four standard deviations of their mean."""
     assert abs(long_bias(n, "f16", cuda_device)) <= 512 * 2.0 ** -23 + 4 * 2.0 ** -11 / math.sqrt(3 * 256)
+
+
+@pytest.mark.parametrize("n", [30, 64])
+def test_sums_of_long_chunks_over_long_segments(cuda_device, n):
+    """Units of 120 and of 256 rows, a million tokens a block. As above, with 128 steps of 8 matrix instructions a sum."""
+    assert abs(long_bias(n, "f16", cuda_device)) <= 1024 * 2.0 ** -23 + 4 * 2.0 ** -11 / math.sqrt(3 * 256)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16"])
+@pytest.mark.parametrize("n", [20, 64, 90])
+def test_chunks_whose_sums_are_put_by(cuda_device, kind, n):
+    """Units of up to 400 steps, on one half or two (a half's sums are put by after 128), beside short ones, some whole and
+    some shared by two blocks of about 490 steps (128 heads; 980 with units of two row tiles), maxima that grow on the way;
+    against 64 bits."""
+    lens = [51200, 700, 20011]
+    Hkv, G, B = 128, 4, len(lens)
+    pages = [-(-t // 128) for t in lens]
+    cache = P.KV4Cache.empty(sum(pages), Hkv, 128, cuda_device)
+    table = torch.full((B, max(pages)), -1, dtype=torch.int32)
+    at = 0
+    for b in range(B):
+        table[b, :pages[b]] = torch.arange(at, at + pages[b])
+        at += pages[b]
+    kv = P.KV4Cache(cache, table.to(cuda_device), i32(lens).to(cuda_device), i32(lens), Hkv * G)
+    gen = torch.Generator(device=cuda_device).manual_seed(n)
+    total = sum(lens)
+    k = torch.randn(total, Hkv, D, generator=gen, device=cuda_device, dtype=torch.bfloat16)
+    pos = torch.cat([torch.arange(t) for t in lens]).to(cuda_device)
+    k[:, :, 3] = (pos // 6000)[:, None].to(k.dtype)          # grows by a stair every 6000 tokens
+    v = torch.randn(total, Hkv, D, generator=gen, device=cuda_device, dtype=torch.bfloat16)
+    cu, st = cu_of(lens), i32([0] * B)
+    P.hsa_kv4_write(kv, k, v, cu.to(cuda_device), cu)
+    k, v = P.hsa_kv4_read(kv, st.to(cuda_device), st, cu.to(cuda_device), cu)
+    news = [n, n, n]
+    q = torch.randn(3 * n, Hkv * G, D, generator=gen, device=cuda_device).to(TYPES[kind])
+    q[::2, :, 3] = 6.0
+    cn = cu_of(news)
+    ws = P.workspace(P.hsa_kv4_workspace_bytes(kv), cuda_device)
+    lse = torch.empty(3 * n, Hkv * G, device=cuda_device)
+    scale = 0.1
+    out = P.dense_prefill_kv4(kv, q, cn.to(cuda_device), cn, scale=scale, lse=lse, workspace_buf=ws).view(3 * n, Hkv, G, D)
+    again = P.dense_prefill_kv4(kv, q, cn.to(cuda_device), cn, scale=scale, workspace_buf=ws).view(3 * n, Hkv, G, D)
+    assert torch.equal(out, again)
+    half = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind]
+    for b in range(B):
+        for h in range(b, Hkv, 13):
+            kk, vv = (x[cu[b]:cu[b + 1], h].double() for x in (k, v))
+            rows_of = q.view(3 * n, Hkv, G, D)[b * n:(b + 1) * n, h].reshape(-1, D).double()
+            x = scale * (rows_of @ kk.T)
+            t = torch.arange(lens[b], device=cuda_device)
+            x.masked_fill_(t[None] > (lens[b] - n + torch.arange(n, device=cuda_device)).repeat_interleave(G)[:, None], -math.inf)
+            ref = torch.softmax(x, -1) @ vv
+            got = out[b * n:(b + 1) * n, h].reshape(-1, D).double()
+            # check()'s bound: logits, weights, sums (cut off 1024 times at most, less than 2^-23 each), the result
+            logit = scale * (rows_of.abs() @ kk.abs().T).max(1).values
+            rel = 2 * (logit * 18 * 2.0 ** -23 + 2.0 ** -21 + 1024 * 2.0 ** -23) + 2.0 ** -11
+            tol = rel * vv.abs().max() + ref.abs().max(1).values * half
+            assert ((got - ref).abs().max(1).values <= tol).all(), (b, h)
+            off = (lse.view(3 * n, Hkv, G)[b * n:(b + 1) * n, h].reshape(-1).double() - torch.logsumexp(x, -1)).abs()
+            assert (off <= rel + 2.0 ** -22 * torch.logsumexp(x, -1).abs()).all(), (b, h)
