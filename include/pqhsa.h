@@ -363,8 +363,9 @@ hsa_status hsa_train_index(const hsa_kv_cache* kv, hsa_index* index, int32_t n_t
  * tiles in the cache, 2^25 query rows a KV head, and of attention's work 2^30 steps of 32 tokens
  * over all sequences, KV heads and tiles of 4 to 32 query rows (fp32 calls, and up to 64 query
  * rows a KV head) or 2^31 steps of 128 tokens and 256 query rows. A replayed call whose device
- * lengths pass that leaves its outputs unwritten and flags HSA_DEVERR_LIMIT. Logits are held in fp32 (times log2(e), so
- * below 2.3e38); q and out do not overlap.
+ * lengths pass that leaves its outputs unwritten and flags HSA_DEVERR_LIMIT. Logits are held in
+ * fp32 (times log2(e), so below 2.3e38), a row of q to 2^-38 of its largest element; q and out
+ * do not overlap.
  */
 #define HSA_KV4_TILE_TOKENS 16
 #define HSA_KV4_TILE_BYTES 2304

@@ -17,9 +17,10 @@
 // Mathematics of a tile, on mma.sync m16n8k16 (fp16 in, fp32 sums): S^T = K q^T with the 16
 // tokens as rows and 8 query rows as columns, P = 2^(S f - ref), O^T += V^T P with dims as
 // rows. Keys and values are code x scale, exact in fp16, made in registers straight from the
-// tile's bytes: its layout is the fragments' own. q is scaled to at most 1 by a power of
-// two (f carries it back); 16-bit q is then one fp16 number, 32-bit q two (hi + lo, 22 bits),
-// and P likewise, so that 32-bit calls keep 32-bit accuracy. With at most four 32-bit rows hi
+// tile's bytes: its layout is the fragments' own. q is scaled by a power of two (q_exponent; f
+// carries it back); 16-bit q is then one fp16 number, 32-bit q two (hi + lo, 22 bits of elements
+// down to 2^-16 of the row's largest, the others to 2^-38 of it), and P likewise, so that 32-bit
+// calls keep 32-bit accuracy. With at most four 32-bit rows hi
 // and lo share one fragment (columns 0-3 and 4-7).
 //
 // ref is the row's largest logit so far less kHead; it moves when a logit exceeds it by
@@ -243,9 +244,6 @@ __device__ __forceinline__ int unit_step(const Kv4AttendParams& p, int RT, int u
   return at.b < p.c.B ? at.steps + (unit - at.units) * sequence(p, at.b, RT).nt : at.steps;
 }
 
-// 2^e for e in [-126, 127].
-__device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
-
 template <typename T>
 __device__ __forceinline__ void store_out(uint8_t* out, size_t at, float4 v);
 template <>
@@ -399,7 +397,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
       for (int i = 0; i < S::stages - 1; ++i) issue(i);
 
       // ---- query fragments and the bounds of each of this lane's columns ----
-      // Row by row, four values a lane: q over a power of two that takes its largest element to [0.5, 1).
+      // Row by row, four values a lane.
       int e_mine[NR];               // lane r: exponent of rows r, 8 + r, ... (of four and four: row r & 3)
 #pragma unroll
       for (int nt = 0; nt < NR; ++nt) {
@@ -428,9 +426,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
           for (int k = 0; k < 4; ++k) {
             const float top =
                 warp_max_f32(fmaxf(fmaxf(fabsf(x[k].x), fabsf(x[k].y)), fmaxf(fabsf(x[k].z), fabsf(x[k].w))));
-            // 2^e > top >= 2^(e - 1) for normal numbers; out of range or not finite: as it is
-            int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
-            e = e > 126 ? 0 : max(e, -126);
+            const int e = q_exponent(top);
             const float down = pow2i(-e);
             const int at = (M == kHiLo ? 2 * nt : nt) * 8 + c0 + k;
             const uint32_t h0 = pack_f16x2(x[k].x * down, x[k].y * down), h1 = pack_f16x2(x[k].z * down, x[k].w * down);
@@ -461,7 +457,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int own = M == kPack ? ((2 * t + j) & 3) : 2 * t + j;
-          // never so small that a masked logit, -inf times f, is NaN; logits under 2^-80 are as good as 0
+          // never so small that a masked logit, -inf times f, is NaN; logits under 2^-81 are as good as 0
           const float fc = p.scale * kLog2e * pow2i(__shfl_sync(0xffffffffu, e_mine[nt], own));
           f[2 * nt + j] = fabsf(fc) < 1e-36f ? copysignf(1e-36f, fc) : fc;
         }

@@ -536,16 +536,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
                             fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          int e = static_cast<int>(__float_as_uint(top) >> 23) - 126;
-          e = e > 126 ? 0 : max(e, -126);
-          const float down = copysignf(__int_as_float((127 - e) << 23), p.scale);
+          const int e = q_exponent(top);
+          const float down = copysignf(pow2i(-e), p.scale);
           const int r = row & 127;
           store16(smem_addr(sm) + Smem::q + (row >> 7) * kOperand + ((lane >> 3) & 1) * kHalfOp + r * 128 +
                       (((lane & 7) ^ (r & 7)) << 4),
                   pack_f16x2(a.x * down, a.y * down), pack_f16x2(a.z * down, a.w * down),
                   pack_f16x2(b.x * down, b.y * down), pack_f16x2(b.z * down, b.w * down));
           // never so small that a masked logit, -inf times f, is NaN
-          if ((lane & 15) == 0) factor[row] = fmaxf(fabsf(p.scale * kLog2e * __int_as_float((e + 127) << 23)), 1e-36f);
+          if ((lane & 15) == 0) factor[row] = fmaxf(fabsf(p.scale * kLog2e * pow2i(e)), 1e-36f);
         }
       }
       fence_proxy_async_smem();

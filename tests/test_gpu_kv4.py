@@ -1023,3 +1023,47 @@ def test_chunks_whose_sums_are_put_by(cuda_device, kind, n):
             assert ((got - ref).abs().max(1).values <= tol).all(), (b, h)
             off = (lse.view(3 * n, Hkv, G)[b * n:(b + 1) * n, h].reshape(-1).double() - torch.logsumexp(x, -1)).abs()
             assert (off <= rel + 2.0 ** -22 * torch.logsumexp(x, -1).abs()).all(), (b, h)
+
+
+@pytest.mark.parametrize("kind,factor", [("f32", 1e4), ("f32", 1e5), ("bf16", 1e4), ("bf16", 1e6), ("f16", 1e5)])
+@pytest.mark.parametrize("n", [1, 5, 12, 40, 200])
+def test_large_elements_of_q_leave_the_others_their_bits(cuda_device, n, kind, factor):
+    """One element of q is `factor` times the others, where the keys are zero: the logits are the others' alone. check()
+    holds them to 2^-22 of scale sum |q||k|, to which that element adds nothing. (fp32: q is held to 2^-38 of its largest
+    element, 2^-21 of a unit with 10^5, a third of that on the mean; its 128 errors are independent.)"""
+    T = 300
+    case = Case([T], 1, 4, 16, seed=63)
+    kv = case.device()
+    gen = torch.Generator().manual_seed(64)
+    k = torch.randn(T, 1, D, generator=gen)
+    k[:, 0, 21] = 0
+    cu = cu_of([T])
+    P.hsa_kv4_write(kv, k.to(cuda_device), torch.randn(T, 1, D, generator=gen).to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    q = rows(case.rng, (n, 4, D), "f32")
+    small = 1.0 if kind != "f16" else 0.25        # 25000: finite in fp16
+    q[..., 21] = factor
+    q = (q * small).to(TYPES[kind])
+    assert torch.isfinite(q).all()
+    scale = 0.1 / small
+    out, lse = prefill(case, q, [n], scale)
+    check(out, lse, q, case, [n], scale, kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [1, 5, 12, 40, 200])
+def test_queries_up_to_the_largest_number(cuda_device, n, kind):
+    """Rows of q whose largest element is 2^125 to just below 2^128, and rows of the smallest numbers, with a scale that
+    makes ordinary logits of the large ones."""
+    case = Case([200], 1, 4, 16, seed=65)
+    case.device()
+    q = rows(case.rng, (n, 4, D), kind)
+    q = q / q.abs().amax(-1, keepdim=True)
+    top = torch.tensor([2.0 ** 125, 2.0 ** 126, 2.0 ** 127, 3.3895e38])
+    q = (q.float() * top[None, :, None]).to(TYPES[kind])
+    if n > 2:
+        q[2] = 2.0 ** -126 * torch.sign(q[2].float())
+    assert torch.isfinite(q).all()
+    scale = 2.0 ** -126
+    out, lse = prefill(case, q, [n], scale)
+    check(out, lse, q, case, [n], scale, kind)
