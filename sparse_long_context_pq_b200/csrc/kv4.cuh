@@ -62,6 +62,8 @@ __device__ __forceinline__ int q_exponent(float top) {
   const int e = static_cast<int>(__float_as_uint(top) >> 23) - 140;
   return e > 114 ? 0 : max(e, -126);
 }
+// Where a row's ref begins: below every logit, and finite, so that a masked one, -inf, less it is -inf.
+constexpr float kLowest = -3.4028235e38f;
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 

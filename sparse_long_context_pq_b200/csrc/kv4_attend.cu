@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
       };
 #pragma unroll
       for (int j = 0; j < 2 * NR; ++j) {
-        ref[j] = -1e30f;
+        ref[j] = kLowest;
         l[j] = 0.f;
       }
 #pragma unroll
@@ -908,7 +908,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int parts = c1 - c0 + 1;
     auto slot_of = [&](int i) { return slots + static_cast<size_t>(2 * i + (i == 0 ? late : 0)) * RT * (kD + 2); };
     // a warp takes every kTeam-th part, four in flight
-    float m = -1e30f, l = 0.f;
+    float m = kLowest, l = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
     for (int i0 = member; i0 < parts; i0 += 4 * kTeam) {

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       const int pos = cur.T - cur.n + token_of(p, cur.row0 + (real ? row : 0));
       const int hi = !real ? -1 : p.causal ? pos : cur.T - 1;
       const int lo = p.window > 0 ? pos - p.window + 1 : 0;
-      float ref = -1e30f;
+      float ref = kLowest;
       bool scaled = false;          // S has been multiplied by f, which is 1 from then on
       unsigned long long l2[2] = {0, 0};
       unsigned poison = 0;          // bits 0-7: dim groups with a value that is not finite, bit 8: the whole row
@@ -702,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
       if (split) {
         asm volatile("bar.sync 1, 256;" ::: "memory");   // both halves are done with q
         if (half == 1 && ok) {
-          other[row] = make_float2(none ? -1e30f : ref, none ? 0.f : l);
+          other[row] = make_float2(none ? kLowest : ref, none ? 0.f : l);
           other_poison[row] = poison;
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
@@ -1085,7 +1085,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32)
   parts = min(parts + 1, blocks - c);   // with the one that ends it
 #pragma unroll 1
   for (int d8 = warp; d8 < kD / 8; d8 += kMergeWarps) {
-    float m = -1e30f, l = 0.f;
+    float m = kLowest, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll 2
     for (int i = 0; i < parts; ++i) {

@@ -1067,3 +1067,31 @@ def test_queries_up_to_the_largest_number(cuda_device, n, kind):
     scale = 2.0 ** -126
     out, lse = prefill(case, q, [n], scale)
     check(out, lse, q, case, [n], scale, kind)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 5, 12, 40, 200])
+def test_logits_far_below_zero(cuda_device, n, kind):
+    """All logits of a row between -3e30 and -1e38: the nearest to zero has all the weight."""
+    T = 260
+    case = Case([T], 1, 1, 16, seed=66)
+    kv = case.device()
+    gen = torch.Generator().manual_seed(67)
+    k = torch.zeros(T, 1, D)
+    k[:, 0, 40] = torch.tensor([1.5, 2.0, 3.0, 4.0, 6.0])[torch.randint(0, 5, (T,), generator=gen)]
+    k[:, 0, 41] = 6.0                    # the block's scale is 1, its codes are the values
+    k[T - n - 7, 0, 40] = 1.0            # every row sees this one
+    cu = cu_of([T])
+    v = torch.randn(T, 1, D, generator=gen)
+    P.hsa_kv4_write(kv, k.to(cuda_device), v.to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    q = torch.zeros(n, 1, D)
+    for top in (3e30, 1e37):
+        q[:, 0, 40] = -32768.0
+        scale = float(np.float32(top / 32768.0))
+        out, lse = prefill(case, q.to(TYPES[kind]), [n], scale)
+        want = case.held(0, 0)[1][T - n - 7]
+        got = out[:, 0].double().cpu().numpy()
+        half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind]
+        assert (np.abs(got - want) <= (half + 2.0 ** -20) * np.abs(want)).all()
+        assert (torch.abs(lse.double().cpu() / -top - 1) <= 2.0 ** -20).all()
