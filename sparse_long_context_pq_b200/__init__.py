@@ -692,7 +692,8 @@ def _kv4_rows(kv: KV4Cache, t: torch.Tensor, name: str, n: int) -> _KV4Rows:
     strides = t.stride()
     if t.shape != (n,) + kv._row_shape or strides[2] != 1:
         raise ValueError(f"{name}: expected [{n}, {kv.Hkv}, {HEAD_DIM}] with contiguous rows")
-    return _KV4Rows(t.data_ptr(), strides[0], strides[1])
+    # between the rows of a dim of one: anything
+    return _KV4Rows(t.data_ptr(), strides[0] if n > 1 else 0, strides[1] if kv._row_shape[0] > 1 else 0)
 
 
 def _kv4_ints(kv: KV4Cache, t: torch.Tensor, host: torch.Tensor, shape, name: str) -> None:
@@ -792,7 +793,7 @@ def dense_prefill_kv4(kv: KV4Cache, q: torch.Tensor, cu_q: torch.Tensor, cu_q_ho
     dense_prefill_kv4 in include/pqhsa.h): chunks of prompts, drafted tokens to verify. q: [rows, Hq, 128] of any
     token stride, rows [cu_q[b], cu_q[b + 1]) of sequence b; out: the same shape, contiguous."""
     n = _kv4_cu(kv, cu_q, cu_q_host, "cu_q")
-    if tuple(q.shape) != (n, kv.Hq, HEAD_DIM) or (n and (q.stride(2) != 1 or q.stride(1) != HEAD_DIM)):
+    if tuple(q.shape) != (n, kv.Hq, HEAD_DIM) or (n and (q.stride(2) != 1 or (kv.Hq > 1 and q.stride(1) != HEAD_DIM))):
         raise ValueError(f"q: expected [{n}, {kv.Hq}, {HEAD_DIM}] with contiguous heads")
     out = _kv4_out(kv, q, out, lse, stream)
     code = _kv4_type(q, out)

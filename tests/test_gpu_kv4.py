@@ -1095,3 +1095,25 @@ def test_logits_far_below_zero(cuda_device, n, kind):
         half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[kind]
         assert (np.abs(got - want) <= (half + 2.0 ** -20) * np.abs(want)).all()
         assert (torch.abs(lse.double().cpu() / -top - 1) <= 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("n", [1, 20])
+def test_strides_of_dims_of_one_are_not_looked_at(cuda_device, n):
+    """One KV head, or one row, whose stride says nothing (torch leaves any number there)."""
+    case = Case([60], 1, 1, 16, seed=83)
+    kv = case.device()
+    cu, st = cu_of([n]), i32([60 - n])
+    cud, std = cu.to(cuda_device), st.to(cuda_device)
+    k, v, q = (torch.randn(n, 1, D, device=cuda_device).half() for _ in range(3))
+    odd = lambda x: x.as_strided((n, 1, D), (D if n > 1 else 3, 5, 1))  # noqa: E731
+    P.hsa_kv4_write(kv, k, v, cud, cu)
+    want = kv.cache.clone()
+    kv.cache[:] = torch.from_numpy(case.bytes).to(cuda_device)
+    P.hsa_kv4_write(kv, odd(k), odd(v), cud, cu)
+    assert torch.equal(kv.cache, want)
+    ko, vo = P.hsa_kv4_read(kv, std, st, cud, cu, dtype=torch.float16)
+    k2, v2 = odd(torch.empty_like(ko)), odd(torch.empty_like(vo))
+    P.hsa_kv4_read(kv, std, st, cud, cu, k_out=k2, v_out=v2)
+    assert torch.equal(k2, ko) and torch.equal(v2, vo)
+    out = P.dense_prefill_kv4(kv, odd(q), cud, cu, scale=0.1)
+    assert torch.equal(out, P.dense_prefill_kv4(kv, q, cud, cu, scale=0.1))
