@@ -405,7 +405,7 @@ hsa_status hsa_kv4_write(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const h
 /*
  * Reads positions [start[b], start[b] + n_b) of every sequence back into rows
  * [cu[b], cu[b + 1]) of k and v (of dtype; written, other rows stay as they are), n_b =
- * cu[b + 1] - cu[b]. Every value is exact in all three types. start: device int32 [B] with
+ * cu[b + 1] - cu[b]. No two of these rows share an element (HSA_ERR_INVALID_ARG). Every value is exact in all three types. start: device int32 [B] with
  * its host copy. Rows whose page is out of range become zero and are flagged.
  */
 hsa_status hsa_kv4_read(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hsa_kv4_rows* v, int32_t dtype,

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 
 #include "../../include/pqhsa.h"
 #include "kv4.cuh"
@@ -56,6 +57,17 @@ hsa_status check_rows(const hsa_kv4_rows* r, int32_t dtype) {
   const long long e = elem_bytes(dtype);
   if (!aligned(r->data, 16) || r->token_stride * e % 16 || r->head_stride * e % 16) return HSA_ERR_ALIGNMENT;
   return HSA_OK;
+}
+
+// Whether no two of n x heads rows share an element.
+bool rows_apart(const hsa_kv4_rows* r, long long n, long long heads) {
+  long long near = std::llabs(r->token_stride), far = std::llabs(r->head_stride), count = n;   // the closer rows, and how many
+  if (n == 1 || (heads > 1 && far < near)) {
+    std::swap(near, far);
+    count = heads;
+  }
+  if (count == 1) return true;
+  return near >= kD && (n == 1 || heads == 1 || far >= near * (count - 1) + kD);
 }
 
 // cu[0] = 0, not falling; *most: the largest step.
@@ -216,6 +228,8 @@ hsa_status hsa_kv4_read(const hsa_kv4_cache* kv, const hsa_kv4_rows* k, const hs
   }
   if ((st = check_workspace(ws, ws_bytes)) != HSA_OK) return st;
   if (most == 0) return HSA_OK;
+  const int n = cu_host[kv->B];
+  if (k->data == v->data || !rows_apart(k, n, kv->Hkv) || !rows_apart(v, n, kv->Hkv)) return HSA_ERR_INVALID_ARG;
   Kv4RowsParams p = rows_params(kv, k, v, dtype, cu, cu_host[kv->B], ws);
   p.start = start;
   return launch_kv4_read(dtype, p, most / kTileTok + 2, stream, pdl_enabled()) == cudaSuccess ? HSA_OK : HSA_ERR_CUDA;

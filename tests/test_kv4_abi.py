@@ -124,6 +124,22 @@ def test_read_refuses(lib, start, steps, status):
     assert _read(lib, kv, np.array(start, dtype=np.int32), _cu(*steps)) == status
 
 
+@pytest.mark.parametrize("Hkv,steps,k,ok", [
+    (2, (1, 2), (256, 128), True), (2, (1, 2), (128, 384), True), (2, (1, 2), (1024, 512), True), (1, (1, 2), (128, 0), True),
+    (2, (1, 0), (0, 128), True), (1, (1, 0), (0, 0), True),
+    (2, (1, 2), (0, 128), False), (2, (1, 2), (256, 0), False), (2, (1, 2), (128, 128), False), (2, (1, 2), (128, 256), False),
+    (2, (1, 2), (192, 128), False), (1, (1, 2), (64, 0), False), (2, (1, 0), (0, 64), False), (2, (1, 2), (-256, 128), True),
+    (2, (1, 2), (-128, 128), False),
+])
+def test_read_refuses_outputs_that_share_elements(lib, Hkv, steps, k, ok):
+    kv, host = _kv(Hkv=Hkv)
+    start, cu, far = np.zeros(2, dtype=np.int32), _cu(*steps), _rows(2 * FAKE, 4096, 2048)
+    want = 6 if ok else 1                                              # 6: no device here
+    assert _read(lib, kv, start, cu, k=_rows(FAKE, *k), v=far) == want
+    assert _read(lib, kv, start, cu, k=far, v=_rows(FAKE, *k)) == want
+    assert _read(lib, kv, start, cu, k=far, v=far) == 1
+
+
 def test_read_refuses_null_start(lib):
     kv, host = _kv()
     assert _read(lib, kv, np.zeros(2, dtype=np.int32), _cu(1, 1), start_dev=None) == 1
