@@ -672,6 +672,7 @@ def _kv4_workspace(kv: KV4Cache, workspace_buf, stream) -> torch.Tensor:
         n = hsa_kv4_workspace_bytes(kv)
         return _kv4_new(kv, stream, lambda: workspace(n, kv.cache.device))
     _kv4_on(kv, workspace_buf)
+    _need(workspace_buf.is_contiguous(), "workspace_buf: expected a contiguous tensor")
     return workspace_buf
 
 

@@ -1117,3 +1117,12 @@ def test_strides_of_dims_of_one_are_not_looked_at(cuda_device, n):
     assert torch.equal(k2, ko) and torch.equal(v2, vo)
     out = P.dense_prefill_kv4(kv, odd(q), cud, cu, scale=0.1)
     assert torch.equal(out, P.dense_prefill_kv4(kv, q, cud, cu, scale=0.1))
+
+
+def test_workspaces_that_are_not_whole_are_refused(cuda_device):
+    """An expanded byte has the workspace's size and none of its memory."""
+    case = Case([40], 2, 2, 16)
+    kv = case.device()
+    ws = torch.zeros(1, dtype=torch.uint8, device=cuda_device).expand(P.hsa_kv4_workspace_bytes(kv))
+    with pytest.raises(ValueError):
+        P.dense_decode_kv4(kv, torch.zeros(1, 4, D, device=cuda_device), scale=0.1, workspace_buf=ws)
