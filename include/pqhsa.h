@@ -327,8 +327,9 @@ hsa_status hsa_train_index(const hsa_kv_cache* kv, hsa_index* index, int32_t n_t
 /*
  * A paged KV cache held in 4 bits: 144 bytes a token and KV head for keys and values
  * together, where the bf16 cache takes 512. The PQ-HSA article has no counterpart; these
- * calls stand beside dense_decode for caches that would not fit in 16 bits, and
- * hsa_kv4_read gives the raw keys that hsa_train_index and hsa_append_encode work on.
+ * calls stand beside dense_decode for caches that would not fit in 16 bits. hsa_decode,
+ * hsa_train_index and hsa_append_encode do not read this cache: they take bf16 pages, and
+ * what hsa_kv4_read gives back is rows by token, which the caller lays into such pages.
  *
  * Number format. A code is a 4-bit float: sign, two exponent bits, one mantissa bit
  * (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6). Blocks of 16 consecutive dims of one token and
@@ -337,7 +338,7 @@ hsa_status hsa_train_index(const hsa_kv_cache* kv, hsa_index* index, int32_t n_t
  * scale, at most six significant bits in [2^-18, 61440]: exact in fp16, bf16 and fp32.
  * Quantising a block x: scale = max|x| / 6 rounded to the nearest scale (at most 10240),
  * code = x / scale rounded to the nearest code (at most 6 in magnitude); ties to the even
- * mantissa. Blocks that hold a NaN or an infinity get the scale byte 255 and read back as
+ * mantissa; a zero may come back with either sign. Blocks that hold a NaN or an infinity get the scale byte 255 and read back as
  * NaN; larger finite values than 61440 saturate there.
  *
  * Memory. One head of a page is page_size / 16 tiles of 16 tokens, HSA_KV4_TILE_BYTES each:

@@ -17,8 +17,9 @@ namespace {
 constexpr int kMaxGroup = 128;      // query heads a KV head
 constexpr int kMaxBatch = 65535;    // grid rows
 // Query rows a KV head up to which the streaming kernel is used. Measured (us), streaming and 256-row kernel: 64 rows on
-// 8 heads of 131072 tokens 147 and 159, of 16384 44 and 57, on 16 x 8 heads of 5000 110 and 104; 72 rows on those 143 and
-// 105, on 8 heads of 131072 203 and 161: its units of 32 rows read the keys a third time from there on.
+// 8 heads of 131072 tokens 149 and 160, of 16384 46 and 57, on 64 x 8 heads of 2000 167 and 214, but on 16 x 8 of 5000 113
+// and 104; 72 rows on those 145 and 105, on 8 heads of 131072 206 and 161: past 64 rows a third unit of 32 reads the
+// cache's bytes a third time.
 constexpr int kFewRows = 64;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -22,7 +22,7 @@
 //
 // What bounds it: the tensor cores need 2048 clocks for a step (4 x 128 x 128 x 128 products),
 // ex2 as many (256 x 128 at 16 a clock), shared memory about 2000 (operands and dequantised tiles).
-// Measured, a step takes about 5400 (2048 tokens over 32768, 32 heads on 8: 1.40 ms, 762 TFLOP/s): a
+// Measured, a step takes about 5400 (2048 tokens over 32768, 32 heads on 8: 1.39 ms, 765 TFLOP/s): a
 // half's chain is S full, maximum, weights, P, P V, the next S, with its softmax (about 2400 for 128 rows
 // x 128 tokens) beside the other half's on the same schedulers, and TMEM has no room for a second S.
 // Between two segments there are about 12000 clocks of output and q (4 sequences of 2048: 0.34 ms).
@@ -192,9 +192,9 @@ __device__ __noinline__ void scale_tmem(uint32_t at, int n, float f) {
   tmem_wait_st();
 }
 // The tensor cores cut off what does not fit a sum, a bias that grows with its tokens (a million of them came out 6e-3
-// too small). So O holds kRun steps at most (16384 tokens, -5e-5): then each thread adds its row, with rounding, to its
+// too small). So O holds kRun steps at most (16384 tokens, -6e-5): then each thread adds its row, with rounding, to its
 // sums in a slot of the workspace, which holds their ref too, and in the end those to O (2048 tokens over 32768
-// 1367 -> 1398 us).
+// 1367 -> 1392 us).
 enum Fold { kFoldFirst, kFoldMore, kFoldBack };
 __device__ __noinline__ void fold(uint32_t o, float* slot, float ref, Fold how) {
   const float w = how == kFoldFirst ? 0.f : fast_exp2(slot[threadIdx.x] - ref);
