@@ -57,7 +57,8 @@ __device__ __forceinline__ size_t kv4_tile_offset(const Kv4View& c, int page, in
 }
 
 // A row of q passes through fp16 over a power of two, 2^q_exponent, which takes its largest element (magnitude `top`) to
-// [2^13, 2^14): fp16 has all its 11 bits down to 2^-27 of that element. Rows that are not finite stay as they are.
+// [2^13, 2^14): fp16 has all its 11 bits down to 2^-27 of that element. A row with an infinity has no weights, whatever
+// its keys, and becomes NaN.
 __device__ __forceinline__ int q_exponent(float top) {
   const int e = static_cast<int>(__float_as_uint(top) >> 23) - 140;
   return e > 114 ? 0 : max(e, -126);
@@ -66,6 +67,8 @@ __device__ __forceinline__ int q_exponent(float top) {
 constexpr float kLowest = -3.4028235e38f;
 // 2^e for e in [-126, 127].
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
+// What a row of q is multiplied by.
+__device__ __forceinline__ float q_factor(float top, int e) { return top < INFINITY ? pow2i(-e) : __int_as_float(0x7fffffff); }
 
 // The four bytes of w, each a pair of codes (low nibble first), as fp16 pairs.
 __device__ __forceinline__ void e2m1_to_f16x2(uint32_t w, uint32_t& r0, uint32_t& r1, uint32_t& r2, uint32_t& r3) {

@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(Shape<NR, M>::max_warps * 32, 1) kv4_attend_ke
             const float top =
                 warp_max_f32(fmaxf(fmaxf(fabsf(x[k].x), fabsf(x[k].y)), fmaxf(fabsf(x[k].z), fabsf(x[k].w))));
             const int e = q_exponent(top);
-            const float down = pow2i(-e);
+            const float down = q_factor(top, e);
             const int at = (M == kHiLo ? 2 * nt : nt) * 8 + c0 + k;
             const uint32_t h0 = pack_f16x2(x[k].x * down, x[k].y * down), h1 = pack_f16x2(x[k].z * down, x[k].w * down);
             *reinterpret_cast<uint2*>(qs + at * kQPitch + lane * 8) = make_uint2(h0, h1);

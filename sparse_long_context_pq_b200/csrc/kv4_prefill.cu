@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const __grid_c
 #pragma unroll
           for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
           const int e = q_exponent(top);
-          const float down = copysignf(pow2i(-e), p.scale);
+          const float down = copysignf(q_factor(top, e), p.scale);
           const int r = row & 127;
           store16(smem_addr(sm) + Smem::q + (row >> 7) * kOperand + ((lane >> 3) & 1) * kHalfOp + r * 128 +
                       (((lane & 7) ^ (r & 7)) << 4),

@@ -1126,3 +1126,27 @@ def test_workspaces_that_are_not_whole_are_refused(cuda_device):
     ws = torch.zeros(1, dtype=torch.uint8, device=cuda_device).expand(P.hsa_kv4_workspace_bytes(kv))
     with pytest.raises(ValueError):
         P.dense_decode_kv4(kv, torch.zeros(1, 4, D, device=cuda_device), scale=0.1, workspace_buf=ws)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 5, 12, 40, 200])
+def test_rows_of_q_that_are_not_finite(cuda_device, n, kind):
+    """An infinite or NaN element makes its row NaN, also where every logit comes out as -inf; other rows keep theirs."""
+    T = 230
+    case = Case([T], 1, 4, 16, seed=68)
+    kv = case.device()
+    gen = torch.Generator().manual_seed(69)
+    k = torch.randn(T, 1, D, generator=gen)
+    k[:, 0, 7] = -k[:, 0, 7].abs() - 1.0
+    cu = cu_of([T])
+    P.hsa_kv4_write(kv, k.to(cuda_device), torch.randn(T, 1, D, generator=gen).to(cuda_device), cu.to(cuda_device), cu)
+    case.bytes = kv.cache.cpu().numpy()
+    q = rows(case.rng, (n, 4, D), kind)
+    q[0, 1, 7], q[n // 2, 3, 7], q[n - 1, 0, 7] = math.inf, -math.inf, math.nan
+    out, lse = prefill(case, q, [n], 0.1)
+    bad = torch.isnan(out).cpu()
+    assert bad[0, 1].all() and bad[n // 2, 3].all() and bad[n - 1, 0].all() and bad.sum() == 3 * D
+    assert torch.isnan(lse).sum() == 3 and torch.isnan(lse[0, 1])
+    q[0, 1, 7], q[n // 2, 3, 7], q[n - 1, 0, 7] = 0.0, 0.0, 0.0
+    fine, _ = prefill(case, q, [n], 0.1)
+    assert torch.equal(out.cpu()[~bad], fine.cpu()[~bad])
